@@ -28,6 +28,7 @@ __all__ = [
     "kgw_wgrad_bf16", "kgw_wgrad_bf16_noalloc", "kgw_wgrad_bf16_ex", "kgw_wgrad_fp8", "kgw_wgrad_fp8_native", "kgw_wgrad_fp8_ex",
     "kgw_wgrad_fp4", "FP4_TOKEN_ALIGN",
     "kgw_quantize_fp8", "kgw_quantize_fp4", "kgw_mgrouped_bf16", "kgw_mgrouped_fp8", "kgw_workspace_bytes",
+    "kgw_moe_rows", "kgw_moe_sort", "kgw_moe_permute", "kgw_moe_unpermute", "kgw_moe_unpermute_grad",
     "KGW_LAYOUT_NT",
     "KGW_LAYOUT_NN",
     "KGW_A_M_MAJOR", "KGW_B_K_MAJOR", "KGW_RAGGED",
@@ -68,7 +69,9 @@ _lib = None
 EXPORTED_SYMBOLS = ("kgw_wgrad_bf16", "kgw_wgrad_bf16_noalloc", "kgw_wgrad_bf16_ex", "kgw_wgrad_fp8", "kgw_wgrad_fp8_native",
                     "kgw_wgrad_fp8_ex", "kgw_wgrad_fp4", "kgw_quantize_fp8", "kgw_quantize_fp4", "kgw_mgrouped_bf16",
                     "kgw_mgrouped_fp8", "kgw_workspace_bytes", "kgw_validate_offsets_host", "kgw_validate_offsets", "kgw_check_offsets",
-                    "kgw_mfma_ceiling", "kgw_status_string", "kgw_device_info")
+                    "kgw_mfma_ceiling", "kgw_status_string", "kgw_device_info", "kgw_moe_rows",
+                    "kgw_moe_sort_workspace_bytes", "kgw_moe_sort", "kgw_moe_permute", "kgw_moe_unpermute",
+                    "kgw_moe_unpermute_grad")
 
 
 def load_library():
@@ -113,6 +116,18 @@ def load_library():
     lib.kgw_check_offsets.argtypes = [p, i32, i64, i32, p, p]
     lib.kgw_mfma_ceiling.restype = ctypes.c_int
     lib.kgw_mfma_ceiling.argtypes = [p, i64, i32, i32, i32, p, p]
+    lib.kgw_moe_rows.restype = i64
+    lib.kgw_moe_rows.argtypes = [i64, i32, i32, i32]
+    lib.kgw_moe_sort_workspace_bytes.restype = sz
+    lib.kgw_moe_sort_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.kgw_moe_sort.restype = ctypes.c_int
+    lib.kgw_moe_sort.argtypes = [p, i32, i64, i32, i32, i32, i64, p, p, p, p, p, sz, p]
+    lib.kgw_moe_permute.restype = ctypes.c_int
+    lib.kgw_moe_permute.argtypes = [p, i64, i32, p, p, i64, i32, i64, i64, p, p]
+    lib.kgw_moe_unpermute.restype = ctypes.c_int
+    lib.kgw_moe_unpermute.argtypes = [p, i64, i32, p, p, i64, i32, i64, i64, p, p]
+    lib.kgw_moe_unpermute_grad.restype = ctypes.c_int
+    lib.kgw_moe_unpermute_grad.argtypes = [p, i64, p, i64, i32, p, p, p, i64, i32, i64, i64, p, p, p]
     lib.kgw_status_string.restype = ctypes.c_char_p
     lib.kgw_status_string.argtypes = [ctypes.c_int]
     lib.kgw_device_info.restype = ctypes.c_int
@@ -731,3 +746,172 @@ def wgrad(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, *, sfa: Optio
         return kgw_wgrad_fp8(a, sfa, b, sfb, offsets, out, out_dtype=out_dtype or torch.bfloat16,
                              accumulate=accumulate, validate=check)
     raise ValueError(f"unsupported operand dtypes {a.dtype}, {b.dtype}")
+
+
+# ----------------------------------------------------------------------------
+# tokens sorted by expert and back
+# ----------------------------------------------------------------------------
+def kgw_moe_rows(tokens: int, topk: int, num_experts: int, alignment: int = FP8_TOKEN_ALIGN) -> int:
+    """Rows that always hold `tokens` tokens of `topk` experts each, every expert's rows padded
+    to a multiple of `alignment`."""
+    rows = load_library().kgw_moe_rows(int(tokens), int(topk), int(num_experts), int(alignment))
+    if rows < 0:
+        raise ValueError(f"no row count for tokens={tokens}, topk={topk}, num_experts={num_experts}, "
+                         f"alignment={alignment}")
+    return rows
+
+
+def _on_gpu(t: torch.Tensor, what: str) -> torch.device:
+    """The tensor's device: the current GPU, whose memory the kernels address."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a GPU tensor, got one on {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _rows_2d(t: torch.Tensor, what: str) -> int:
+    """Row stride of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D, got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} needs contiguous rows (stride 1 along the last axis)")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{what} has overlapping rows")
+    return max(t.stride(0), cols) if rows > 1 else cols
+
+
+def _routing(t: torch.Tensor, what: str, dim: int, device):
+    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dim}-D int32 tensor")
+    if t.device != device:
+        raise ValueError(f"{what} must live on the rows' device")
+
+
+def _weights(t: torch.Tensor, row_of: torch.Tensor, what: str = "weights"):
+    if t.dtype != torch.float32 or t.shape != row_of.shape or not t.is_contiguous() or t.device != row_of.device:
+        raise ValueError(f"{what} must be a contiguous float32 tensor of row_of's shape, on its device")
+
+
+def _result(out: Optional[torch.Tensor], shape, dtype, device, what: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+    return out
+
+
+def kgw_moe_sort(ids: torch.Tensor, num_experts: int, *, alignment: int = FP8_TOKEN_ALIGN,
+                 rows: Optional[int] = None, stream=None):
+    """Sort the assignments ids (tokens, topk), int32 or int64, by expert.
+
+    Returns int32 tensors (counts, offsets, row_of, src_of): counts (num_experts,) and offsets
+    (num_experts,) as kgw_wgrad_* and kgw_mgrouped_* take them (every count rounded up to
+    `alignment`), row_of (tokens, topk) and src_of (rows,).  An id outside [0, num_experts)
+    gets row -1.  `rows` (default: kgw_moe_rows, which always suffices) bounds the sorted rows; the
+    assignments past it get row -1.
+    """
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous 2-D int32 or int64 tensor")
+    tokens, topk = ids.shape
+    E = int(num_experts)
+    if rows is None:
+        rows = kgw_moe_rows(tokens, topk, E, alignment)
+    rows = int(rows)
+    if E < 1 or topk < 1 or rows < 0:
+        raise ValueError("need at least one expert, one expert per token and a non-negative row count")
+    device = _on_gpu(ids, "ids")
+    lib = load_library()
+    need = lib.kgw_moe_sort_workspace_bytes(tokens, topk, E)
+    # one allocation for the small results and the scratch
+    small = torch.empty(2 * E, dtype=torch.int32, device=device)
+    row_of = torch.empty((tokens, topk), dtype=torch.int32, device=device)
+    src_of = torch.empty(rows, dtype=torch.int32, device=device)
+    ws = None
+    if need:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        for t in (small, row_of, src_of, ws):
+            if t is not None:
+                t.record_stream(stream)
+    counts, offsets = small[:E], small[E:]
+    st = lib.kgw_moe_sort(ids.data_ptr(), ids.element_size(), tokens, topk, E, int(alignment), rows,
+                          counts.data_ptr(), offsets.data_ptr(), row_of.data_ptr(), src_of.data_ptr(), _ptr(ws), need,
+                          _stream_ptr(stream))
+    _check(st, "kgw_moe_sort")
+    return counts, offsets, row_of, src_of
+
+
+def kgw_moe_permute(x: torch.Tensor, row_of: torch.Tensor, src_of: torch.Tensor,
+                    out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
+    """x (tokens, hidden) -> out (rows, hidden): out[row_of[t][j]] = x[t], every other row zero.
+
+    fp32, bf16 or fp16; x may have any row stride.  Gradient: kgw_moe_unpermute without weights.
+    """
+    code = _out_code(x.dtype)
+    ld = _rows_2d(x, "x")
+    device = _on_gpu(x, "x")
+    _routing(row_of, "row_of", 2, device)
+    _routing(src_of, "src_of", 1, device)
+    tokens, hidden = x.shape
+    if row_of.shape[0] != tokens:
+        raise ValueError(f"row_of has {row_of.shape[0]} tokens, x has {tokens}")
+    rows = src_of.shape[0]
+    out = _result(out, (rows, hidden), x.dtype, device, "out")
+    st = load_library().kgw_moe_permute(x.data_ptr(), ld, code, row_of.data_ptr(), src_of.data_ptr(), tokens,
+                                        row_of.shape[1], rows, hidden, out.data_ptr(), _stream_ptr(stream))
+    _check(st, "kgw_moe_permute")
+    return out
+
+
+def kgw_moe_unpermute(y: torch.Tensor, row_of: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
+    """y (rows, hidden) -> out (tokens, hidden): out[t] = sum_j weights[t][j] * y[row_of[t][j]].
+
+    weights float32 (tokens, topk), None for all ones (the gradient of kgw_moe_permute).  Summed in
+    fp32, rounded once to y's type; an assignment without a row adds nothing.
+    """
+    code = _out_code(y.dtype)
+    ld = _rows_2d(y, "y")
+    device = _on_gpu(y, "y")
+    _routing(row_of, "row_of", 2, device)
+    if weights is not None:
+        _weights(weights, row_of)
+    rows, hidden = y.shape
+    tokens, topk = row_of.shape
+    out = _result(out, (tokens, hidden), y.dtype, device, "out")
+    st = load_library().kgw_moe_unpermute(y.data_ptr(), ld, code, row_of.data_ptr(), _ptr(weights), tokens, topk,
+                                          rows, hidden, out.data_ptr(), _stream_ptr(stream))
+    _check(st, "kgw_moe_unpermute")
+    return out
+
+
+def kgw_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_of: torch.Tensor, src_of: torch.Tensor,
+                           weights: torch.Tensor, dy: Optional[torch.Tensor] = None,
+                           dweights: Optional[torch.Tensor] = None, *, stream=None):
+    """Gradients of kgw_moe_unpermute(y, row_of, weights) for dout (tokens, hidden): (dy, dweights).
+
+    dy (rows, hidden) in y's type, zero in every row without a source; dweights float32
+    (tokens, topk), zero for an assignment without a row.  (Without weights dy is
+    kgw_moe_permute(dout, row_of, src_of).)
+    """
+    code = _out_code(y.dtype)
+    ld_y, ld_d = _rows_2d(y, "y"), _rows_2d(dout, "dout")
+    device = _on_gpu(y, "y")
+    _routing(row_of, "row_of", 2, device)
+    _routing(src_of, "src_of", 1, device)
+    _weights(weights, row_of)
+    rows, hidden = y.shape
+    tokens, topk = row_of.shape
+    if dout.dtype != y.dtype or dout.device != device or tuple(dout.shape) != (tokens, hidden):
+        raise ValueError(f"dout must be a {(tokens, hidden)} {y.dtype} tensor on {device}")
+    if src_of.shape[0] != rows:
+        raise ValueError(f"src_of has {src_of.shape[0]} rows, y has {rows}")
+    dy = _result(dy, (rows, hidden), y.dtype, device, "dy")
+    dweights = _result(dweights, (tokens, topk), torch.float32, device, "dweights")
+    st = load_library().kgw_moe_unpermute_grad(dout.data_ptr(), ld_d, y.data_ptr(), ld_y, code, row_of.data_ptr(),
+                                               src_of.data_ptr(), weights.data_ptr(), tokens, topk, rows, hidden,
+                                               dy.data_ptr(), dweights.data_ptr(), _stream_ptr(stream))
+    _check(st, "kgw_moe_unpermute_grad")
+    return dy, dweights

@@ -22,12 +22,7 @@ static __device__ __align__(256) float scratch[kScratchBytes / sizeof(float)];
 
 namespace {
 
-struct DeviceProps {
-    int num_cus = 0;
-    int is_gfx950 = 0;
-    int num_xcds = 1;
-    bool ok = false;
-};
+using kgw::DeviceProps;
 
 constexpr int kMaxDevices = 64;
 std::once_flag g_once[kMaxDevices];
@@ -283,6 +278,10 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
 }
 
 }  // namespace
+
+namespace kgw {
+bool device_props(DeviceProps* out) { return current_props(out) == KGW_SUCCESS; }
+}  // namespace kgw
 
 extern "C" {
 

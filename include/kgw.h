@@ -538,6 +538,82 @@ const char* kgw_status_string(kgw_status_t status);
  */
 kgw_status_t kgw_device_info(int32_t* num_cus, int32_t* is_gfx950, int32_t* num_xcds);
 
+/* ------------------------------------------------------------------------
+ * Tokens sorted by expert and back: what makes the rows and offsets that the
+ * grouped products take, what brings their results back to the tokens, and the
+ * gradients of both.  `dtype` is the element type of the rows (KGW_OUT_FP32,
+ * KGW_OUT_BF16 or KGW_OUT_FP16); row strides (ld_*) count elements and are at
+ * least `hidden`; hidden is any size and rows may start at any element.
+ * tokens * topk < 2^31, rows < 2^31, hidden < 2^28.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kgw_moe_rows -- rows that always hold `tokens` tokens of `topk` experts each,
+ * every expert's rows padded to a multiple of `alignment`: an expert that gets
+ * tokens wastes at most alignment - 1 rows.  Host only; -1 for invalid arguments.
+ */
+int64_t kgw_moe_rows(int64_t tokens, int32_t topk, int32_t num_experts, int32_t alignment);
+
+/* Device scratch of kgw_moe_sort, 4-byte aligned, no initial contents (0: none). */
+size_t kgw_moe_sort_workspace_bytes(int64_t tokens, int32_t topk, int32_t num_experts);
+
+/*
+ * kgw_moe_sort -- a stable counting sort of the assignments (t, j) by expert.
+ *
+ *   ids      (tokens, topk) expert ids, id_bytes 4 (int32) or 8 (int64).  An id
+ *            outside [0, num_experts) is an expert of another rank: its
+ *            assignment gets no row.
+ *   counts   int32 (num_experts,): assignments of every expert.
+ *   offsets  int32 (num_experts,): inclusive cumulative counts, each count first
+ *            rounded up to a multiple of `alignment`; the offsets of kgw_wgrad_*
+ *            and kgw_mgrouped_*.
+ *   row_of   int32 (tokens, topk): row of every assignment, -1 for none.  Rows of
+ *            one expert are in the order of t * topk + j.
+ *   src_of   int32 (rows,): t * topk + j of every row, -1 for a padding row and for
+ *            the rows past the last offset.
+ *   rows     rows there is room for, a multiple of alignment; kgw_moe_rows() always
+ *            suffices.  With fewer, offsets stop at `rows` and the assignments past
+ *            it get no row (counts still has them).
+ * num_experts <= 2048; tokens * topk + num_experts * alignment < 2^31.
+ * Deterministic.  tokens == 0 is valid.
+ */
+kgw_status_t kgw_moe_sort(const void* ids, int32_t id_bytes, int64_t tokens, int32_t topk, int32_t num_experts,
+                          int32_t alignment, int64_t rows, int32_t* counts, int32_t* offsets, int32_t* row_of,
+                          int32_t* src_of, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kgw_moe_permute -- out (rows, hidden), contiguous: out[row_of[t][j]] = x[t], and +0.0
+ * in every row whose src_of is negative (padding rows and those past the last offset).
+ * row_of and src_of come from one kgw_moe_sort.  A row_of outside [0, rows) is skipped.
+ * Its gradient is kgw_moe_unpermute without weights; the gradient of that is kgw_moe_permute.
+ */
+kgw_status_t kgw_moe_permute(const void* x, int64_t ld_x, int32_t dtype, const int32_t* row_of,
+                             const int32_t* src_of, int64_t tokens, int32_t topk, int64_t rows, int64_t hidden,
+                             void* out, void* stream);
+
+/*
+ * kgw_moe_unpermute -- out (tokens, hidden), contiguous:
+ *     out[t] = sum over j of weights[t][j] * y[row_of[t][j]]
+ * in fp32 in the order of j, rounded once; an assignment without a row adds nothing (a
+ * token without any gets +0.0), whatever its weight.  weights fp32 (tokens, topk), contiguous;
+ * NULL: all ones.
+ */
+kgw_status_t kgw_moe_unpermute(const void* y, int64_t ld_y, int32_t dtype, const int32_t* row_of,
+                               const float* weights, int64_t tokens, int32_t topk, int64_t rows, int64_t hidden,
+                               void* out, void* stream);
+
+/*
+ * kgw_moe_unpermute_grad -- gradients of kgw_moe_unpermute with weights:
+ *     dy[row_of[t][j]] = weights[t][j] * dout[t]     dy (rows, hidden), contiguous; +0.0 in
+ *                                                    every row whose src_of is negative
+ *     dweights[t][j]   = <dout[t], y[row_of[t][j]]>  fp32 (tokens, topk); 0 without a row
+ * dot products in fp32, in a fixed order.
+ */
+kgw_status_t kgw_moe_unpermute_grad(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y, int32_t dtype,
+                                    const int32_t* row_of, const int32_t* src_of, const float* weights,
+                                    int64_t tokens, int32_t topk, int64_t rows, int64_t hidden, void* dy,
+                                    float* dweights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

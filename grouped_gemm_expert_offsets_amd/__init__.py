@@ -29,6 +29,7 @@ __all__ = [
     "kgw_wgrad_fp4", "FP4_TOKEN_ALIGN",
     "kgw_quantize_fp8", "kgw_quantize_fp4", "kgw_mgrouped_bf16", "kgw_mgrouped_fp8", "kgw_workspace_bytes",
     "kgw_moe_rows", "kgw_moe_sort", "kgw_moe_permute", "kgw_moe_unpermute", "kgw_moe_unpermute_grad",
+    "kgw_newton_schulz", "NEWTON_SCHULZ_COEFFICIENTS",
     "KGW_LAYOUT_NT",
     "KGW_LAYOUT_NN",
     "KGW_A_M_MAJOR", "KGW_B_K_MAJOR", "KGW_RAGGED",
@@ -71,7 +72,7 @@ EXPORTED_SYMBOLS = ("kgw_wgrad_bf16", "kgw_wgrad_bf16_noalloc", "kgw_wgrad_bf16_
                     "kgw_mgrouped_fp8", "kgw_workspace_bytes", "kgw_validate_offsets_host", "kgw_validate_offsets", "kgw_check_offsets",
                     "kgw_mfma_ceiling", "kgw_status_string", "kgw_device_info", "kgw_moe_rows",
                     "kgw_moe_sort_workspace_bytes", "kgw_moe_sort", "kgw_moe_permute", "kgw_moe_unpermute",
-                    "kgw_moe_unpermute_grad")
+                    "kgw_moe_unpermute_grad", "kgw_newton_schulz", "kgw_newton_schulz_workspace_bytes")
 
 
 def load_library():
@@ -128,6 +129,11 @@ def load_library():
     lib.kgw_moe_unpermute.argtypes = [p, i64, i32, p, p, i64, i32, i64, i64, p, p]
     lib.kgw_moe_unpermute_grad.restype = ctypes.c_int
     lib.kgw_moe_unpermute_grad.argtypes = [p, i64, p, i64, i32, p, p, p, i64, i32, i64, i64, p, p, p]
+    lib.kgw_newton_schulz.restype = ctypes.c_int
+    lib.kgw_newton_schulz.argtypes = [p, i64, i64, i32, i32, i64, i64, i32, ctypes.POINTER(ctypes.c_float),
+                                      ctypes.c_float, p, i32, p, sz, p]
+    lib.kgw_newton_schulz_workspace_bytes.restype = sz
+    lib.kgw_newton_schulz_workspace_bytes.argtypes = [i32, i64, i64, i32]
     lib.kgw_status_string.restype = ctypes.c_char_p
     lib.kgw_status_string.argtypes = [ctypes.c_int]
     lib.kgw_device_info.restype = ctypes.c_int
@@ -915,3 +921,62 @@ def kgw_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_of: torch.Te
                                                dy.data_ptr(), dweights.data_ptr(), _stream_ptr(stream))
     _check(st, "kgw_moe_unpermute_grad")
     return dy, dweights
+
+
+# ----------------------------------------------------------------------------
+# weight gradients made orthogonal
+# ----------------------------------------------------------------------------
+# a, b, c of X <- a X + (b A + c A A) X: steep at zero, so five steps bring singular values
+# from 0.01 of the norm on into [0.7, 1.2].
+NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def kgw_newton_schulz(G: torch.Tensor, *, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps: float = 1e-7,
+                      out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Orthogonalise G (m, n) or a batch (batch, m, n) by `steps` Newton-Schulz steps:
+    X = G / (|G|_F + eps), then X <- a X + (b A + c A A) X with A = X X^T.
+
+    G is fp32, bf16 or fp16 with contiguous rows (any row and batch stride), as kgw_wgrad_* writes
+    it.  `coefficients` is one (a, b, c) or one per step.  The result has `out_dtype` (default: G's): bf16
+    runs one fp16 product where fp32 and fp16 run three and keep fp32's precision.  `workspace`: a uint8
+    tensor of kgw_newton_schulz_workspace_bytes bytes to reuse; allocated here when None.
+    """
+    code = _out_code(G.dtype)
+    if G.dim() not in (2, 3):
+        raise ValueError(f"G must be (m, n) or (batch, m, n), got {tuple(G.shape)}")
+    batch = 1 if G.dim() == 2 else G.shape[0]
+    m, n = G.shape[-2:]
+    if n > 1 and G.stride(-1) != 1:
+        raise ValueError("G needs contiguous rows (stride 1 along the last axis)")
+    ld = G.stride(-2) if m > 1 else n
+    if ld < n:
+        raise ValueError("G has overlapping rows")
+    stride = G.stride(0) if G.dim() == 3 else 0
+    steps = int(steps)
+    if steps < 1 or steps > 64:
+        raise ValueError("steps must be 1 .. 64")
+    values = list(coefficients)
+    if len(values) == 3 and not hasattr(values[0], "__len__"):
+        values = values * steps
+    elif len(values) == steps and all(len(v) == 3 for v in values):
+        values = [float(x) for v in values for x in v]
+    else:
+        raise ValueError("coefficients must be (a, b, c), or one such triple per step")
+    device = _on_gpu(G, "G")
+    dtype = out.dtype if out is not None else (G.dtype if out_dtype is None else out_dtype)
+    out_code = _out_code(dtype)
+    out = _result(out, G.shape, dtype, device, "out")
+    lib = load_library()
+    need = lib.kgw_newton_schulz_workspace_bytes(batch, m, n, out_code)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be a contiguous uint8 tensor on G's device")
+    st = lib.kgw_newton_schulz(G.data_ptr(), ld, stride, code, batch, m, n, steps,
+                               (ctypes.c_float * (3 * steps))(*values), eps, out.data_ptr(), out_code,
+                               workspace.data_ptr(), workspace.numel(), _stream_ptr(stream))
+    _check(st, "kgw_newton_schulz")
+    return out

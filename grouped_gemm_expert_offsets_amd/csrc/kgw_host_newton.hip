@@ -1,0 +1,70 @@
+// C-ABI layer of the Newton-Schulz orthogonalisation: argument checks and dispatch.
+// Declarations and the contract of every entry point are in include/kgw.h.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/kgw.h"
+#include "kgw_internal.h"
+
+namespace {
+
+bool known_dtype(int32_t d) { return d == KGW_OUT_FP32 || d == KGW_OUT_BF16 || d == KGW_OUT_FP16; }
+
+kgw_status_t check_sizes(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
+    if (batch < 0 || m < 0 || n < 0 || !known_dtype(out_dtype)) return KGW_ERROR_INVALID_VALUE;
+    // a tile's rows are addressed with 32-bit byte offsets, a grid has 16-bit y and z extents
+    if (batch > 65535 || m > ((int64_t)1 << 20) || n > ((int64_t)1 << 20)) return KGW_ERROR_UNSUPPORTED;
+    const int64_t r = (m < n ? m : n) + 256, c = (m < n ? n : m) + 256;
+    if (r / 64 > 65535 || batch * (r / 128) * (c / 128) >= (int64_t)1 << 23) return KGW_ERROR_UNSUPPORTED;
+    return KGW_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kgw_newton_schulz_workspace_bytes(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
+    if (check_sizes(batch, m, n, out_dtype) != KGW_SUCCESS || batch == 0 || m == 0 || n == 0) return 0;
+    return kgw::newton_plan(batch, m, n, out_dtype).total;
+}
+
+kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_t dtype, int32_t batch, int64_t m,
+                               int64_t n, int32_t steps, const float* coefficients, float eps, void* out,
+                               int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!known_dtype(dtype) || steps < 1 || !coefficients || !(eps >= 0.0f)) return KGW_ERROR_INVALID_VALUE;
+    kgw_status_t st = check_sizes(batch, m, n, out_dtype);
+    if (st != KGW_SUCCESS) return st;
+    if (steps > kgw::kNewtonMaxSteps) return KGW_ERROR_UNSUPPORTED;
+    if (batch == 0 || m == 0 || n == 0) return KGW_SUCCESS;
+    if (!G || !out || !workspace || ld < n || (batch > 1 && stride < 0)) return KGW_ERROR_INVALID_VALUE;
+    if (((uintptr_t)G & (dtype == KGW_OUT_FP32 ? 3u : 1u)) || ((uintptr_t)out & (out_dtype == KGW_OUT_FP32 ? 3u : 1u)) ||
+        ((uintptr_t)workspace & 255u))
+        return KGW_ERROR_MISALIGNED;
+    const kgw::NewtonPlan plan = kgw::newton_plan(batch, m, n, out_dtype);
+    if (workspace_bytes < plan.total) return KGW_ERROR_INVALID_VALUE;
+    kgw::DeviceProps d;
+    if (!kgw::device_props(&d) || !d.is_gfx950) return KGW_ERROR_DEVICE;
+    kgw::NewtonParams p;
+    p.G = G;
+    p.out = out;
+    p.ld = ld;
+    p.stride = stride;
+    p.m = m;
+    p.n = n;
+    p.batch = batch;
+    p.dtype = dtype;
+    p.out_dtype = out_dtype;
+    p.steps = steps;
+    p.eps = eps;
+    char* ws = (char*)workspace;
+    p.x[0] = ws;
+    p.x[1] = ws + plan.x_bytes;
+    p.a = ws + 2 * plan.x_bytes;
+    p.b = p.a + plan.a_bytes;
+    p.parts = (double*)(p.b + plan.a_bytes);
+    return kgw::launch_newton(p, plan, coefficients, d.num_cus, d.num_xcds, (hipStream_t)stream) == hipSuccess
+               ? KGW_SUCCESS
+               : KGW_ERROR_DEVICE;
+}
+
+}  // extern "C"

@@ -199,4 +199,39 @@ void moe_sort_plan(int64_t assignments, int32_t* groups, int64_t* chunk);
 hipError_t launch_moe_sort(const MoeSortParams& p, bool wide_ids, hipStream_t stream);
 hipError_t launch_moe_rows(const MoeRowsParams& p, int op, int dtype, hipStream_t stream);
 
+// ----------------------------------------------------------------------------
+// Newton-Schulz orthogonalisation (kgw_newton.hip)
+// ----------------------------------------------------------------------------
+constexpr int kNewtonMaxSteps = 64;
+constexpr int kNewtonParts = 64;        // partial sums of squares per matrix
+
+struct NewtonParams {
+    const void* G;          // (batch, m, n), rows contiguous
+    void* out;              // (batch, m, n), contiguous
+    int64_t ld, stride;     // of G, in elements
+    int64_t m, n;
+    int32_t batch;
+    int32_t dtype, out_dtype;
+    int32_t steps;
+    float eps;
+    // workspace
+    double* parts;          // (batch, kNewtonParts)
+    char* x[2];             // iterates, see kgw_newton.hip
+    char* a;
+    char* b;
+};
+
+// Layout of the workspace: tile edge, padded sizes (rows r of the short side, columns c of the
+// long one) and bytes of each piece.
+struct NewtonPlan {
+    int32_t tile;
+    bool split;             // three products of 16-bit halves instead of one
+    bool tall;              // m > n: the iterates hold the transposes
+    int64_t r, c;           // padded
+    size_t x_bytes, a_bytes, parts_bytes, total;
+};
+NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype);
+hipError_t launch_newton(const NewtonParams& p, const NewtonPlan& plan, const float* coefficients, int num_cus,
+                         int num_xcds, hipStream_t stream);
+
 }  // namespace kgw

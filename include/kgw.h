@@ -614,6 +614,33 @@ kgw_status_t kgw_moe_unpermute_grad(const void* dout, int64_t ld_dout, const voi
                                     int64_t tokens, int32_t topk, int64_t rows, int64_t hidden, void* dy,
                                     float* dweights, void* stream);
 
+/*
+ * kgw_newton_schulz -- orthogonalises a batch of matrices, the update that a weight gradient
+ * gives an optimiser which moves along orthogonal matrices:
+ *
+ *     X = G / (|G|_F + eps);   `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X
+ *
+ * (for m > n on the transposes, which is the same).  coefficients, on the HOST, holds a, b, c of
+ * every step, 3 * steps floats.
+ *
+ *   G        (batch, m, n) of `dtype`, rows contiguous, `ld` >= n elements apart, matrices
+ *            `stride` elements apart (any ld and stride; the dense gradient has n and m * n).
+ *   out      (batch, m, n) of `out_dtype`, contiguous; may not overlap G.
+ *   workspace  kgw_newton_schulz_workspace_bytes() bytes, 256-byte aligned, no initial contents.
+ *
+ * Precision follows out_dtype.  KGW_OUT_BF16: operands of the products are rounded to fp16 and the
+ * linear term a X keeps 22 bits, which leaves errors below bf16's own rounding.  KGW_OUT_FP32 and
+ * KGW_OUT_FP16: every operand keeps 22 bits, with the errors of fp32 arithmetic, at three times the products.
+ * Sums are fp32, the norm's 64 bits.  The iterates' singular values must stay below 8
+ * (the usual coefficients keep them below 1.3).  A zero matrix gives zeros (eps > 0); infinities or NaN
+ * in a matrix give NaN in that matrix alone.  Deterministic.
+ * batch <= 65535; m, n <= 2^20; 1 <= steps <= 64; eps >= 0.
+ */
+kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_t dtype, int32_t batch, int64_t m,
+                               int64_t n, int32_t steps, const float* coefficients, float eps, void* out,
+                               int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+size_t kgw_newton_schulz_workspace_bytes(int32_t batch, int64_t m, int64_t n, int32_t out_dtype);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,7 +22,12 @@ static __device__ __align__(256) float scratch[kScratchBytes / sizeof(float)];
 
 namespace {
 
-using kgw::DeviceProps;
+struct DeviceProps {
+    int num_cus = 0;
+    int is_gfx950 = 0;
+    int num_xcds = 1;
+    bool ok = false;
+};
 
 constexpr int kMaxDevices = 64;
 std::once_flag g_once[kMaxDevices];
@@ -278,10 +283,6 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
 }
 
 }  // namespace
-
-namespace kgw {
-bool device_props(DeviceProps* out) { return current_props(out) == KGW_SUCCESS; }
-}  // namespace kgw
 
 extern "C" {
 

@@ -4,16 +4,15 @@
 #include <stdint.h>
 
 #include "../../include/kgw.h"
-#include "kgw_internal.h"
+#include "kgw_layer.h"
 
 namespace {
 
-using kgw::DeviceProps;
-
 bool aligned_to(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-kgw_status_t usable_device(DeviceProps* d) {
-    return kgw::device_props(d) && d->is_gfx950 ? KGW_SUCCESS : KGW_ERROR_DEVICE;
+kgw_status_t usable_device() {
+    int32_t is_gfx950 = 0;
+    return kgw_device_info(nullptr, &is_gfx950, nullptr) == KGW_SUCCESS && is_gfx950 ? KGW_SUCCESS : KGW_ERROR_DEVICE;
 }
 
 int element_size(int32_t dtype) { return dtype == KGW_OUT_FP32 ? 4 : 2; }
@@ -35,8 +34,7 @@ kgw_status_t check_rows(int32_t dtype, int64_t tokens, int32_t topk, int64_t row
 bool rows_aligned(const void* p, int32_t dtype) { return aligned_to(p, (uintptr_t)element_size(dtype)); }
 
 kgw_status_t run_rows(const kgw::MoeRowsParams& p, int op, int32_t dtype, void* stream) {
-    DeviceProps d;
-    const kgw_status_t st = usable_device(&d);
+    const kgw_status_t st = usable_device();
     if (st != KGW_SUCCESS) return st;
     return kgw::launch_moe_rows(p, op, dtype, (hipStream_t)stream) == hipSuccess ? KGW_SUCCESS : KGW_ERROR_DEVICE;
 }
@@ -77,8 +75,7 @@ kgw_status_t kgw_moe_sort(const void* ids, int32_t id_bytes, int64_t tokens, int
         return KGW_ERROR_MISALIGNED;
     const size_t need = kgw_moe_sort_workspace_bytes(tokens, topk, num_experts);
     if (need && (!workspace || workspace_bytes < need)) return KGW_ERROR_INVALID_VALUE;
-    DeviceProps d;
-    const kgw_status_t st = usable_device(&d);
+    const kgw_status_t st = usable_device();
     if (st != KGW_SUCCESS) return st;
     kgw::MoeSortParams p;
     p.ids = ids;

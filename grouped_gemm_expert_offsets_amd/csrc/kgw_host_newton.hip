@@ -4,7 +4,7 @@
 #include <stdint.h>
 
 #include "../../include/kgw.h"
-#include "kgw_internal.h"
+#include "kgw_layer.h"
 
 namespace {
 
@@ -42,8 +42,8 @@ kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_
         return KGW_ERROR_MISALIGNED;
     const kgw::NewtonPlan plan = kgw::newton_plan(batch, m, n, out_dtype);
     if (workspace_bytes < plan.total) return KGW_ERROR_INVALID_VALUE;
-    kgw::DeviceProps d;
-    if (!kgw::device_props(&d) || !d.is_gfx950) return KGW_ERROR_DEVICE;
+    int32_t num_cus = 0, is_gfx950 = 0, num_xcds = 1;
+    if (kgw_device_info(&num_cus, &is_gfx950, &num_xcds) != KGW_SUCCESS || !is_gfx950) return KGW_ERROR_DEVICE;
     kgw::NewtonParams p;
     p.G = G;
     p.out = out;
@@ -61,8 +61,11 @@ kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_
     p.x[1] = ws + plan.x_bytes;
     p.a = ws + 2 * plan.x_bytes;
     p.b = p.a + plan.a_bytes;
-    p.parts = (double*)(p.b + plan.a_bytes);
-    return kgw::launch_newton(p, plan, coefficients, d.num_cus, d.num_xcds, (hipStream_t)stream) == hipSuccess
+    // at least 8192 elements a workgroup of the norm
+    const int64_t parts = (m * n + 8191) / 8192;
+    p.num_parts = (int32_t)(parts < kgw::kNewtonParts ? parts : kgw::kNewtonParts);
+    p.parts = (double*)(p.b + plan.b_bytes);
+    return kgw::launch_newton(p, plan, coefficients, num_cus, num_xcds, (hipStream_t)stream) == hipSuccess
                ? KGW_SUCCESS
                : KGW_ERROR_DEVICE;
 }

@@ -144,94 +144,4 @@ hipError_t launch_wgrad_fp8_layout(const GroupedParams& p, bool a_m_major, bool 
 // m-grouped product with fp8 operands and 1x128 UE8M0 scales along K, forward (nt) or dgrad (nn).
 hipError_t launch_mgrouped_fp8(const MGroupedParams& p, bool nt, int out_kind, int grid, hipStream_t stream);
 
-
-// Properties of the current device (kgw_host.hip); false when there is none to use.
-struct DeviceProps {
-    int num_cus = 0;
-    int is_gfx950 = 0;
-    int num_xcds = 1;
-    bool ok = false;
-};
-bool device_props(DeviceProps* out);
-
-// ----------------------------------------------------------------------------
-// tokens sorted by expert and back (kgw_moe.hip)
-// ----------------------------------------------------------------------------
-constexpr int kMoeMaxExperts = 2048;    // per-wave counters of one workgroup stay in LDS
-constexpr int kMoeSortGroups = 128;     // workgroups of the sort (each reads the others' counts)
-
-struct MoeSortParams {
-    const void* ids;        // (assignments,) int32 or int64
-    int32_t* counts;        // (num_experts,)
-    int32_t* offsets;       // (num_experts,) inclusive, aligned, at most rows
-    int32_t* row_of;        // (assignments,)
-    int32_t* src_of;        // (rows,)
-    int32_t* hist;          // (groups, num_experts) workspace, groups > 1 only
-    int64_t assignments;
-    int64_t chunk;          // assignments of one workgroup
-    int64_t rows;
-    int32_t num_experts;
-    int32_t alignment;
-    int32_t groups;
-    int32_t id_bits;        // bits that tell the experts apart
-    int32_t src_aligned;    // src_of is 16-byte aligned
-};
-
-struct MoeRowsParams {
-    const void* in;         // permute: x; unpermute: y; gradient: dout
-    const void* y;          // gradient only
-    void* out;              // permute: rows; unpermute: tokens; gradient: dy (contiguous)
-    float* dweights;        // gradient only
-    const float* weights;   // (tokens, topk) or NULL
-    const int32_t* row_of;  // (tokens, topk)
-    const int32_t* src_of;  // (rows,)
-    int64_t ld_in, ld_y;    // row strides in elements
-    int64_t tokens, rows, hidden;
-    int64_t items;          // waves (permute, unpermute) or workgroups (gradient) of tokens
-    int64_t segments;       // waves of one row
-    int32_t topk;
-};
-
-constexpr int kMoePermute = 0, kMoeUnpermute = 1, kMoeUnpermuteGrad = 2;
-
-// Workgroups of the sort and the assignments of each.
-void moe_sort_plan(int64_t assignments, int32_t* groups, int64_t* chunk);
-hipError_t launch_moe_sort(const MoeSortParams& p, bool wide_ids, hipStream_t stream);
-hipError_t launch_moe_rows(const MoeRowsParams& p, int op, int dtype, hipStream_t stream);
-
-// ----------------------------------------------------------------------------
-// Newton-Schulz orthogonalisation (kgw_newton.hip)
-// ----------------------------------------------------------------------------
-constexpr int kNewtonMaxSteps = 64;
-constexpr int kNewtonParts = 64;        // partial sums of squares per matrix
-
-struct NewtonParams {
-    const void* G;          // (batch, m, n), rows contiguous
-    void* out;              // (batch, m, n), contiguous
-    int64_t ld, stride;     // of G, in elements
-    int64_t m, n;
-    int32_t batch;
-    int32_t dtype, out_dtype;
-    int32_t steps;
-    float eps;
-    // workspace
-    double* parts;          // (batch, kNewtonParts)
-    char* x[2];             // iterates, see kgw_newton.hip
-    char* a;
-    char* b;
-};
-
-// Layout of the workspace: tile edge, padded sizes (rows r of the short side, columns c of the
-// long one) and bytes of each piece.
-struct NewtonPlan {
-    int32_t tile;
-    bool split;             // three products of 16-bit halves instead of one
-    bool tall;              // m > n: the iterates hold the transposes
-    int64_t r, c;           // padded
-    size_t x_bytes, a_bytes, parts_bytes, total;
-};
-NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype);
-hipError_t launch_newton(const NewtonParams& p, const NewtonPlan& plan, const float* coefficients, int num_cus,
-                         int num_xcds, hipStream_t stream);
-
 }  // namespace kgw

@@ -18,7 +18,7 @@
 #include <type_traits>
 
 #include "kgw_device.h"
-#include "kgw_internal.h"
+#include "kgw_layer.h"
 
 namespace kgw {
 namespace {

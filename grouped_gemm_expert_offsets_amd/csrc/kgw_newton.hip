@@ -19,15 +19,11 @@
 //
 // A and A A are symmetric: only tiles on and below the diagonal are computed and their mirror
 // images written along.
-#include <type_traits>
-
-#include "kgw_device.h"
-#include "kgw_internal.h"
+#include "kgw_newton_device.h"
 
 namespace kgw {
 namespace {
 
-constexpr float kXScale = 8192.0f, kAScale = 1024.0f, kBScale = 128.0f;
 constexpr int NT = 256;
 
 // ----------------------------------------------------------------------------
@@ -42,94 +38,74 @@ __device__ __forceinline__ int64_t element(int64_t row, int64_t col, int64_t col
     else return row * cols + col;
 }
 
-__device__ __forceinline__ float half_bits(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
-__device__ __forceinline__ uint16_t to_half(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+// Eight consecutive elements of one row of a stored matrix, as one or two planes of halves.
+template <bool TWO>
+__device__ __forceinline__ void store_planes(const float (&v)[8], uint16_t* out, int64_t lo_off) {
+    i32x4 h, l;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        h[u] = (int)pack_f16x2(v[2 * u], v[2 * u + 1]);
+        if constexpr (TWO) l[u] = (int)pack_f16x2(v[2 * u] - f16_lo((uint32_t)h[u]), v[2 * u + 1] - f16_hi((uint32_t)h[u]));
+    }
+    *(gbl_i32x4*)out = h;
+    if constexpr (TWO) *(gbl_i32x4*)(out + lo_off) = l;
+}
 
 // ----------------------------------------------------------------------------
 // |G|_F and the first iterate
 // ----------------------------------------------------------------------------
-template <int DT>
-__device__ __forceinline__ float load_value(const void* p, int64_t i) {
-    if constexpr (DT == kOutF32) return ((const float*)p)[i];
-    else return half_lo<DT>((uint32_t)((const uint16_t*)p)[i]);
-}
-
-// Sum of squares of rows part, part + parts, ... of one matrix, in 64 bits: gradients may be so
-// large or small that their squares leave fp32's range.
+// Sum of squares of this workgroup's share of one matrix, in 64 bits: gradients may be so large or
+// small that their squares leave fp32's range.
 template <int DT>
 __global__ __launch_bounds__(NT) void newton_norm_kernel(NewtonParams p) {
     __shared__ double sums[NT / 64];
-    const int tid = threadIdx.x;
-    const int64_t base = (int64_t)blockIdx.y * p.stride;
+    const int tid = threadIdx.x, b = blockIdx.y;
+    const uint32_t per_row = (uint32_t)((p.n + 7) / 8);
+    const int64_t pieces = p.m * (int64_t)per_row;
     double s = 0.0;
-    for (int64_t row = blockIdx.x; row < p.m; row += kNewtonParts)
-        for (int64_t col = tid; col < p.n; col += NT) {
-            const double v = (double)load_value<DT>(p.G, base + row * p.ld + col);
-            s += v * v;
-        }
+#pragma unroll 2
+    for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < pieces; i += (int64_t)p.num_parts * NT) {
+        const int64_t row = i >> 32 ? i / per_row : (uint32_t)i / per_row;
+        float v[8];
+        load_eight<DT>(p, b, row, 8 * (i - row * per_row), v);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += (double)v[u] * (double)v[u];
+    }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
     if ((tid & 63) == 0) sums[tid >> 6] = s;
     __syncthreads();
-    if (tid == 0) p.parts[(int64_t)blockIdx.y * kNewtonParts + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-}
-
-// 2^13 / (|G|_F + eps) of matrix b, the same in every workgroup.
-__device__ __forceinline__ float first_scale(const NewtonParams& p, int b) {
-    double s = p.parts[(int64_t)b * kNewtonParts + (threadIdx.x & 63)];
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-    return (float)((double)kXScale / (__builtin_sqrt(s) + (double)p.eps));
+    if (tid == 0) p.parts[(int64_t)b * kNewtonParts + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
 // One 64 x 64 tile of the padded first iterate.
 template <int DT, bool SPLIT, bool TALL>
 __global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, int64_t R, int64_t C) {
-    __shared__ float tile[64][65];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.z;
+    __shared__ float tile[TALL ? 64 : 1][65];
+    const int b = blockIdx.z, i0 = threadIdx.x >> 3, q = threadIdx.x & 7;
     const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+    float v[2][8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load_eight<DT>(p, b, (TALL ? c0 : r0) + i0 + 32 * u, (TALL ? r0 : c0) + 8 * q, v[u]);
     const float scale = first_scale(p, b);
-    const int64_t base = (int64_t)b * p.stride;
-    for (int i = wave; i < 64; i += NT / 64) {
-        // TALL: row i of the tile read is row c0 + i of G
-        const int64_t gr = (TALL ? c0 : r0) + i, gc = (TALL ? r0 : c0) + lane;
-        const float v = gr < p.m && gc < p.n ? load_value<DT>(p.G, base + gr * p.ld + gc) * scale : 0.0f;
-        if constexpr (TALL) tile[lane][i] = v;
-        else tile[i][lane] = v;
+    if constexpr (TALL) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) tile[8 * q + e][i0 + 32 * u] = v[u][e];
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[u][e] = tile[i0 + 32 * u][8 * q + e];
     }
-    __syncthreads();
-    uint16_t* const hi = (uint16_t*)p.x[0] + (int64_t)b * R * C * (SPLIT ? 2 : 1);
-    uint16_t* const lo = SPLIT ? hi + 32 : (uint16_t*)p.x[0] + ((int64_t)p.batch + b) * R * C;
-    for (int i = wave; i < 64; i += NT / 64) {
-        const float v = tile[i][lane];
-        const uint16_t h = to_half(v);
-        const int64_t at = element<SPLIT>(r0 + i, c0 + lane, C);
-        hi[at] = h;
-        lo[at] = to_half(v - half_bits(h));
-    }
-}
-
-// One 64 x 64 tile of the result from the last iterate.
-template <int DT, bool SPLIT, bool TALL>
-__global__ __launch_bounds__(NT) void newton_last_kernel(NewtonParams p, const char* x, int64_t R, int64_t C) {
-    __shared__ float tile[64][65];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.z;
-    const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-    const uint16_t* const hi = (const uint16_t*)x + (int64_t)b * R * C * (SPLIT ? 2 : 1);
-    const uint16_t* const lo = SPLIT ? hi + 32 : (const uint16_t*)x + ((int64_t)p.batch + b) * R * C;
-    for (int i = wave; i < 64; i += NT / 64) {
-        const int64_t at = element<SPLIT>(r0 + i, c0 + lane, C);
-        const float v = (half_bits(hi[at]) + half_bits(lo[at])) * (1.0f / kXScale);
-        if constexpr (TALL) tile[lane][i] = v;
-        else tile[i][lane] = v;
-    }
-    __syncthreads();
-    for (int i = wave; i < 64; i += NT / 64) {
-        const int64_t gr = (TALL ? c0 : r0) + i, gc = (TALL ? r0 : c0) + lane;
-        if (gr >= p.m || gc >= p.n) continue;
-        const int64_t at = ((int64_t)b * p.m + gr) * p.n + gc;
-        if constexpr (DT == kOutF32) ((float*)p.out)[at] = tile[i][lane];
-        else ((uint16_t*)p.out)[at] = (uint16_t)pack_half2<DT>(tile[i][lane], 0.0f);
+    uint16_t* const x = (uint16_t*)p.x[0] + (int64_t)b * R * C * (SPLIT ? 2 : 1);
+    const int64_t lo_off = SPLIT ? 32 : (int64_t)p.batch * R * C;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] *= scale;
+        store_planes<true>(v[u], x + element<SPLIT>(r0 + i0 + 32 * u, c0 + 8 * q, C), lo_off);
     }
 }
 
@@ -141,9 +117,12 @@ enum NewtonProduct { kGram, kSquare, kUpdate };
 struct NewtonGemm {
     const char* left;       // (batch, R, K) rows of the product
     const char* right;      // gram, square: left again; update: the iterate (batch, K, C)
-    char* out;              // gram: A; square: B; update: the next iterate
-    const char* add;        // square: A; update: the iterate
-    float scale, add_scale; // out = scale * product + add_scale * add
+    char* out;              // gram: A; square: B; update: the next iterate, or NULL in the last step
+    void* result;           // last update: (batch, m, n) of result_dtype
+    int64_t m, n;
+    int32_t result_dtype, tall;
+    float scale;            // out = scale * (product + linear * (square: A; update: the iterate))
+    float linear;
     int64_t rows, cols, k;  // padded sizes of the product
     int32_t batch, tiles_m, tiles_n;
     int32_t items;          // workgroups with work
@@ -158,6 +137,17 @@ __device__ __forceinline__ int item_of(int bid, int items, int num_xcds) {
     return x * each + min(x, more) + bid / num_xcds;
 }
 
+// The update's tiles come in columns of this many rows of tiles; all of one group walk K alike, so that
+// they share the iterate's panels in L2 (each starting behind its own rows cost 4% of the update).
+constexpr int kRowGroup = 4;
+template <bool SPLIT, NewtonProduct KIND>
+__device__ __forceinline__ int turn_of(const NewtonGemm& p, int tm, int tile) {
+    if (!SPLIT || KIND != kUpdate) return 0;
+    const int rows = tile == 256 ? kRowGroup : 1;
+    const int end = min((tm / rows + 1) * rows, p.tiles_m);
+    return end == p.tiles_m ? 0 : end * tile / 32;
+}
+
 // Tile `index` of a product with tiles_m x tiles_n tiles a matrix: all of them (update), or those on
 // and below the diagonal.
 template <NewtonProduct KIND>
@@ -166,7 +156,7 @@ __device__ __forceinline__ void tile_of(const NewtonGemm& p, int index, int& b, 
     b = index / per;
     const int local = index - b * per;
     if constexpr (KIND == kUpdate) {
-        tile_coords(local, p.tiles_m, p.tiles_n, 4, tm, tn);
+        tile_coords(local, p.tiles_m, p.tiles_n, kRowGroup, tm, tn);
     } else {
         tm = (int)((__builtin_sqrtf(8.0f * (float)local + 1.0f) - 1.0f) * 0.5f);
         while ((tm + 1) * (tm + 2) / 2 <= local) ++tm;
@@ -182,44 +172,39 @@ __device__ __forceinline__ uint32_t image_at(int row, int chunk) {
     return (uint32_t)(row * W * 4 + ((chunk ^ (row & (W / 4 - 1))) << 4));
 }
 
-// Eight consecutive elements of one row of the result: v = product, then scaled, added to and stored
-// as one or two planes of halves.
-template <NewtonProduct KIND, bool TWO>
-struct Addend {
-    i32x4 hi, lo;
-    __device__ __forceinline__ void load(const uint16_t* add, int64_t at, int64_t lo_off) {
-        if constexpr (KIND != kGram) {
-            hi = *(const gbl_i32x4*)(add + at);
-            if constexpr (TWO) lo = *(const gbl_i32x4*)(add + at + lo_off);
-        }
-    }
-};
-template <NewtonProduct KIND, bool TWO>
-__device__ __forceinline__ void store_eight(const NewtonGemm& p, const float (&v)[8], const Addend<KIND, TWO>& old,
-                                            uint16_t* out, int64_t at, int64_t lo_off) {
-    i32x4 h, l;
+// Eight consecutive elements of row `row` of the result, those inside it.
+template <int DT>
+__device__ __forceinline__ void store_result(const NewtonGemm& p, const float (&v)[8], int b, int64_t row, int64_t col) {
+    if (row >= p.m || col >= p.n) return;
+    const int64_t at = ((int64_t)b * p.m + row) * p.n + col;
+    if constexpr (DT == kOutF32) {
+        float* const to = (float*)p.result + at;
+        if (col + 8 <= p.n) {
+            ((__attribute__((address_space(1))) Floats4*)to)[0].v = f32x4{v[0], v[1], v[2], v[3]};
+            ((__attribute__((address_space(1))) Floats4*)to)[1].v = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        float x[2] = {v[2 * u] * p.scale, v[2 * u + 1] * p.scale};
-        if constexpr (KIND != kGram) {
-            float y[2] = {f16_lo((uint32_t)old.hi[u]), f16_hi((uint32_t)old.hi[u])};
-            if constexpr (TWO) {
-                y[0] += f16_lo((uint32_t)old.lo[u]);
-                y[1] += f16_hi((uint32_t)old.lo[u]);
-            }
-            x[0] += p.add_scale * y[0];
-            x[1] += p.add_scale * y[1];
+            for (int u = 0; u < 8; ++u)
+                if (col + u < p.n) to[u] = v[u];
         }
-        h[u] = (int)pack_f16x2(x[0], x[1]);
-        if constexpr (TWO) l[u] = (int)pack_f16x2(x[0] - f16_lo((uint32_t)h[u]), x[1] - f16_hi((uint32_t)h[u]));
+    } else {
+        uint16_t* const to = (uint16_t*)p.result + at;
+        i32x4 w;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = (int)pack_half2<DT>(v[2 * u], v[2 * u + 1]);
+        if (col + 8 <= p.n) {
+            ((__attribute__((address_space(1))) Halves8*)to)->v = w;
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (col + u < p.n) to[u] = (uint16_t)(((uint32_t)w[u >> 1] >> (16 * (u & 1))) & 0xFFFFu);
+        }
     }
-    *(gbl_i32x4*)(out + at) = h;
-    if constexpr (TWO) *(gbl_i32x4*)(out + at + lo_off) = l;
 }
 
 // One TILE x TILE tile at rows m0 and columns n0 of matrix b.  A stage of the K loop is a 128-byte line
 // of every row of the left tile (64 halves of K, or 32 of both planes) and as many bytes of the right
-// one, in two slots.  Left tiles, and the right ones of the symmetric products, are read as
+// one, in a ring of SLOTS.  Left tiles, and the right ones of the symmetric products, are read as
 // K-contiguous rows with 16-byte chunk q of row i in slot q ^ ((i >> 1) & 7); the iterate's rows (K
 // across them) through the transposing reads, chunk q of row k in slot q ^ 4 (k & 3).  Both keep every
 // read free of bank conflicts.
@@ -227,9 +212,9 @@ __device__ __forceinline__ void store_eight(const NewtonGemm& p, const float (&v
 // A stage is four (six) groups of matrix products; each group's fragments are read while the group before
 // multiplies.  Before the last group every read of the stage is done, so the barrier that hands the
 // slot over stands there, and the next stage's first fragments and the loads of the one after
-// next go out under the last group's products.
-template <int TILE, int WAVES, bool SPLIT, NewtonProduct KIND>
-__device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int b, int64_t m0, int64_t n0) {
+// ring go out under the last group's products.
+template <int TILE, int WAVES, int SLOTS, bool SPLIT, NewtonProduct KIND>
+__device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int b, int64_t m0, int64_t n0, int turn) {
     constexpr int WM = 2, WN = WAVES / 2;               // waves along rows and columns
     constexpr int WTM = TILE / WM, WTN = TILE / WN;     // a wave's part
     constexpr int NBM = WTM / 32, NBN = WTN / 32;       // 32 x 32 blocks of it
@@ -268,13 +253,16 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     }
     const int stages = (int)(p.k / KSTAGE);
     const int64_t r_step = KIND == kUpdate ? KSTAGE * ldr : 128;
-    // load t of stage s; past the last stage an empty range (no memory is read)
-    auto load_one = [&](int s, int t) __attribute__((always_inline)) {
-        const uint32_t dst = lds0 + (uint32_t)((s & 1) * 2 * STAGE) + (uint32_t)(wave * LOADS) * 1024u;
-        const uint32_t range = s < stages ? 0xFFFFFFFFu : 0u;
-        const int u = t >> 1;
-        if (t & 1) dma_16B(rsrc_words(right + s * r_step, range), r_off[u], dst + (uint32_t)(STAGE + u * 1024));
-        else dma_16B(rsrc_words(left + (int64_t)s * 128, range), l_off[u], dst + (uint32_t)u * 1024u);
+    // Three products: the update walks K from stage `turn` on, so that its linear term comes late (fold()).
+    auto place_of = [&](int s) __attribute__((always_inline)) { return s + turn < stages ? s + turn : s + turn - stages; };
+    // Slot n % SLOTS takes the n-th operand stage, left and right in turn.  Load t of slot `slot` with
+    // operand stage n; past the last one an empty range (no memory is read).
+    auto load_one = [&](int n, int slot, int t) __attribute__((always_inline)) {
+        const uint32_t dst = lds0 + (uint32_t)(slot * STAGE + (wave * LOADS + t) * 1024);
+        const uint32_t range = (n >> 1) < stages ? 0xFFFFFFFFu : 0u;
+        const int at = place_of(n >> 1);
+        if (n & 1) dma_16B(rsrc_words(right + at * r_step, range), r_off[t], dst);
+        else dma_16B(rsrc_words(left + (int64_t)at * 128, range), l_off[t], dst);
     };
 
     // fragment q (0..3) of a stage: one product: K = 16 q ..; three: plane q >> 1, K = 16 (q & 1) ..
@@ -282,12 +270,11 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     const int sw = (l32 >> 1) & 7;
     const int kr = 8 * (g16 >> 1) + (i16 >> 2);
     const int cq = 2 * (g16 & 1) + ((i16 & 3) >> 1);
-    auto read_left = [&](int s, int q, int i) __attribute__((always_inline)) {
-        const lds_char* const base = lds + (s & 1) * 2 * STAGE;
-        return lds_load_16B(base, l_row + (uint32_t)i * 4096u + (uint32_t)(((2 * q + lhi) ^ sw) << 4));
+    auto read_left = [&](int slot, int q, int i) __attribute__((always_inline)) {
+        return lds_load_16B(lds + slot * STAGE, l_row + (uint32_t)i * 4096u + (uint32_t)(((2 * q + lhi) ^ sw) << 4));
     };
-    auto read_right = [&](int s, int q, int j) __attribute__((always_inline)) {
-        const lds_char* const base = lds + (s & 1) * 2 * STAGE + STAGE;
+    auto read_right = [&](int slot, int q, int j) __attribute__((always_inline)) {
+        const lds_char* const base = lds + slot * STAGE;
         if constexpr (KIND == kUpdate) {
             const int chunk = SPLIT ? (wn * NBN + j) * 8 + (q >> 1) * 4 + cq : wn * (WTN / 8) + 4 * j + cq;
             const uint32_t at = (uint32_t)((SPLIT ? 16 * (q & 1) : 16 * q) + kr) * (uint32_t)ROWB +
@@ -309,110 +296,176 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
 
+    // The linear term's matrix passes through LDS as an operand of the product: the stages over
+    // the tile's own rows (update: the iterate, right) or columns (square: A, left) hold the tile itself, and each lane
+    // adds its elements to its sums from there.  a X decides the small singular values, and every
+    // product summed after it rounds it once more: where the result is to be that exact, the tiles of a group of rows
+    // start behind the group's own rows and meet them last.
+    auto fold = [&](int s, int slot) __attribute__((always_inline)) {
+        const int d = KSTAGE * place_of(s) - (int)(KIND == kUpdate ? m0 : n0);
+        if (d < 0 || d >= TILE) return;
+        const lds_char* const base = lds + slot * STAGE;
+#pragma unroll
+        for (int e = 0; e < KSTAGE / 32; ++e) {
+            const int at = d + 32 * e;
+            if (at / (KIND == kUpdate ? WTM : WTN) != (KIND == kUpdate ? wm : wn)) continue;
+            const int block = at % (KIND == kUpdate ? WTM : WTN) / 32;
+            each<PRODUCTS>([&](auto k) __attribute__((always_inline)) {
+                constexpr int j = k / NBM, i = k % NBM;
+                if (block != (KIND == kUpdate ? i : j)) return;
+                // The empty asm statements differ from block to block: the compiler would otherwise merge
+                // the branches' code and reach the sums through pointers, in scratch memory.
+                asm volatile("; block %0" ::"n"(k.value));
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int plane = 0; plane < (SPLIT ? 2 : 1); ++plane) {
+                        uint32_t from;
+                        if constexpr (KIND == kUpdate) {
+                            const int krow = 32 * e + l32;
+                            const int chunk = SPLIT ? (wn * NBN + j) * 8 + plane * 4 + g : wn * (WTN / 8) + 4 * j + g;
+                            from = (uint32_t)(krow * ROWB + ((chunk ^ ((krow & 3) << 2)) << 4));
+                        } else {
+                            const int chunk = SPLIT ? plane * 4 + g : 4 * e + g;
+                            from = l_row + (uint32_t)i * 4096u + (uint32_t)((chunk ^ sw) << 4);
+                        }
+                        const i32x2 x = lds_load_8B(base, from + (uint32_t)lhi * 8u);
+                        acc[j][i][4 * g] += p.linear * f16_lo((uint32_t)x[0]);
+                        acc[j][i][4 * g + 1] += p.linear * f16_hi((uint32_t)x[0]);
+                        acc[j][i][4 * g + 2] += p.linear * f16_lo((uint32_t)x[1]);
+                        acc[j][i][4 * g + 3] += p.linear * f16_hi((uint32_t)x[1]);
+                    }
+                asm volatile("; block %0" ::"n"(k.value));
+            });
+        }
+    };
+
     struct Left { i32x4 v[NBM]; };
     struct Right { i32x4 v[NBN]; };
     // All products of one group; `other(k)` goes out after product k.
     auto group = [&](const Left& l, const Right& r, auto other) __attribute__((always_inline)) {
-#pragma unroll
-        for (int k = 0; k < PRODUCTS; ++k) {
-            const int j = k / NBM, i = k % NBM;
+        each<PRODUCTS>([&](auto k) __attribute__((always_inline)) {
+            constexpr int j = k / NBM, i = k % NBM;
             acc[j][i] = mfma_f16_32x32x16(r.v[j], l.v[i], acc[j][i]);
             __builtin_amdgcn_sched_barrier(0);
             other(k);
             __builtin_amdgcn_sched_barrier(0);
-        }
+        });
     };
-    // Share of `n` things that go out after product k, as evenly as they come.
-    auto share = [](int k, int n, auto one) __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < n; ++t)
-            if (t * PRODUCTS / n == k) one(t);
+    // Those of `n` things that go out after product k, as evenly as they come.
+    auto share = [](auto k, auto n, auto one) __attribute__((always_inline)) {
+        each<n>([&](auto t) __attribute__((always_inline)) {
+            if constexpr (t * PRODUCTS / n == k) one(t);
+        });
     };
-    auto read_both = [&](int s, int q, Left& l, Right& r, int t) __attribute__((always_inline)) {
-        if (t < NBM) l.v[t] = read_left(s, q, t);
-        else r.v[t - NBM] = read_right(s, q, t - NBM);
+    auto read_both = [&](int lslot, int rslot, int q, Left& l, Right& r, auto t) __attribute__((always_inline)) {
+        if constexpr (t < NBM) l.v[t] = read_left(lslot, q, t);
+        else r.v[t - NBM] = read_right(rslot, q, t - NBM);
     };
-    // The stage's reads are done: wait for the next one's loads and hand the slots over.
+    constexpr std::integral_constant<int, NBM + NBN> BOTH{};
+    constexpr std::integral_constant<int, NBM> LEFTS{};
+    constexpr std::integral_constant<int, NBN> RIGHTS{};
+    constexpr int GROUPS = SPLIT ? 6 : 4;
+    // The stage's reads are done: wait for the next one's loads (of the SLOTS - 4 operand stages after it some
+    // may still be on their way) and hand its slots over.
     auto hand_over = [&]() __attribute__((always_inline)) {
         wait_lgkmcnt0();
-        wait_vmcnt<0>();
+        wait_vmcnt<(SLOTS - 4) * LOADS>();
         barrier_no_fence();
         __builtin_amdgcn_sched_barrier(0);
     };
 
 #pragma unroll
-    for (int t = 0; t < 2 * LOADS; ++t) load_one(0, t);
+    for (int n = 0; n < SLOTS - 2; ++n)
 #pragma unroll
-    for (int t = 0; t < 2 * LOADS; ++t) load_one(1, t);
-    wait_vmcnt<2 * LOADS>();
+        for (int t = 0; t < LOADS; ++t) load_one(n, n, t);
+    wait_vmcnt<(SLOTS - 4) * LOADS>();
     barrier_no_fence();
     Left l0, l1;
     Right r0, r1;
-#pragma unroll
-    for (int t = 0; t < NBM + NBN; ++t) read_both(0, 0, l0, r0, t);
+    each<BOTH>([&](auto t) __attribute__((always_inline)) { read_both(0, 1, 0, l0, r0, t); });
+    int lslot = 0, rslot = 1;                           // of this stage
+    int freed = SLOTS - 2;                              // the two slots handed over last, the second one next to it
     for (int s = 0; s < stages; ++s) {
-        // under the last group: the next stage's first fragments, then the loads of the stage after it
-        auto next_stage = [&](Left& l, Right& r) {
-            return [&, s](int k) __attribute__((always_inline)) {
-                share(k, NBM + NBN, [&](int t) { read_both(s + 1, 0, l, r, t); });
-                share(k, 2 * LOADS, [&](int t) { load_one(s + 2, t); });
+        const int lnext = lslot + 2 < SLOTS ? lslot + 2 : lslot + 2 - SLOTS;
+        const int rnext = rslot + 2 < SLOTS ? rslot + 2 : rslot + 2 - SLOTS;
+        const int freed1 = freed + 1 < SLOTS ? freed + 1 : 0;
+        // Under group g: the loads of its share of the two freed slots ...
+        auto loads = [&](auto g, auto k) __attribute__((always_inline)) {
+            each<2 * LOADS>([&](auto t) __attribute__((always_inline)) {
+                if constexpr (t * (GROUPS - 1) * PRODUCTS / (2 * LOADS) == g * PRODUCTS + k)
+                    load_one(2 * s + SLOTS - 2 + t / LOADS, t / LOADS ? freed1 : freed, t % LOADS);
+            });
+        };
+        // ... and the next group's fragments
+        auto both = [&](auto g, int ls, int rs, int q, Left& l, Right& r) __attribute__((always_inline)) {
+            return [&, g, ls, rs, q](auto k) __attribute__((always_inline)) {
+                share(k, BOTH, [&](auto t) __attribute__((always_inline)) { read_both(ls, rs, q, l, r, t); });
+                loads(g, k);
             };
         };
+        constexpr std::integral_constant<int, 0> G0{};
+        constexpr std::integral_constant<int, 1> G1{};
+        constexpr std::integral_constant<int, 2> G2{};
+        constexpr std::integral_constant<int, 3> G3{};
+        constexpr std::integral_constant<int, 4> G4{};
+        constexpr std::integral_constant<int, 5> G5{};
+        if constexpr (KIND != kGram) fold(s, KIND == kUpdate ? rslot : lslot);
         if constexpr (!SPLIT) {
-            group(l0, r0, [&](int k) { share(k, NBM + NBN, [&](int t) { read_both(s, 1, l1, r1, t); }); });
-            group(l1, r1, [&](int k) { share(k, NBM + NBN, [&](int t) { read_both(s, 2, l0, r0, t); }); });
-            group(l0, r0, [&](int k) { share(k, NBM + NBN, [&](int t) { read_both(s, 3, l1, r1, t); }); });
+            group(l0, r0, both(G0, lslot, rslot, 1, l1, r1));
+            group(l1, r1, both(G1, lslot, rslot, 2, l0, r0));
+            group(l0, r0, both(G2, lslot, rslot, 3, l1, r1));
             hand_over();
-            group(l1, r1, next_stage(l0, r0));
+            group(l1, r1, both(G3, lnext, rnext, 0, l0, r0));
         } else {
             Left low_l;
             Right low_r;
-            group(l0, r0, [&](int k) { share(k, NBN, [&](int t) { low_r.v[t] = read_right(s, 2, t); }); });
-            group(l0, low_r, [&](int k) { share(k, NBM, [&](int t) { low_l.v[t] = read_left(s, 2, t); }); });
-            group(low_l, r0, [&](int k) { share(k, NBM + NBN, [&](int t) { read_both(s, 1, l1, r1, t); }); });
-            group(l1, r1, [&](int k) { share(k, NBN, [&](int t) { low_r.v[t] = read_right(s, 3, t); }); });
-            group(l1, low_r, [&](int k) { share(k, NBM, [&](int t) { low_l.v[t] = read_left(s, 3, t); }); });
+            auto rights = [&](auto g, int q) __attribute__((always_inline)) {
+                return [&, g, q](auto k) __attribute__((always_inline)) {
+                    share(k, RIGHTS, [&](auto t) __attribute__((always_inline)) { low_r.v[t] = read_right(rslot, q, t); });
+                    loads(g, k);
+                };
+            };
+            auto lefts = [&](auto g, int q) __attribute__((always_inline)) {
+                return [&, g, q](auto k) __attribute__((always_inline)) {
+                    share(k, LEFTS, [&](auto t) __attribute__((always_inline)) { low_l.v[t] = read_left(lslot, q, t); });
+                    loads(g, k);
+                };
+            };
+            group(l0, r0, rights(G0, 2));
+            group(l0, low_r, lefts(G1, 2));
+            group(low_l, r0, both(G2, lslot, rslot, 1, l1, r1));
+            group(l1, r1, rights(G3, 3));
+            group(l1, low_r, lefts(G4, 3));
             hand_over();
-            group(low_l, r1, next_stage(l0, r0));
+            group(low_l, r1, both(G5, lnext, rnext, 0, l0, r0));
         }
+        freed = lslot;
+        lslot = lnext;
+        rslot = rnext;
     }
     wait_lgkmcnt0();
     wait_vmcnt<0>();
     barrier_no_fence();
 
-    // acc[j][i][4g + t] is the product at row 32 i + l32 and column 32 j + 8 g + 4 lhi + t of the
-    // wave's part.  It goes out through LDS, 32 rows at a time, so that every store writes whole runs of a row: once as
-    // it is and, for a tile below the diagonal, once transposed.
+    // acc[j][i][4g + t] is the sum at row 32 i + l32 and column 32 j + 8 g + 4 lhi + t of the wave's
+    // part.  It goes out through LDS, 32 rows at a time, so that every store writes whole runs of a row: once as it
+    // is and, for a tile below the diagonal, once transposed.
     constexpr bool TWO = SPLIT || KIND == kUpdate;      // both planes are kept
+    constexpr bool LOW = !SPLIT && KIND == kUpdate;     // the iterate's low plane was no operand: added here
     const int64_t lo_off = SPLIT ? 32 : (int64_t)p.batch * p.rows * p.cols;
     const int64_t matrix = (int64_t)b * p.rows * p.cols * (SPLIT ? 2 : 1);
     uint16_t* const out = (uint16_t*)p.out + matrix;
-    const uint16_t* const add = (const uint16_t*)p.add + matrix;
-    lds_char* const mine = lds + wave * (4 * STAGE / WAVES);
-    static_assert(32 * (WTM > WTN ? WTM : WTN) * 4 <= 4 * STAGE / WAVES, "the image fits the wave's share of LDS");
+    const uint16_t* const low = (const uint16_t*)p.right + matrix + lo_off;
+    const float low_scale = p.linear * p.scale;
+    const int64_t row_w = m0 + wm * WTM, col_w = n0 + wn * WTN;
+    lds_char* const mine = lds + wave * (SLOTS * STAGE / WAVES);
+    static_assert(32 * (WTM > WTN ? WTM : WTN) * 4 <= SLOTS * STAGE / WAVES, "the image fits the wave's share of LDS");
     // the wave's own LDS accesses keep their order; this keeps the compiler from changing it
-    auto image_written = [] { asm volatile("" ::: "memory"); };
-    auto drain = [&](auto width, int64_t row0, int64_t col0) __attribute__((always_inline)) {
-        constexpr int W = decltype(width)::value, LPR = W / 8, RPI = 64 / LPR, N = 32 / RPI;
-        int64_t at[N];
-        Addend<KIND, TWO> old[N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            at[n] = element<SPLIT>(row0 + n * RPI + lane / LPR, col0 + 8 * (lane % LPR), p.cols);
-            old[n].load(add, at[n], lo_off);
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int r = n * RPI + lane / LPR, c = 2 * (lane % LPR);
-            const f32x4 u = __builtin_bit_cast(f32x4, lds_load_16B(mine, image_at<W>(r, c)));
-            const f32x4 w = __builtin_bit_cast(f32x4, lds_load_16B(mine, image_at<W>(r, c + 1)));
-            const float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
-            store_eight<KIND, TWO>(p, v, old[n], out, at[n], lo_off);
-        }
-        asm volatile("" ::: "memory");
-    };
-#pragma unroll
-    for (int i = 0; i < NBM; ++i) {
+    auto in_order = [] { asm volatile("" ::: "memory"); };
+    // Rows 32 i .. of the part as they are, or (turned) columns 32 j .. as rows.
+    auto write_rows = [&](int i) __attribute__((always_inline)) {
+        in_order();
 #pragma unroll
         for (int j = 0; j < NBN; ++j)
 #pragma unroll
@@ -420,24 +473,112 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
                 const f32x4 v = {acc[j][i][4 * g], acc[j][i][4 * g + 1], acc[j][i][4 * g + 2], acc[j][i][4 * g + 3]};
                 lds_store_16B(mine, image_at<WTN>(l32, 8 * j + 2 * g + lhi), __builtin_bit_cast(i32x4, v));
             }
-        image_written();
-        drain(std::integral_constant<int, WTN>{}, m0 + wm * WTM + 32 * i, n0 + wn * WTN);
-    }
-    if (KIND != kUpdate && m0 != n0) {
+        in_order();
+    };
+    auto write_turned = [&](int j) __attribute__((always_inline)) {
+        in_order();
+#pragma unroll
+        for (int i = 0; i < NBM; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint32_t at = image_at<WTM>(8 * g + 4 * lhi + t, 8 * i + (l32 >> 2)) + (l32 & 3) * 4u;
+                    *reinterpret_cast<__attribute__((address_space(3))) float*>(mine + at) = acc[j][i][4 * g + t];
+                }
+        in_order();
+    };
+    // Each lane's eight elements of the image's rows: store(r, n, v) with the row r of the first lane in store n.
+    auto read_rows = [&](auto width, auto store) __attribute__((always_inline)) {
+        constexpr int W = decltype(width)::value, LPR = W / 8, RPI = 64 / LPR;
+        each<32 / RPI>([&](auto n) __attribute__((always_inline)) {
+            const int r = n * RPI + lane / LPR, c = lane % LPR;
+            const f32x4 u = __builtin_bit_cast(f32x4, lds_load_16B(mine, image_at<W>(r, 2 * c)));
+            const f32x4 w = __builtin_bit_cast(f32x4, lds_load_16B(mine, image_at<W>(r, 2 * c + 1)));
+            float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] *= p.scale;
+            store(n * RPI, n, v);
+        });
+    };
+    // Element (row0 + the lane's row, col0 + the lane's columns) of a stored matrix: a uniform base and the
+    // lane's own 32-bit offset.
+    const int64_t row_step = p.cols * (SPLIT ? 2 : 1);
+    auto lane_row = [&](auto width) { return lane / (decltype(width)::value / 8); };
+    auto lane_col = [&](auto width) { return 8 * (lane % (decltype(width)::value / 8)); };
+    auto lane_at = [&](auto width) { return (uint32_t)element<SPLIT>(lane_row(width), lane_col(width), p.cols); };
+    const std::integral_constant<int, WTN> across;
+    const std::integral_constant<int, WTM> turned;
+    auto result_at = [&](int64_t row, int64_t col, const float (&v)[8]) __attribute__((always_inline)) {
+        if constexpr (!SPLIT) {
+            store_result<kOutBf16>(p, v, b, row, col);
+        } else {
+            if (p.result_dtype == kOutF16) store_result<kOutF16>(p, v, b, row, col);
+            else store_result<kOutF32>(p, v, b, row, col);
+        }
+    };
+
+    if (KIND == kUpdate && !p.out && p.tall) {
+        // the last step of a matrix taken transposed: its result is the transpose
+        if constexpr (LOW) {
+#pragma unroll
+            for (int i = 0; i < NBM; ++i) {
+                in_order();                             // a few loads at a time: the registers are full
+#pragma unroll
+                for (int j = 0; j < NBN; ++j)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const i16x4 x = *(const __attribute__((address_space(1))) i16x4*)(
+                            low + (row_w + 32 * i + l32) * p.cols + col_w + 32 * j + 8 * g + 4 * lhi);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) acc[j][i][4 * g + t] += p.linear * half_bits((uint16_t)x[t]);
+                    }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NBN; ++j) {
-#pragma unroll
-            for (int i = 0; i < NBM; ++i)
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t at = image_at<WTM>(8 * g + 4 * lhi + t, 8 * i + (l32 >> 2)) + (l32 & 3) * 4u;
-                        *reinterpret_cast<__attribute__((address_space(3))) float*>(mine + at) = acc[j][i][4 * g + t];
-                    }
-            image_written();
-            drain(std::integral_constant<int, WTM>{}, n0 + wn * WTN + 32 * j, m0 + wm * WTM);
+            write_turned(j);
+            read_rows(turned, [&](int r, int, const float (&v)[8]) __attribute__((always_inline)) {
+                result_at(col_w + 32 * j + r + lane_row(turned), row_w + lane_col(turned), v);
+            });
         }
+        return;
+    }
+    constexpr int PIECES = WTN / 16;                    // of eight elements a lane in 32 rows
+    const uint32_t at_across = lane_at(across), at_turned = lane_at(turned);
+    i32x4 lows[2][PIECES];                              // 32 rows ahead of their use
+    auto load_low = [&](auto i) __attribute__((always_inline)) {
+        if constexpr (LOW)
+            each<PIECES>([&](auto n) __attribute__((always_inline)) {
+                const uint16_t* const from = low + (row_w + 32 * i + n * (512 / WTN)) * p.cols + col_w;
+                lows[i & 1][n] = *(const gbl_i32x4*)(from + at_across);
+            });
+    };
+    load_low(std::integral_constant<int, 0>{});
+    each<NBM>([&](auto i) __attribute__((always_inline)) {
+        if constexpr (i + 1 < NBM) load_low(std::integral_constant<int, i + 1>{});
+        write_rows(i);
+        read_rows(across, [&](int r, auto n, float (&v)[8]) __attribute__((always_inline)) {
+            const int64_t row = row_w + 32 * i + r;
+            if constexpr (LOW) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    v[2 * u] += low_scale * f16_lo((uint32_t)lows[i & 1][n][u]);
+                    v[2 * u + 1] += low_scale * f16_hi((uint32_t)lows[i & 1][n][u]);
+                }
+            }
+            if (KIND == kUpdate && !p.out) result_at(row + lane_row(across), col_w + lane_col(across), v);
+            else store_planes<TWO>(v, out + row * row_step + col_w * (SPLIT ? 2 : 1) + at_across, lo_off);
+        });
+    });
+    if (KIND != kUpdate && m0 != n0) {
+        each<NBN>([&](auto j) __attribute__((always_inline)) {
+            write_turned(j);
+            read_rows(turned, [&](int r, int, const float (&v)[8]) __attribute__((always_inline)) {
+                const int64_t row = col_w + 32 * j + r;
+                store_planes<TWO>(v, out + row * row_step + row_w * (SPLIT ? 2 : 1) + at_turned, lo_off);
+            });
+        });
     }
 }
 
@@ -447,27 +588,30 @@ constexpr int kBigWaves = 8;
 // 256 x 256 tiles; the items past p.whole are quarters of one.
 template <bool SPLIT, NewtonProduct KIND>
 __global__ __launch_bounds__(64 * kBigWaves<SPLIT>, kBigWaves<SPLIT> / 4) void newton_big_kernel(NewtonGemm p) {
-    __shared__ __attribute__((aligned(1024))) char smem[4 * 256 * 128];
+    __shared__ __attribute__((aligned(1024))) char smem[5 * 256 * 128];
     const int bid = blockIdx.x;
-    int b, tm, tn;
+    int b, tm, tn, turn;
     if (bid < p.whole) {
         tile_of<KIND>(p, item_of(bid, p.whole, p.num_xcds), b, tm, tn);
-        newton_tile<256, kBigWaves<SPLIT>, SPLIT, KIND>(p, smem, b, (int64_t)tm * 256, (int64_t)tn * 256);
+        turn = turn_of<SPLIT, KIND>(p, tm, 256);
+        newton_tile<256, kBigWaves<SPLIT>, 5, SPLIT, KIND>(p, smem, b, (int64_t)tm * 256, (int64_t)tn * 256, turn);
     } else {
         const int part = bid - p.whole;
         tile_of<KIND>(p, p.whole + (part >> 2), b, tm, tn);
+        turn = turn_of<SPLIT, KIND>(p, tm, 256);
         const int64_t m0 = (int64_t)tm * 256 + (part & 1) * 128, n0 = (int64_t)tn * 256 + ((part >> 1) & 1) * 128;
         if (KIND != kUpdate && n0 > m0) return;         // the mirror image of another quarter
-        newton_tile<128, kBigWaves<SPLIT>, SPLIT, KIND>(p, smem, b, m0, n0);
+        newton_tile<128, kBigWaves<SPLIT>, 10, SPLIT, KIND>(p, smem, b, m0, n0, turn);
     }
 }
 
-template <bool SPLIT, NewtonProduct KIND>
-__global__ __launch_bounds__(256, 2) void newton_small_kernel(NewtonGemm p) {
-    __shared__ __attribute__((aligned(1024))) char smem[4 * 128 * 128];
+// 128 x 128 tiles: two workgroups a CU with five slots each, or one with ten.
+template <int SLOTS, bool SPLIT, NewtonProduct KIND>
+__global__ __launch_bounds__(256, SLOTS == 5 ? 2 : 1) void newton_small_kernel(NewtonGemm p) {
+    __shared__ __attribute__((aligned(1024))) char smem[SLOTS * 128 * 128];
     int b, tm, tn;
     tile_of<KIND>(p, item_of(blockIdx.x, p.items, p.num_xcds), b, tm, tn);
-    newton_tile<128, 4, SPLIT, KIND>(p, smem, b, (int64_t)tm * 128, (int64_t)tn * 128);
+    newton_tile<128, 4, SLOTS, SPLIT, KIND>(p, smem, b, (int64_t)tm * 128, (int64_t)tn * 128, turn_of<SPLIT, KIND>(p, tm, 128));
 }
 
 template <bool SPLIT, NewtonProduct KIND>
@@ -484,7 +628,10 @@ void launch_product(NewtonGemm g, int tile, int num_cus, hipStream_t stream) {
                            stream, g);
     } else {
         g.items = g.whole = tiles;
-        hipLaunchKernelGGL((newton_small_kernel<SPLIT, KIND>), dim3((uint32_t)g.items), dim3(256), 0, stream, g);
+        if (tiles > num_cus)
+            hipLaunchKernelGGL((newton_small_kernel<5, SPLIT, KIND>), dim3((uint32_t)g.items), dim3(256), 0, stream, g);
+        else
+            hipLaunchKernelGGL((newton_small_kernel<10, SPLIT, KIND>), dim3((uint32_t)g.items), dim3(256), 0, stream, g);
     }
 }
 
@@ -495,6 +642,10 @@ void launch_steps(const NewtonParams& p, const NewtonPlan& plan, const float* co
     g.batch = p.batch;
     g.num_xcds = num_xcds;
     g.rows = plan.r;
+    g.m = p.m;
+    g.n = p.n;
+    g.result_dtype = p.out_dtype;
+    g.tall = plan.tall ? 1 : 0;
     for (int s = 0; s < p.steps; ++s) {
         const char* const x = p.x[s & 1];
         g.cols = plan.r;
@@ -503,18 +654,22 @@ void launch_steps(const NewtonParams& p, const NewtonPlan& plan, const float* co
         g.out = p.a;
         g.scale = kAScale / (kXScale * kXScale);
         launch_product<SPLIT, kGram>(g, plan.tile, num_cus, stream);
+        // c A A + b A = c (A A + b / c A)
+        const float b = co[3 * s + 1], c = newton_c(co + 3 * s);
         g.k = plan.r;
-        g.left = g.right = g.add = p.a;
+        g.left = g.right = p.a;
         g.out = p.b;
-        g.scale = co[3 * s + 2] * (kBScale / (kAScale * kAScale));
-        g.add_scale = co[3 * s + 1] * (kBScale / kAScale);
+        g.scale = c * (kBScale / (kAScale * kAScale));
+        g.linear = c != 0.0f ? b / c * kAScale : 0.0f;
         launch_product<SPLIT, kSquare>(g, plan.tile, num_cus, stream);
         g.cols = plan.c;
         g.left = p.b;
-        g.right = g.add = x;
-        g.out = p.x[(s + 1) & 1];
-        g.scale = 1.0f / kBScale;
-        g.add_scale = co[3 * s];
+        g.right = x;
+        const bool last = s + 1 == p.steps;
+        g.out = last ? nullptr : p.x[(s + 1) & 1];
+        g.result = p.out;
+        g.scale = (last ? 1.0f / kXScale : 1.0f) / kBScale;
+        g.linear = co[3 * s] * kBScale;
         launch_product<SPLIT, kUpdate>(g, plan.tile, num_cus, stream);
     }
 }
@@ -522,51 +677,54 @@ void launch_steps(const NewtonParams& p, const NewtonPlan& plan, const float* co
 template <bool SPLIT, bool TALL>
 void launch_all(const NewtonParams& p, const NewtonPlan& plan, const float* co, int num_cus, int num_xcds,
                 hipStream_t stream) {
-    const dim3 norm_grid(kNewtonParts, (uint32_t)p.batch);
+    launch_newton_norm(p, stream);
     const dim3 tiles((uint32_t)(plan.c / 64), (uint32_t)(plan.r / 64), (uint32_t)p.batch);
     auto first = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        hipLaunchKernelGGL((newton_norm_kernel<DT>), norm_grid, dim3(NT), 0, stream, p);
         hipLaunchKernelGGL((newton_first_kernel<DT, SPLIT, TALL>), tiles, dim3(NT), 0, stream, p, plan.r, plan.c);
     };
     if (p.dtype == kOutBf16) first(std::integral_constant<int, kOutBf16>{});
     else if (p.dtype == kOutF16) first(std::integral_constant<int, kOutF16>{});
     else first(std::integral_constant<int, kOutF32>{});
     launch_steps<SPLIT>(p, plan, co, num_cus, num_xcds, stream);
-    const char* const x = p.x[p.steps & 1];
-    auto last = [&](auto dt) {
-        constexpr int DT = decltype(dt)::value;
-        hipLaunchKernelGGL((newton_last_kernel<DT, SPLIT, TALL>), tiles, dim3(NT), 0, stream, p, x, plan.r, plan.c);
-    };
-    if constexpr (!SPLIT) {
-        last(std::integral_constant<int, kOutBf16>{});
-    } else {
-        if (p.out_dtype == kOutF16) last(std::integral_constant<int, kOutF16>{});
-        else last(std::integral_constant<int, kOutF32>{});
-    }
 }
 
 }  // namespace
 
+void launch_newton_norm(const NewtonParams& p, hipStream_t stream) {
+    const dim3 grid((uint32_t)p.num_parts, (uint32_t)p.batch);
+    if (p.dtype == kOutBf16) hipLaunchKernelGGL((newton_norm_kernel<kOutBf16>), grid, dim3(NT), 0, stream, p);
+    else if (p.dtype == kOutF16) hipLaunchKernelGGL((newton_norm_kernel<kOutF16>), grid, dim3(NT), 0, stream, p);
+    else hipLaunchKernelGGL((newton_norm_kernel<kOutF32>), grid, dim3(NT), 0, stream, p);
+}
+
 NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
-    NewtonPlan plan;
+    NewtonPlan plan = {};
     const int64_t r = m < n ? m : n, c = m < n ? n : m;
-    plan.split = out_dtype != kOutBf16;
     plan.tall = m > n;
+    plan.parts_bytes = ((size_t)batch * kNewtonParts * sizeof(double) + 1023) / 1024 * 1024;
+    plan.narrow = r <= kNarrowMax;
+    if (plan.narrow) {
+        newton_narrow_plan(batch, r, c, &plan);
+        return plan;
+    }
+    plan.split = out_dtype != kOutBf16;
     // 256 x 256 tiles where the update alone has one for every CU, else four times as many of 128 x 128
     plan.tile = ((r + 255) / 256) * ((c + 255) / 256) * batch >= 256 ? 256 : 128;
     plan.r = (r + plan.tile - 1) / plan.tile * plan.tile;
     plan.c = (c + plan.tile - 1) / plan.tile * plan.tile;
     plan.x_bytes = (size_t)batch * plan.r * plan.c * 4;
     plan.a_bytes = (size_t)batch * plan.r * plan.r * (plan.split ? 4 : 2);
-    plan.parts_bytes = ((size_t)batch * kNewtonParts * sizeof(double) + 1023) / 1024 * 1024;
-    plan.total = plan.parts_bytes + 2 * plan.x_bytes + 2 * plan.a_bytes;
+    plan.b_bytes = plan.a_bytes;
+    plan.total = plan.parts_bytes + 2 * plan.x_bytes + plan.a_bytes + plan.b_bytes;
     return plan;
 }
 
 hipError_t launch_newton(const NewtonParams& p, const NewtonPlan& plan, const float* coefficients, int num_cus,
                          int num_xcds, hipStream_t stream) {
-    if (plan.split) {
+    if (plan.narrow) {
+        launch_newton_narrow(p, plan, coefficients, stream);
+    } else if (plan.split) {
         if (plan.tall) launch_all<true, true>(p, plan, coefficients, num_cus, num_xcds, stream);
         else launch_all<true, false>(p, plan, coefficients, num_cus, num_xcds, stream);
     } else {

@@ -1,0 +1,81 @@
+// Device code shared by the Newton-Schulz kernels: the planes' scales, loading of G and small helpers.
+#pragma once
+
+#include <type_traits>
+#include <utility>
+
+#include "kgw_device.h"
+#include "kgw_layer.h"
+
+namespace kgw {
+
+constexpr float kXScale = 8192.0f, kAScale = 1024.0f, kBScale = 128.0f;
+
+typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
+__device__ __forceinline__ f32x16 mfma_f16_32x32x16(i32x4 a, i32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float half_bits(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
+
+// f(0), f(1), .. f(N - 1) with compile-time arguments: register arrays indexed by them stay in registers.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f) {
+    each_of(std::make_integer_sequence<int, N>{}, f);
+}
+
+// Eight consecutive elements of row `row` of matrix b, zeros past the matrix; rows may start at any element.
+struct __attribute__((packed, aligned(2))) Halves8 { i32x4 v; };
+struct __attribute__((packed, aligned(4))) Floats4 { f32x4 v; };
+template <int DT>
+__device__ __forceinline__ void load_eight(const NewtonParams& p, int b, int64_t row, int64_t col, float (&v)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = 0.0f;
+    if (row >= p.m || col >= p.n) return;
+    const int64_t at = (int64_t)b * p.stride + row * p.ld + col;
+    if constexpr (DT == kOutF32) {
+        const float* const from = (const float*)p.G + at;
+        if (col + 8 <= p.n) {
+            const f32x4 x = ((const __attribute__((address_space(1))) Floats4*)from)[0].v;
+            const f32x4 y = ((const __attribute__((address_space(1))) Floats4*)from)[1].v;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                v[u] = x[u];
+                v[4 + u] = y[u];
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (col + u < p.n) v[u] = from[u];
+        }
+    } else {
+        const uint16_t* const from = (const uint16_t*)p.G + at;
+        if (col + 8 <= p.n) {
+            const i32x4 x = ((const __attribute__((address_space(1))) Halves8*)from)->v;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                v[2 * u] = half_lo<DT>((uint32_t)x[u]);
+                v[2 * u + 1] = half_hi<DT>((uint32_t)x[u]);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (col + u < p.n) v[u] = half_lo<DT>((uint32_t)from[u]);
+        }
+    }
+}
+
+// 2^13 / (|G|_F + eps) of matrix b, the same in every wave.
+__device__ __forceinline__ float first_scale(const NewtonParams& p, int b) {
+    double s = 0.0;
+    for (int i = threadIdx.x & 63; i < p.num_parts; i += 64) s += p.parts[(int64_t)b * kNewtonParts + i];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    return (float)((double)kXScale / (__builtin_sqrt(s) + (double)p.eps));
+}
+
+}  // namespace kgw

@@ -65,6 +65,9 @@ kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_
     const int64_t parts = (m * n + 8191) / 8192;
     p.num_parts = (int32_t)(parts < kgw::kNewtonParts ? parts : kgw::kNewtonParts);
     p.parts = (double*)(p.b + plan.b_bytes);
+    char* const slabs = p.b + plan.b_bytes + plan.parts_bytes;
+    p.slabs = plan.slab_bytes ? (float*)slabs : nullptr;
+    p.arrived = plan.slab_bytes ? (uint32_t*)(slabs + plan.slab_bytes - kgw::kNewtonSlabs * sizeof(uint32_t)) : nullptr;
     return kgw::launch_newton(p, plan, coefficients, num_cus, num_xcds, (hipStream_t)stream) == hipSuccess
                ? KGW_SUCCESS
                : KGW_ERROR_DEVICE;

@@ -58,6 +58,8 @@ hipError_t launch_moe_rows(const MoeRowsParams& p, int op, int dtype, hipStream_
 constexpr int kNewtonMaxSteps = 64;
 constexpr int kNewtonParts = 256;       // partial sums of squares per matrix, at most
 
+constexpr int kNewtonSlabs = 256;       // workgroups that may share tiles: one for every CU
+
 struct NewtonParams {
     const void* G;          // (batch, m, n), rows contiguous
     void* out;              // (batch, m, n), contiguous
@@ -73,6 +75,8 @@ struct NewtonParams {
     char* x[2];             // iterates, see kgw_newton.hip and kgw_newton_narrow.hip
     char* a;
     char* b;
+    float* slabs;           // (kNewtonSlabs, tile, tile), small tiles only
+    uint32_t* arrived;      // (kNewtonSlabs,), or NULL
 };
 
 // The factor c of one step's (a, b, c), for c A A + b A = c (A A + b / c A): one that is nothing beside b
@@ -91,8 +95,8 @@ struct NewtonPlan {
     int64_t r, c;           // padded sizes of the iterates, r the short side
     int32_t chunks;         // narrow: 128-column chunks of a matrix
     int32_t per_group;      // narrow: chunks of one workgroup
-    int32_t groups;         // narrow: workgroups of a matrix
-    size_t x_bytes, a_bytes, b_bytes, parts_bytes, total;
+    int32_t groups;         // narrow: workgroups of a matrix (0: one that runs all steps)
+    size_t x_bytes, a_bytes, b_bytes, parts_bytes, slab_bytes, total;
 };
 constexpr int64_t kNarrowMax = 128;
 NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype);

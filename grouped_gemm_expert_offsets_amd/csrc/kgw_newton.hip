@@ -25,6 +25,7 @@ namespace kgw {
 namespace {
 
 constexpr int NT = 256;
+static_assert(kNewtonSlabs <= NT, "one workgroup clears the counters");
 
 // ----------------------------------------------------------------------------
 // storage
@@ -44,8 +45,9 @@ __device__ __forceinline__ void store_planes(const float (&v)[8], uint16_t* out,
     i32x4 h, l;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        h[u] = (int)pack_f16x2(v[2 * u], v[2 * u + 1]);
-        if constexpr (TWO) l[u] = (int)pack_f16x2(v[2 * u] - f16_lo((uint32_t)h[u]), v[2 * u + 1] - f16_hi((uint32_t)h[u]));
+        const HalfPair p = split_pair(v[2 * u], v[2 * u + 1]);
+        h[u] = (int)p.hi;
+        if constexpr (TWO) l[u] = (int)p.lo;
     }
     *(gbl_i32x4*)out = h;
     if constexpr (TWO) *(gbl_i32x4*)(out + lo_off) = l;
@@ -75,6 +77,7 @@ __global__ __launch_bounds__(NT) void newton_norm_kernel(NewtonParams p) {
     for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
     if ((tid & 63) == 0) sums[tid >> 6] = s;
     __syncthreads();
+    if (p.arrived && blockIdx.x == 0 && b == 0 && tid < kNewtonSlabs) p.arrived[tid] = 0;
     if (tid == 0) p.parts[(int64_t)b * kNewtonParts + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, int64_
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] *= scale;
+        for (int e = 0; e < 8; ++e) v[u][e] = as_fp32(v[u][e] * scale);
         store_planes<true>(v[u], x + element<SPLIT>(r0 + i0 + 32 * u, c0 + 8 * q, C), lo_off);
     }
 }
@@ -127,6 +130,11 @@ struct NewtonGemm {
     int32_t batch, tiles_m, tiles_n;
     int32_t items;          // workgroups with work
     int32_t whole;          // the first of them: one tile each; the others a quarter of one
+    int32_t tiles;          // of 256 x 256 in all matrices
+    int32_t strips;         // quarters of one matrix beside its tiles
+    int32_t parts;          // workgroups that share a tile's K (small tiles of the symmetric products)
+    float* slabs;           // their sums, one tile each
+    uint32_t* arrived;      // per tile, zero between launches
     int32_t num_xcds;
 };
 
@@ -202,6 +210,63 @@ __device__ __forceinline__ void store_result(const NewtonGemm& p, const float (&
     }
 }
 
+// Puts this workgroup's sums down beside those of the other parts of its tile's K.  The last one to arrive adds
+// all of them up, in the order of the parts whoever is last, and goes on with the tile (true).  No one
+// waits: a workgroup that is not the last is done.
+//
+// The parts of a tile may run on different dies, whose L2 caches do not see each other's stores.  The sums
+// therefore go out and come back as device-scope accesses, which are performed beyond those caches; a store
+// counts as done (vmcnt) only there, so waiting for the own stores before counting the arrival is all the
+// release that is needed.  A fence would write back each die's whole L2 for every workgroup: with 216
+// workgroups of 64 KiB it made a product of 35 us take 57.
+template <int NBM, int NBN>
+__device__ bool join_parts(const NewtonGemm& p, char* smem, int tile, int part, int wave, int lane,
+                           f32x16 (&acc)[NBN][NBM]) {
+    constexpr int WAVE = NBM * NBN * 1024;              // floats of one wave
+    float* const tile_slabs = p.slabs + (int64_t)tile * p.parts * (4 * WAVE) + wave * WAVE + lane;
+    float* const own = tile_slabs + part * (4 * WAVE);
+#pragma unroll
+    for (int j = 0; j < NBN; ++j)
+#pragma unroll
+        for (int i = 0; i < NBM; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                __hip_atomic_store(own + ((j * NBM + i) * 16 + e) * 64, acc[j][i][e], __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" ::: "memory");
+    wait_vmcnt<0>();
+    barrier_no_fence();                                 // every wave's sums are down
+    uint32_t* const last = (uint32_t*)smem;
+    if (threadIdx.x == 0)
+        *last = __hip_atomic_fetch_add(p.arrived + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                        (uint32_t)p.parts - 1u
+                    ? 1u
+                    : 0u;
+    __syncthreads();
+    const bool is_last = *last != 0;
+    __syncthreads();                                    // smem is free again
+    if (!is_last) return false;
+    if (threadIdx.x == 0) __hip_atomic_store(p.arrived + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int j = 0; j < NBN; ++j)
+#pragma unroll
+        for (int i = 0; i < NBM; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[j][i][e] = 0.0f;
+    for (int w = 0; w < p.parts; ++w) {
+        const float* const from = tile_slabs + w * (4 * WAVE);
+#pragma unroll
+        for (int j = 0; j < NBN; ++j)
+#pragma unroll
+            for (int i = 0; i < NBM; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc[j][i][e] += __hip_atomic_load(from + ((j * NBM + i) * 16 + e) * 64, __ATOMIC_RELAXED,
+                                                      __HIP_MEMORY_SCOPE_AGENT);
+    }
+    return true;
+}
+
 // One TILE x TILE tile at rows m0 and columns n0 of matrix b.  A stage of the K loop is a 128-byte line
 // of every row of the left tile (64 halves of K, or 32 of both planes) and as many bytes of the right
 // one, in a ring of SLOTS.  Left tiles, and the right ones of the symmetric products, are read as
@@ -213,8 +278,9 @@ __device__ __forceinline__ void store_result(const NewtonGemm& p, const float (&
 // multiplies.  Before the last group every read of the stage is done, so the barrier that hands the
 // slot over stands there, and the next stage's first fragments and the loads of the one after
 // ring go out under the last group's products.
-template <int TILE, int WAVES, int SLOTS, bool SPLIT, NewtonProduct KIND>
-__device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int b, int64_t m0, int64_t n0, int turn) {
+template <int TILE, int WAVES, int SLOTS, bool SPLIT, bool JOIN, NewtonProduct KIND>
+__device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int b, int64_t m0, int64_t n0, int turn,
+                                            int tile = 0, int part = 0) {
     constexpr int WM = 2, WN = WAVES / 2;               // waves along rows and columns
     constexpr int WTM = TILE / WM, WTN = TILE / WN;     // a wave's part
     constexpr int NBM = WTM / 32, NBN = WTN / 32;       // 32 x 32 blocks of it
@@ -246,15 +312,20 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
         if constexpr (KIND == kUpdate) {
             const int at = (wave * LOADS + t) * 64 + lane;
             const int krow = at / CPR;
-            r_off[t] = (uint32_t)krow * (uint32_t)ldr + (uint32_t)((at % CPR) ^ ((krow & 3) << 2)) * 16u;
+            r_off[t] = (uint32_t)krow * (uint32_t)ldr + (uint32_t)((at % CPR) ^ (((krow & 3) << 2) & (CPR - 1))) * 16u;
         } else {
             r_off[t] = (uint32_t)row * (uint32_t)ldr + chunk * 16u;
         }
     }
-    const int stages = (int)(p.k / KSTAGE);
+    const int all_stages = (int)(p.k / KSTAGE);
+    const int first_stage = JOIN ? all_stages * part / p.parts : 0;
+    const int stages = JOIN ? all_stages * (part + 1) / p.parts - first_stage : all_stages;
     const int64_t r_step = KIND == kUpdate ? KSTAGE * ldr : 128;
     // Three products: the update walks K from stage `turn` on, so that its linear term comes late (fold()).
-    auto place_of = [&](int s) __attribute__((always_inline)) { return s + turn < stages ? s + turn : s + turn - stages; };
+    // Parts of K: the stages from first_stage on (never both).
+    auto place_of = [&](int s) __attribute__((always_inline)) {
+        return KIND != kUpdate ? first_stage + s : s + turn < stages ? s + turn : s + turn - stages;
+    };
     // Slot n % SLOTS takes the n-th operand stage, left and right in turn.  Load t of slot `slot` with
     // operand stage n; past the last one an empty range (no memory is read).
     auto load_one = [&](int n, int slot, int t) __attribute__((always_inline)) {
@@ -278,7 +349,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
         if constexpr (KIND == kUpdate) {
             const int chunk = SPLIT ? (wn * NBN + j) * 8 + (q >> 1) * 4 + cq : wn * (WTN / 8) + 4 * j + cq;
             const uint32_t at = (uint32_t)((SPLIT ? 16 * (q & 1) : 16 * q) + kr) * (uint32_t)ROWB +
-                                (uint32_t)((chunk ^ ((i16 >> 2) << 2)) << 4) + (uint32_t)(i16 & 1) * 8u;
+                                (uint32_t)((chunk ^ (((i16 >> 2) << 2) & (CPR - 1))) << 4) + (uint32_t)(i16 & 1) * 8u;
             const i16x4 lo = lds_read_tr16(base, at);
             const i16x4 hi = lds_read_tr16(base, at + 4 * ROWB);
             const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -324,7 +395,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
                         if constexpr (KIND == kUpdate) {
                             const int krow = 32 * e + l32;
                             const int chunk = SPLIT ? (wn * NBN + j) * 8 + plane * 4 + g : wn * (WTN / 8) + 4 * j + g;
-                            from = (uint32_t)(krow * ROWB + ((chunk ^ ((krow & 3) << 2)) << 4));
+                            from = (uint32_t)(krow * ROWB + ((chunk ^ (((krow & 3) << 2) & (CPR - 1))) << 4));
                         } else {
                             const int chunk = SPLIT ? plane * 4 + g : 4 * e + g;
                             from = l_row + (uint32_t)i * 4096u + (uint32_t)((chunk ^ sw) << 4);
@@ -447,6 +518,16 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     wait_lgkmcnt0();
     wait_vmcnt<0>();
     barrier_no_fence();
+
+    if constexpr (JOIN) {
+        // the sums stay in one kind of registers: the compiler would otherwise move them to the other kind and back
+        // in every stage, for the stores below
+#pragma unroll
+        for (int j = 0; j < NBN; ++j)
+#pragma unroll
+            for (int i = 0; i < NBM; ++i) asm volatile("" : "+v"(acc[j][i]));
+        if (!join_parts<NBM, NBN>(p, smem, tile, part, wave, lane, acc)) return;
+    }
 
     // acc[j][i][4g + t] is the sum at row 32 i + l32 and column 32 j + 8 g + 4 lhi + t of the wave's
     // part.  It goes out through LDS, 32 rows at a time, so that every store writes whole runs of a row: once as it
@@ -582,6 +663,34 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     }
 }
 
+// Quarter `index`: those of the tiles past p.whole, then the 128-wide strips at the ends of odd sizes (of every
+// matrix in turn: down the right side, then along the bottom; along the bottom only for the symmetric products).
+template <NewtonProduct KIND>
+__device__ __forceinline__ void quarter_of(const NewtonGemm& p, int index, int& b, int64_t& m0, int64_t& n0) {
+    const int cut = p.tiles - p.whole;
+    if (index < 4 * cut) {
+        int tm, tn;
+        tile_of<KIND>(p, p.whole + (index >> 2), b, tm, tn);
+        m0 = (int64_t)tm * 256 + (index & 1) * 128;
+        n0 = (int64_t)tn * 256 + ((index >> 1) & 1) * 128;
+        return;
+    }
+    const int per = p.strips;
+    const int e = index - 4 * cut;
+    b = e / per;
+    int at = e - b * per;
+    const int rows = (int)(p.rows / 128);
+    const bool right = KIND == kUpdate && (p.cols & 128);
+    if (right && at < rows) {
+        m0 = (int64_t)at * 128;
+        n0 = p.cols - 128;
+    } else {
+        if (right) at -= rows;
+        m0 = p.rows - 128;
+        n0 = (int64_t)at * 128;
+    }
+}
+
 template <bool SPLIT>
 constexpr int kBigWaves = 8;
 
@@ -594,24 +703,87 @@ __global__ __launch_bounds__(64 * kBigWaves<SPLIT>, kBigWaves<SPLIT> / 4) void n
     if (bid < p.whole) {
         tile_of<KIND>(p, item_of(bid, p.whole, p.num_xcds), b, tm, tn);
         turn = turn_of<SPLIT, KIND>(p, tm, 256);
-        newton_tile<256, kBigWaves<SPLIT>, 5, SPLIT, KIND>(p, smem, b, (int64_t)tm * 256, (int64_t)tn * 256, turn);
+        newton_tile<256, kBigWaves<SPLIT>, 5, SPLIT, false, KIND>(p, smem, b, (int64_t)tm * 256, (int64_t)tn * 256, turn);
     } else {
-        const int part = bid - p.whole;
-        tile_of<KIND>(p, p.whole + (part >> 2), b, tm, tn);
-        turn = turn_of<SPLIT, KIND>(p, tm, 256);
-        const int64_t m0 = (int64_t)tm * 256 + (part & 1) * 128, n0 = (int64_t)tn * 256 + ((part >> 1) & 1) * 128;
+        int64_t m0, n0;
+        quarter_of<KIND>(p, bid - p.whole, b, m0, n0);
         if (KIND != kUpdate && n0 > m0) return;         // the mirror image of another quarter
-        newton_tile<128, kBigWaves<SPLIT>, 10, SPLIT, KIND>(p, smem, b, m0, n0, turn);
+        turn = turn_of<SPLIT, KIND>(p, (int)(m0 / 256), 256);
+        newton_tile<128, kBigWaves<SPLIT>, 10, SPLIT, false, KIND>(p, smem, b, m0, n0, turn);
     }
 }
 
-// 128 x 128 tiles: two workgroups a CU with five slots each, or one with ten.
-template <int SLOTS, bool SPLIT, NewtonProduct KIND>
-__global__ __launch_bounds__(256, SLOTS == 5 ? 2 : 1) void newton_small_kernel(NewtonGemm p) {
-    __shared__ __attribute__((aligned(1024))) char smem[SLOTS * 128 * 128];
+// Small tiles: two workgroups a CU with SLOTS slots each (80 KiB), or one with twice as many.
+// JOIN: p.parts of them share a tile's K.
+template <int TILE, bool TWO, bool JOIN, bool SPLIT, NewtonProduct KIND>
+__global__ __launch_bounds__(256, 2) void newton_small_kernel(NewtonGemm p) {
+    constexpr int SLOTS = (TWO ? 5 : 10) * (128 / TILE);
+    __shared__ __attribute__((aligned(1024))) char smem[SLOTS * TILE * 128];
+    const int item = item_of(blockIdx.x, p.items, p.num_xcds);
+    const int tile = JOIN ? item / p.parts : item;
     int b, tm, tn;
-    tile_of<KIND>(p, item_of(blockIdx.x, p.items, p.num_xcds), b, tm, tn);
-    newton_tile<128, 4, SLOTS, SPLIT, KIND>(p, smem, b, (int64_t)tm * 128, (int64_t)tn * 128, turn_of<SPLIT, KIND>(p, tm, 128));
+    tile_of<KIND>(p, tile, b, tm, tn);
+    newton_tile<TILE, 4, SLOTS, SPLIT, JOIN, KIND>(p, smem, b, (int64_t)tm * TILE, (int64_t)tn * TILE,
+                                             turn_of<SPLIT, KIND>(p, tm, TILE), tile, JOIN ? item - tile * p.parts : 0);
+}
+
+template <int TILE, bool SPLIT, NewtonProduct KIND>
+void launch_small(NewtonGemm g, int tiles, hipStream_t stream) {
+    // Few tiles and a long K: workgroups share a tile's K.  Joining costs a 64-edged tile about as much a part as
+    // two stages, so about sqrt(stages / 2) parts are best (1 x 200 x 7000: 418 -> 190 us); for a
+    // 128-edged one it pays from 24 stages a part on (56 stages in two: 35 -> 29 us, 32 stages: 27 -> 30 us).
+    const int64_t stages = g.k / (SPLIT ? 32 : 64);
+    int64_t parts = 1;
+    if (KIND != kUpdate) {
+        if (TILE == 64) while (stages > 16 && 2 * (parts + 1) * (parts + 1) <= stages) ++parts;
+        else parts = stages / 24;
+        if (parts > kNewtonSlabs / tiles) parts = kNewtonSlabs / tiles;
+    }
+    g.parts = parts > 1 ? (int32_t)parts : 1;
+    g.items = tiles * g.parts;
+    const dim3 grid((uint32_t)g.items);
+    if constexpr (KIND != kUpdate) {
+        if (g.parts > 1) {
+            hipLaunchKernelGGL((newton_small_kernel<TILE, false, true, SPLIT, KIND>), grid, dim3(256), 0, stream, g);
+            return;
+        }
+    }
+    if (g.items > kNewtonSlabs)
+        hipLaunchKernelGGL((newton_small_kernel<TILE, true, false, SPLIT, KIND>), grid, dim3(256), 0, stream, g);
+    else
+        hipLaunchKernelGGL((newton_small_kernel<TILE, false, false, SPLIT, KIND>), grid, dim3(256), 0, stream, g);
+}
+
+// Time of what follows the whole rounds of 256 x 256 tiles, in tiles' times: `rest` tiles and `edges` quarters of
+// the strips.  A quarter takes 0.36 of a tile's time.  Either the rest stays whole, with quarters on the
+// CUs it leaves, or it is taken in quarters too.
+double rest_kept(int64_t rest, int64_t edges, int64_t cus) {
+    const double beside = rest ? (double)(cus - rest) / 0.36 : 0.0;
+    const double more = (double)edges > beside ? ((double)edges - beside) / (double)cus : 0.0;
+    return (rest ? 1.0 : 0.0) + 0.36 * (double)(int64_t)(more + 0.999);
+}
+double rest_in_quarters(int64_t rest, int64_t edges, int64_t cus) { return 0.36 * (double)((4 * rest + edges + cus - 1) / cus); }
+
+// Estimated time of one step with tiles of 256 or 128, in K values of one 256 x 256 tile.  Two 128 x 128
+// tiles on a CU take 0.55 of its time, one alone 0.36.  The model puts 8 x 4096 x 2048 9% behind with 128
+// (measured: 10%), 16 x 700 x 2000 16% ahead (20%), 27 x 1352 x 1072 7% ahead (10%).
+double step_cost(int64_t batch, int64_t r, int64_t c, int tile) {
+    constexpr int64_t cus = 256;
+    const int64_t R = (r + 127) / 128, C = (c + 127) / 128;
+    auto cost = [&](int64_t big, int64_t edges, int64_t small) {
+        if (tile == 256) {
+            const int64_t rest = big % cus;
+            const double kept = rest_kept(rest, edges, cus), cut = rest_in_quarters(rest, edges, cus);
+            return (double)(big / cus) + (cut < kept ? cut : kept);
+        }
+        const int64_t rest = small % (2 * cus);
+        return 0.55 * (double)(small / (2 * cus)) + (rest > cus ? 0.55 : rest ? 0.36 : 0.0);
+    };
+    const int64_t r2 = R / 2, c2 = C / 2;
+    const double square = cost(batch * r2 * (r2 + 1) / 2, R % 2 ? batch * R : 0, batch * R * (R + 1) / 2);
+    const int64_t right = C % 2 ? R : 0;
+    const double update = cost(batch * r2 * c2, batch * (right + (R % 2 ? C - (right ? 1 : 0) : 0)), batch * R * C);
+    return square * (double)(c + r) + update * (double)r;
 }
 
 template <bool SPLIT, NewtonProduct KIND>
@@ -619,19 +791,20 @@ void launch_product(NewtonGemm g, int tile, int num_cus, hipStream_t stream) {
     g.tiles_m = (int32_t)(g.rows / tile);
     g.tiles_n = (int32_t)(g.cols / tile);
     const int tiles = g.batch * (KIND == kUpdate ? g.tiles_m * g.tiles_n : g.tiles_m * (g.tiles_m + 1) / 2);
+    g.parts = 1;
     if (tile == 256) {
-        // whole rounds of tiles on all CUs, then the rest as quarters when they fill two rounds at most
-        const int rest = tiles % num_cus;
-        g.whole = 2 * rest <= num_cus ? tiles - rest : tiles;
-        g.items = g.whole + 4 * (tiles - g.whole);
+        const int rows = (int)(g.rows / 128), cols = (int)(g.cols / 128);
+        const int right = KIND == kUpdate && cols % 2 ? rows : 0;
+        g.strips = right + (rows % 2 ? cols - (right ? 1 : 0) : 0);
+        g.tiles = tiles;
+        const int rest = tiles % num_cus, edges = g.batch * g.strips;
+        g.whole = rest_in_quarters(rest, edges, num_cus) < rest_kept(rest, edges, num_cus) ? tiles - rest : tiles;
+        g.items = g.whole + 4 * (tiles - g.whole) + edges;
         hipLaunchKernelGGL((newton_big_kernel<SPLIT, KIND>), dim3((uint32_t)g.items), dim3(64 * kBigWaves<SPLIT>), 0,
                            stream, g);
     } else {
-        g.items = g.whole = tiles;
-        if (tiles > num_cus)
-            hipLaunchKernelGGL((newton_small_kernel<5, SPLIT, KIND>), dim3((uint32_t)g.items), dim3(256), 0, stream, g);
-        else
-            hipLaunchKernelGGL((newton_small_kernel<10, SPLIT, KIND>), dim3((uint32_t)g.items), dim3(256), 0, stream, g);
+        if (tile == 128) launch_small<128, SPLIT, KIND>(g, tiles, stream);
+        else launch_small<64, SPLIT, KIND>(g, tiles, stream);
     }
 }
 
@@ -640,6 +813,8 @@ void launch_steps(const NewtonParams& p, const NewtonPlan& plan, const float* co
                   hipStream_t stream) {
     NewtonGemm g = {};
     g.batch = p.batch;
+    g.slabs = p.slabs;
+    g.arrived = p.arrived;
     g.num_xcds = num_xcds;
     g.rows = plan.r;
     g.m = p.m;
@@ -709,14 +884,18 @@ NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
         return plan;
     }
     plan.split = out_dtype != kOutBf16;
-    // 256 x 256 tiles where the update alone has one for every CU, else four times as many of 128 x 128
-    plan.tile = ((r + 255) / 256) * ((c + 255) / 256) * batch >= 256 ? 256 : 128;
-    plan.r = (r + plan.tile - 1) / plan.tile * plan.tile;
-    plan.c = (c + plan.tile - 1) / plan.tile * plan.tile;
+    // 256 x 256 tiles where the update alone has one for every CU, smaller ones where it has less
+    auto tiles = [&](int64_t edge) { return ((r + edge - 1) / edge) * ((c + edge - 1) / edge) * batch; };
+    plan.tile = tiles(128) < 256 ? 64 : r >= 256 && step_cost(batch, r, c, 256) < step_cost(batch, r, c, 128) ? 256 : 128;
+    const int64_t edge = plan.tile == 64 ? 64 : 128;    // an odd half tile at an end is taken in quarters
+    plan.r = (r + edge - 1) / edge * edge;
+    plan.c = (c + edge - 1) / edge * edge;
     plan.x_bytes = (size_t)batch * plan.r * plan.c * 4;
     plan.a_bytes = (size_t)batch * plan.r * plan.r * (plan.split ? 4 : 2);
     plan.b_bytes = plan.a_bytes;
-    plan.total = plan.parts_bytes + 2 * plan.x_bytes + plan.a_bytes + plan.b_bytes;
+    // sums of parts of K (kNewtonSlabs of them at most, one a workgroup) and their counters
+    plan.slab_bytes = plan.tile == 256 ? 0 : (size_t)kNewtonSlabs * (plan.tile * plan.tile * 4 + 4);
+    plan.total = plan.parts_bytes + 2 * plan.x_bytes + plan.a_bytes + plan.b_bytes + plan.slab_bytes;
     return plan;
 }
 

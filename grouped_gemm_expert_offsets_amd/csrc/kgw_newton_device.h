@@ -16,6 +16,31 @@ __device__ __forceinline__ f32x16 mfma_f16_32x32x16(i32x4 a, i32x4 b, f32x16 c) 
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// Two floats as two halves, rounded to nearest even by one instruction (v_cvt_pk_f16_f32).
+__device__ __forceinline__ uint32_t to_halves(float lo, float hi) {
+    typedef __attribute__((ext_vector_type(2))) float f2;
+    typedef __attribute__((ext_vector_type(2))) _Float16 h2;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{lo, hi}), h2));
+}
+
+// x as it is in fp32: the compiler does not take its last operation together with what follows (a product and its
+// conversion to half as one rounding), so that a value does not depend on the code around it.
+__device__ __forceinline__ float as_fp32(float x) {
+    asm("" : "+v"(x));
+    return x;
+}
+
+// Two values as their halves and the halves of what is left of them.
+struct HalfPair {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ HalfPair split_pair(float a, float b) {
+    HalfPair p;
+    p.hi = to_halves(a, b);
+    p.lo = to_halves(a - f16_lo(p.hi), b - f16_hi(p.hi));
+    return p;
+}
+
 __device__ __forceinline__ float half_bits(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
 
 // f(0), f(1), .. f(N - 1) with compile-time arguments: register arrays indexed by them stay in registers.

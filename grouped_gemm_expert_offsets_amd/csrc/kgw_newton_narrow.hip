@@ -1,7 +1,8 @@
 // Newton-Schulz orthogonalisation of matrices whose short side is at most 128 (gfx950).
 //
-// Such a matrix has so little work that launches and the way through memory decide its time, so a
-// step is one launch: every workgroup holds all r rows of its columns, squares the r x r matrix A = X X^T for itself
+// Such a matrix has so little work that launches and the way through memory decide its time.  Where the
+// iterate fits into one workgroup's LDS (64 x 512 or 128 x 128), one launch runs everything, the norm
+// included (narrow_whole_kernel).  Longer ones take a launch a step: every workgroup holds all r rows of its columns, squares the r x r matrix A = X X^T for itself
 // (128^3 products, 1.3 us), updates its columns and adds up their part of the next A:
 //
 //     A = sum of the parts;  B = b A + c A A;  X <- a X + B X;  part = X X^T over the own columns
@@ -43,12 +44,18 @@ struct NarrowParams {
     float x_scale, linear;  // X = x_scale * (B X + linear * X)
 };
 
+// The scales of every step, for the kernel that runs all of them.
+struct NarrowSteps {
+    float b_scale[kNewtonMaxSteps], b_linear[kNewtonMaxSteps], linear[kNewtonMaxSteps];
+};
+
 // 8 sums of one lane -> its 16 bytes of a fragment, high and low plane.
 __device__ __forceinline__ void split_eight(const float (&v)[8], i32x4& hi, i32x4& lo) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        hi[u] = (int)pack_f16x2(v[2 * u], v[2 * u + 1]);
-        lo[u] = (int)pack_f16x2(v[2 * u] - f16_lo((uint32_t)hi[u]), v[2 * u + 1] - f16_hi((uint32_t)hi[u]));
+        const HalfPair p = split_pair(v[2 * u], v[2 * u + 1]);
+        hi[u] = (int)p.hi;
+        lo[u] = (int)p.lo;
     }
 }
 
@@ -66,28 +73,48 @@ struct Narrow {
     static __device__ __forceinline__ uint32_t a_at(int k, int rows, int plane) { return x_at(k, rows, plane); }
 };
 
-// sums += three products of the fragments (hi, lo) x (hi, lo).
-__device__ __forceinline__ f32x16 mfma3(i32x4 ah, i32x4 al, i32x4 bh, i32x4 bl, f32x16 c) {
-    c = mfma_f16_32x32x16(ah, bl, c);
-    c = mfma_f16_32x32x16(al, bh, c);
-    return mfma_f16_32x32x16(ah, bh, c);
+// acc[j] += col[j] x row over K slices of 16, each operand as three products of its planes, col (ROW_FIRST: row) down
+// the registers and the other one over the lanes; read(k, f) reads the fragments of slice k.  The next slice is read under the products of this one, and the products go over
+// all of acc in turn, so that no product waits for a read or for the one just before it.
+template <int COLS>
+struct Slice {
+    i32x4 row[2], col[COLS][2];                         // high and low plane
+};
+template <int SLICES_OF_K, bool ROW_FIRST, int COLS, class Read>
+__device__ __forceinline__ void multiply(f32x16 (&acc)[COLS], Read read) {
+    Slice<COLS> f[2];
+    auto product = [&](const Slice<COLS>& g, int j, int col_plane, int row_plane) __attribute__((always_inline)) {
+        const i32x4 c = g.col[j][col_plane], r = g.row[row_plane];
+        acc[j] = ROW_FIRST ? mfma_f16_32x32x16(r, c, acc[j]) : mfma_f16_32x32x16(c, r, acc[j]);
+    };
+    read(std::integral_constant<int, 0>{}, f[0]);
+    each<SLICES_OF_K>([&](auto k) __attribute__((always_inline)) {
+        if constexpr (k + 1 < SLICES_OF_K) read(std::integral_constant<int, k + 1>{}, f[(k + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        const Slice<COLS>& g = f[k & 1];
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) product(g, j, 0, 1);
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) product(g, j, 1, 0);
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) product(g, j, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    });
 }
 
-// Adds this wave's blocks of X X^T over a chunk in LDS to acc.
-template <int RB>
-__device__ __forceinline__ void add_gram(const lds_char* x, int wave, int lane, f32x16 (&acc)[Narrow<RB>::MINE]) {
+// Adds this wave's blocks of M M^T to acc: the rows block over the lanes, columns blocks down the registers.
+template <int RB, int SLICES_OF_K>
+__device__ __forceinline__ void add_gram(const lds_char* m, int wave, int lane, f32x16 (&acc)[Narrow<RB>::MINE]) {
     using N = Narrow<RB>;
+    multiply<SLICES_OF_K, false>(acc, [&](auto k, Slice<N::MINE>& f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < SLICES; ++k) {
-        const i32x4 rh = lds_load_16B(x, N::x_at(k, N::row_of(wave, 0), 0) + lane * 16u);
-        const i32x4 rl = lds_load_16B(x, N::x_at(k, N::row_of(wave, 0), 1) + lane * 16u);
+        for (int plane = 0; plane < 2; ++plane) {
+            f.row[plane] = lds_load_16B(m, N::x_at(k, N::row_of(wave, 0), plane) + lane * 16u);
 #pragma unroll
-        for (int j = 0; j < N::MINE; ++j) {
-            const i32x4 ch = lds_load_16B(x, N::x_at(k, N::col_of(wave, j), 0) + lane * 16u);
-            const i32x4 cl = lds_load_16B(x, N::x_at(k, N::col_of(wave, j), 1) + lane * 16u);
-            acc[j] = mfma3(ch, cl, rh, rl, acc[j]);     // columns block down the registers, rows over the lanes
+            for (int j = 0; j < N::MINE; ++j)
+                f.col[j][plane] = lds_load_16B(m, N::x_at(k, N::col_of(wave, j), plane) + lane * 16u);
         }
-    }
+    });
 }
 
 template <int RB>
@@ -105,6 +132,195 @@ __device__ __forceinline__ void store_part(const NarrowParams& q, int b, int gro
     }
 }
 
+template <int N>
+__device__ __forceinline__ void clear(f32x16 (&m)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m[j][e] = 0.0f;
+}
+
+// One chunk of the first iterate into LDS.
+template <int RB, int DT>
+__device__ __forceinline__ void first_chunk(const NarrowParams& q, int b, int chunk, float scale, lds_char* x, int tid) {
+    using N = Narrow<RB>;
+    const int64_t n0 = (int64_t)chunk * CHUNK;
+    if (!q.tall) {
+        // eight consecutive columns of one row: two runs of four, for the two lane halves
+        for (int i = tid; i < 32 * RB * (CHUNK / 8); i += NT) {
+            const int row = i / (CHUNK / 8), c8 = i % (CHUNK / 8);
+            float v[8];
+            load_eight<DT>(q.p, b, row, n0 + 8 * c8, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = as_fp32(v[e] * scale);
+            i32x4 hi, lo;
+            split_eight(v, hi, lo);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int plane = 0; plane < 2; ++plane) {
+                    const i32x4 w = plane ? lo : hi;
+                    const i32x2 half = {w[2 * h], w[2 * h + 1]};
+                    const uint32_t at = N::x_at(c8 >> 1, row >> 5, plane) + (uint32_t)(32 * h + (row & 31)) * 16u +
+                                        (uint32_t)(c8 & 1) * 8u;
+                    *reinterpret_cast<__attribute__((address_space(3))) i32x2*>(x + at) = half;
+                }
+        }
+    } else {
+        // G is (c, r): eight consecutive rows of the iterate in one of its columns
+        for (int i = tid; i < CHUNK * 4 * RB; i += NT) {
+            const int col = i / (4 * RB), r8 = i % (4 * RB);
+            float v[8];
+            load_eight<DT>(q.p, b, n0 + col, 8 * r8, v);
+            const int in = col & 15;                         // column 4 h + 8 s + t: half h, run s, place t
+            const uint32_t place = (uint32_t)((in >> 2) & 1) * 512u + (uint32_t)(in >> 3) * 8u + (uint32_t)(in & 3) * 2u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int row = 8 * r8 + e;
+                const HalfPair u = split_pair(as_fp32(v[e] * scale), 0.0f);
+                const uint32_t at = place + (uint32_t)(row & 31) * 16u;
+                *reinterpret_cast<__attribute__((address_space(3))) uint16_t*>(x + N::x_at(col >> 4, row >> 5, 0) + at) = (uint16_t)u.hi;
+                *reinterpret_cast<__attribute__((address_space(3))) uint16_t*>(x + N::x_at(col >> 4, row >> 5, 1) + at) = (uint16_t)u.lo;
+            }
+        }
+    }
+}
+
+// This wave's blocks of an r x r matrix as fragments into LDS: rows over the lanes, K = columns.
+template <int RB>
+__device__ __forceinline__ void write_blocks(lds_char* a, int wave, int lane, const f32x16 (&m)[Narrow<RB>::MINE]) {
+    using N = Narrow<RB>;
+#pragma unroll
+    for (int j = 0; j < N::MINE; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = m[j][8 * s + e];
+            i32x4 hi, lo;
+            split_eight(v, hi, lo);
+            const int k = 2 * N::col_of(wave, j) + s, rows = N::row_of(wave, j);
+            lds_store_16B(a, N::a_at(k, rows, 0) + lane * 16u, hi);
+            lds_store_16B(a, N::a_at(k, rows, 1) + lane * 16u, lo);
+        }
+}
+
+// B = b_scale (A A + b_linear A) as fragments in LDS, from the blocks of sums / a_scale that each wave has.
+// The caller's barriers: no one reads `a` any more before, all have written it after.
+template <int RB>
+__device__ __forceinline__ void make_b(const NarrowParams& q, lds_char* a, int wave, int lane,
+                                       f32x16 (&mine)[Narrow<RB>::MINE]) {
+    using N = Narrow<RB>;
+#pragma unroll
+    for (int j = 0; j < N::MINE; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mine[j][e] *= q.a_scale;
+    write_blocks<RB>(a, wave, lane, mine);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N::MINE; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mine[j][e] *= q.b_linear;
+    add_gram<RB, 2 * RB>(a, wave, lane, mine);
+#pragma unroll
+    for (int j = 0; j < N::MINE; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mine[j][e] *= q.b_scale;
+    __syncthreads();
+    write_blocks<RB>(a, wave, lane, mine);
+}
+
+// acc = x_scale (B X + linear X) in this wave's 32 columns of a chunk: columns down the registers, rows
+// over the lanes.
+template <int RB>
+__device__ __forceinline__ void update_chunk(const NarrowParams& q, const lds_char* x, const lds_char* a, int wave, int lane,
+                                             float x_scale, f32x16 (&acc)[RB]) {
+    using N = Narrow<RB>;
+    const int g16 = lane >> 4, i16 = lane & 15;
+    clear(acc);
+    // row: 32 columns of X; col: the rows blocks of B
+    multiply<2 * RB, true>(acc, [&](auto k, Slice<RB>& f) __attribute__((always_inline)) {
+        // Transposed fragment of rows 16 k .. of X: 16 lanes read 4 rows x 16 columns, of which
+        // piece c (4 columns) of a row is half c & 1, run c >> 1 of its place in the image.
+#pragma unroll
+        for (int plane = 0; plane < 2; ++plane) {
+            const int slice = 2 * wave + (g16 & 1), c = i16 & 3;
+            const int row = 16 * k + 4 * (g16 >> 1) + (i16 >> 2);
+            const uint32_t at = N::x_at(slice, 0, plane) + (uint32_t)(k >> 1) * 2048u + (uint32_t)(c & 1) * 512u +
+                                (uint32_t)(row & 31) * 16u + (uint32_t)(c >> 1) * 8u;
+            const i16x4 v0 = lds_read_tr16(x, at);
+            const i16x4 v1 = lds_read_tr16(x, at + 8 * 16);
+            const i16x8 v = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+            f.row[plane] = __builtin_bit_cast(i32x4, v);
+#pragma unroll
+            for (int i = 0; i < RB; ++i) f.col[i][plane] = lds_load_16B(a, N::a_at(k, i, plane) + lane * 16u);
+        }
+    });
+    // a X from the same image, added last: it decides the small singular values
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const i32x4 hi = lds_load_16B(x, N::x_at(2 * wave + s, i, 0) + lane * 16u);
+            const i32x4 lo = lds_load_16B(x, N::x_at(2 * wave + s, i, 1) + lane * 16u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float x0 = acc[i][8 * s + 2 * u] + q.linear * f16_lo((uint32_t)lo[u]);
+                const float x1 = acc[i][8 * s + 2 * u + 1] + q.linear * f16_hi((uint32_t)lo[u]);
+                acc[i][8 * s + 2 * u] = x_scale * (x0 + q.linear * f16_lo((uint32_t)hi[u]));
+                acc[i][8 * s + 2 * u + 1] = x_scale * (x1 + q.linear * f16_hi((uint32_t)hi[u]));
+            }
+        }
+}
+
+// This wave's part of the next iterate into the image, and to `to` where that is not NULL.
+template <int RB>
+__device__ __forceinline__ void store_chunk(lds_char* x, char* to, int wave, int lane, const f32x16 (&acc)[RB]) {
+    using N = Narrow<RB>;
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = acc[i][8 * s + e];
+            i32x4 hi, lo;
+            split_eight(v, hi, lo);
+            const uint32_t at = N::x_at(2 * wave + s, i, 0) + lane * 16u;
+            lds_store_16B(x, at, hi);
+            lds_store_16B(x, at + 1024u, lo);
+            if (to) {
+                *(gbl_i32x4*)(to + at) = hi;
+                *(gbl_i32x4*)(to + at + 1024u) = lo;
+            }
+        }
+}
+
+template <int RB>
+__device__ __forceinline__ void store_result(const NarrowParams& q, int b, int chunk, int wave, int lane,
+                                             const f32x16 (&acc)[RB]) {
+    // at most 128 x 2^20 elements a matrix: 32-bit offsets
+    const int r = (int)(q.tall ? q.p.n : q.p.m), c = (int)(q.tall ? q.p.m : q.p.n), ld = (int)q.p.n;
+    const int row_step = q.tall ? 1 : ld, col_step = q.tall ? ld : 1;
+    const int c0 = chunk * CHUNK + 32 * wave + 4 * (lane >> 5);
+    const int at0 = (lane & 31) * row_step + c0 * col_step;
+    char* const out = (char*)q.p.out + (int64_t)b * q.p.m * q.p.n * (q.p.out_dtype == kOutF32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+        if (32 * i + (lane & 31) >= r) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (c0 + 8 * g + t >= c) continue;
+                const int at = at0 + 32 * i * row_step + (8 * g + t) * col_step;
+                const float v = acc[i][4 * g + t];
+                if (q.p.out_dtype == kOutF32) ((float*)out)[at] = v;
+                else ((uint16_t*)out)[at] = (uint16_t)(q.p.out_dtype == kOutBf16 ? pack_bf16x2(v, 0.0f) : to_halves(v, 0.0f));
+            }
+    }
+}
+
 // The first iterate's chunks and their parts of A.
 template <int RB, int DT>
 __global__ __launch_bounds__(NT, 1) void narrow_first_kernel(NarrowParams q) {
@@ -115,62 +331,18 @@ __global__ __launch_bounds__(NT, 1) void narrow_first_kernel(NarrowParams q) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int b = blockIdx.y, group = blockIdx.x;
     const float scale = first_scale(q.p, b);
-    f32x16 acc[N::MINE];
-#pragma unroll
-    for (int j = 0; j < N::MINE; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[j][e] = 0.0f;
+    f32x16 part[N::MINE];
+    clear(part);
     const int first = group * q.per_group, last = min(q.chunks, first + q.per_group);
     for (int chunk = first; chunk < last; ++chunk) {
-        const int64_t n0 = (int64_t)chunk * CHUNK;
         __syncthreads();
-        if (!q.tall) {
-            // eight consecutive columns of one row: two runs of four, for the two lane halves
-            for (int i = tid; i < 32 * RB * (CHUNK / 8); i += NT) {
-                const int row = i / (CHUNK / 8), c8 = i % (CHUNK / 8);
-                float v[8];
-                load_eight<DT>(q.p, b, row, n0 + 8 * c8, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= scale;
-                i32x4 hi, lo;
-                split_eight(v, hi, lo);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int plane = 0; plane < 2; ++plane) {
-                        const i32x4 w = plane ? lo : hi;
-                        const i32x2 half = {w[2 * h], w[2 * h + 1]};
-                        const uint32_t at = N::x_at(c8 >> 1, row >> 5, plane) + (uint32_t)(32 * h + (row & 31)) * 16u +
-                                            (uint32_t)(c8 & 1) * 8u;
-                        *reinterpret_cast<__attribute__((address_space(3))) i32x2*>(x + at) = half;
-                    }
-            }
-        } else {
-            // G is (c, r): eight consecutive rows of the iterate in one of its columns
-            for (int i = tid; i < CHUNK * 4 * RB; i += NT) {
-                const int col = i / (4 * RB), r8 = i % (4 * RB);
-                float v[8];
-                load_eight<DT>(q.p, b, n0 + col, 8 * r8, v);
-                const int in = col & 15;                         // column 4 h + 8 s + t: half h, run s, place t
-                const uint32_t place = (uint32_t)((in >> 2) & 1) * 512u + (uint32_t)(in >> 3) * 8u + (uint32_t)(in & 3) * 2u;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int row = 8 * r8 + e;
-                    const float u = v[e] * scale;
-                    const uint32_t hi = pack_f16x2(u, 0.0f);
-                    const uint32_t lo = pack_f16x2(u - f16_lo(hi), 0.0f);
-                    const uint32_t at = place + (uint32_t)(row & 31) * 16u;
-                    *reinterpret_cast<__attribute__((address_space(3))) uint16_t*>(x + N::x_at(col >> 4, row >> 5, 0) + at) = (uint16_t)hi;
-                    *reinterpret_cast<__attribute__((address_space(3))) uint16_t*>(x + N::x_at(col >> 4, row >> 5, 1) + at) = (uint16_t)lo;
-                }
-            }
-        }
+        first_chunk<RB, DT>(q, b, chunk, scale, x, tid);
         __syncthreads();
         char* const to = q.x_out + ((int64_t)b * q.chunks + chunk) * N::X_BYTES;
         for (uint32_t i = tid * 16u; i < N::X_BYTES; i += NT * 16u) *(gbl_i32x4*)(to + i) = lds_load_16B(x, i);
-        add_gram<RB>(x, wave, lane, acc);
+        add_gram<RB, SLICES>(x, wave, lane, part);
     }
-    store_part<RB>(q, b, group, wave, lane, acc);
+    store_part<RB>(q, b, group, wave, lane, part);
 }
 
 // One step.  LAST: the result instead of the next iterate and its part of A.
@@ -183,7 +355,6 @@ __global__ __launch_bounds__(NT, 1) void narrow_step_kernel(NarrowParams q) {
     const uint32_t x_addr = lds_addr(smem);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l32 = lane & 31, lhi = lane >> 5, g16 = lane >> 4, i16 = lane & 15;
     const int b = blockIdx.y, group = blockIdx.x;
     const int first = group * q.per_group, last = min(q.chunks, first + q.per_group);
 
@@ -199,161 +370,37 @@ __global__ __launch_bounds__(NT, 1) void narrow_step_kernel(NarrowParams q) {
 
     // A: this wave's blocks, added up in the order of the parts
     f32x16 mine[N::MINE];
-    {
-        const float* from = q.parts_in + (int64_t)b * q.groups_in * (RB * RB * 1024);
-#pragma unroll
-        for (int j = 0; j < N::MINE; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) mine[j][e] = 0.0f;
-        for (int w = 0; w < q.groups_in; ++w, from += RB * RB * 1024) {
-#pragma unroll
-            for (int j = 0; j < N::MINE; ++j) {
-                const int block = N::row_of(wave, j) * RB + N::col_of(wave, j);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x4 v = *(const gbl_f32x4*)(from + block * 1024 + g * 256 + lane * 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mine[j][4 * g + e] += v[e];
-                }
-            }
-        }
-    }
-    // Blocks of an r x r matrix as fragments into LDS: rows over the lanes, K = columns.
-    auto write_blocks = [&](const f32x16 (&m)[N::MINE]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < N::MINE; ++j)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = m[j][8 * s + e];
-                i32x4 hi, lo;
-                split_eight(v, hi, lo);
-                const int k = 2 * N::col_of(wave, j) + s, rows = N::row_of(wave, j);
-                lds_store_16B(a, N::a_at(k, rows, 0) + lane * 16u, hi);
-                lds_store_16B(a, N::a_at(k, rows, 1) + lane * 16u, lo);
-            }
-    };
-#pragma unroll
-    for (int j = 0; j < N::MINE; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mine[j][e] *= q.a_scale;
-    write_blocks(mine);
-    __syncthreads();
-    // B = b_scale (A A + b_linear A)
-    f32x16 square[N::MINE];
-#pragma unroll
-    for (int j = 0; j < N::MINE; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) square[j][e] = q.b_linear * mine[j][e];
-#pragma unroll
-    for (int k = 0; k < 2 * RB; ++k) {
-        const i32x4 rh = lds_load_16B(a, N::a_at(k, N::row_of(wave, 0), 0) + lane * 16u);
-        const i32x4 rl = lds_load_16B(a, N::a_at(k, N::row_of(wave, 0), 1) + lane * 16u);
+    clear(mine);
+    const float* from = q.parts_in + (int64_t)b * q.groups_in * (RB * RB * 1024);
+    for (int w = 0; w < q.groups_in; ++w, from += RB * RB * 1024) {
 #pragma unroll
         for (int j = 0; j < N::MINE; ++j) {
-            const i32x4 ch = lds_load_16B(a, N::a_at(k, N::col_of(wave, j), 0) + lane * 16u);
-            const i32x4 cl = lds_load_16B(a, N::a_at(k, N::col_of(wave, j), 1) + lane * 16u);
-            square[j] = mfma3(ch, cl, rh, rl, square[j]);
+            const int block = N::row_of(wave, j) * RB + N::col_of(wave, j);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 v = *(const gbl_f32x4*)(from + block * 1024 + g * 256 + lane * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[j][4 * g + e] += v[e];
+            }
         }
     }
-#pragma unroll
-    for (int j = 0; j < N::MINE; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) square[j][e] *= q.b_scale;
-    __syncthreads();
-    write_blocks(square);
+    make_b<RB>(q, a, wave, lane, mine);
 
     f32x16 part[N::MINE];
-#pragma unroll
-    for (int j = 0; j < N::MINE; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) part[j][e] = 0.0f;
+    clear(part);
     for (int chunk = first; chunk < last; ++chunk) {
         wait_vmcnt<0>();
         __syncthreads();                                // the chunk and B are in LDS
-        // this wave's 32 columns: rows of X over K, columns down the registers, rows of the result over the lanes
         f32x16 acc[RB];
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][e] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 2 * RB; ++k) {
-            // Transposed fragment of rows 16 k .. of X: 16 lanes read 4 rows x 16 columns, of which
-            // piece c (4 columns) of a row is half c & 1, run c >> 1 of its place in the image.
-            i32x4 xt[2];
-#pragma unroll
-            for (int plane = 0; plane < 2; ++plane) {
-                const int slice = 2 * wave + (g16 & 1), c = i16 & 3;
-                const int row = 16 * k + 4 * (g16 >> 1) + (i16 >> 2);
-                const uint32_t at = N::x_at(slice, 0, plane) + (uint32_t)(k >> 1) * 2048u + (uint32_t)(c & 1) * 512u +
-                                    (uint32_t)(row & 31) * 16u + (uint32_t)(c >> 1) * 8u;
-                const i16x4 v0 = lds_read_tr16(x, at);
-                const i16x4 v1 = lds_read_tr16(x, at + 8 * 16);
-                const i16x8 v = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-                xt[plane] = __builtin_bit_cast(i32x4, v);
-            }
-#pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const i32x4 bh = lds_load_16B(a, N::a_at(k, i, 0) + lane * 16u);
-                const i32x4 bl = lds_load_16B(a, N::a_at(k, i, 1) + lane * 16u);
-                acc[i] = mfma3(xt[0], xt[1], bh, bl, acc[i]);
-            }
-        }
-        // a X from the same image, added last: it decides the small singular values
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const i32x4 hi = lds_load_16B(x, N::x_at(2 * wave + s, i, 0) + lane * 16u);
-                const i32x4 lo = lds_load_16B(x, N::x_at(2 * wave + s, i, 1) + lane * 16u);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    acc[i][8 * s + 2 * u] = q.x_scale * (acc[i][8 * s + 2 * u] + q.linear * (f16_lo((uint32_t)hi[u]) + f16_lo((uint32_t)lo[u])));
-                    acc[i][8 * s + 2 * u + 1] = q.x_scale * (acc[i][8 * s + 2 * u + 1] + q.linear * (f16_hi((uint32_t)hi[u]) + f16_hi((uint32_t)lo[u])));
-                }
-            }
+        update_chunk<RB>(q, x, a, wave, lane, q.x_scale, acc);
         __syncthreads();                                // all have read the chunk
         if constexpr (LAST) {
             if (chunk + 1 < last) load_chunk(chunk + 1);
-            const int64_t c0 = (int64_t)chunk * CHUNK + 32 * wave + 4 * lhi;
-#pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const int64_t row = 32 * i + l32;
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int64_t col = c0 + 8 * g + t;
-                        const int64_t gr = q.tall ? col : row, gc = q.tall ? row : col;
-                        if (gr >= q.p.m || gc >= q.p.n) continue;
-                        const int64_t at = ((int64_t)b * q.p.m + gr) * q.p.n + gc;
-                        const float v = acc[i][4 * g + t];
-                        if (q.p.out_dtype == kOutF32) ((float*)q.p.out)[at] = v;
-                        else if (q.p.out_dtype == kOutBf16) ((uint16_t*)q.p.out)[at] = (uint16_t)pack_bf16x2(v, 0.0f);
-                        else ((uint16_t*)q.p.out)[at] = (uint16_t)pack_f16x2(v, 0.0f);
-                    }
-            }
+            store_result<RB>(q, b, chunk, wave, lane, acc);
         } else {
-            char* const to = q.x_out + ((int64_t)b * q.chunks + chunk) * N::X_BYTES;
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = acc[i][8 * s + e];
-                    i32x4 hi, lo;
-                    split_eight(v, hi, lo);
-                    const uint32_t at = N::x_at(2 * wave + s, i, 0) + lane * 16u;
-                    lds_store_16B(x, at, hi);
-                    lds_store_16B(x, at + 1024u, lo);
-                    *(gbl_i32x4*)(to + at) = hi;
-                    *(gbl_i32x4*)(to + at + 1024u) = lo;
-                }
+            store_chunk<RB>(x, q.x_out + ((int64_t)b * q.chunks + chunk) * N::X_BYTES, wave, lane, acc);
             __syncthreads();
-            add_gram<RB>(x, wave, lane, part);
+            add_gram<RB, SLICES>(x, wave, lane, part);
             if (chunk + 1 < last) {
                 __syncthreads();                        // all have read the image
                 load_chunk(chunk + 1);
@@ -361,6 +408,67 @@ __global__ __launch_bounds__(NT, 1) void narrow_step_kernel(NarrowParams q) {
         }
     }
     if constexpr (!LAST) store_part<RB>(q, b, group, wave, lane, part);
+}
+
+// Short matrices, all steps of one in one workgroup: its iterate stays in LDS.
+template <int RB>
+constexpr int kWholeChunks = RB == 2 ? 4 : 1;
+
+template <int RB, int DT>
+__global__ __launch_bounds__(NT, 1) void narrow_whole_kernel(NarrowParams q, NarrowSteps steps) {
+    using N = Narrow<RB>;
+    __shared__ __attribute__((aligned(1024))) char smem[kWholeChunks<RB> * N::X_BYTES + N::A_BYTES];
+    __shared__ double sums[NT / 64];
+    lds_char* const x = (lds_char*)smem;
+    lds_char* const a = x + kWholeChunks<RB> * N::X_BYTES;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int b = blockIdx.x;
+    // |G|_F, in 64 bits as in newton_norm_kernel
+    const int per_row = (int)((q.p.n + 7) / 8);
+    double s = 0.0;
+    for (int i = tid; i < (int)q.p.m * per_row; i += NT) {
+        const int row = i / per_row;
+        float v[8];
+        load_eight<DT>(q.p, b, row, 8 * (i - row * per_row), v);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += (double)v[u] * (double)v[u];
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    if (lane == 0) sums[wave] = s;
+    __syncthreads();
+    const double norm = __builtin_sqrt((sums[0] + sums[1]) + (sums[2] + sums[3]));
+    const float scale = (float)((double)kXScale / (norm + (double)q.p.eps));
+
+    f32x16 mine[N::MINE];
+    for (int chunk = 0; chunk < q.chunks; ++chunk) first_chunk<RB, DT>(q, b, chunk, scale, x + chunk * N::X_BYTES, tid);
+    __syncthreads();
+    clear(mine);
+    for (int chunk = 0; chunk < q.chunks; ++chunk) add_gram<RB, SLICES>(x + chunk * N::X_BYTES, wave, lane, mine);
+    for (int step = 0; step < q.p.steps; ++step) {
+        q.b_scale = steps.b_scale[step];
+        q.b_linear = steps.b_linear[step];
+        q.linear = steps.linear[step];
+        const bool last = step + 1 == q.p.steps;
+        make_b<RB>(q, a, wave, lane, mine);
+        __syncthreads();
+        clear(mine);
+        for (int chunk = 0; chunk < q.chunks; ++chunk) {
+            lds_char* const at = x + chunk * N::X_BYTES;
+            f32x16 acc[RB];
+            update_chunk<RB>(q, at, a, wave, lane, (last ? 1.0f / kXScale : 1.0f) / kBScale, acc);
+            if (last) {
+                store_result<RB>(q, b, chunk, wave, lane, acc);
+                continue;
+            }
+            __syncthreads();                            // all have read the chunk
+            store_chunk<RB>(at, nullptr, wave, lane, acc);
+            __syncthreads();
+            add_gram<RB, SLICES>(at, wave, lane, mine);
+        }
+        __syncthreads();                                // all have read B
+    }
 }
 
 // Adds up many parts of A, in their order: 16 bytes a thread.
@@ -387,6 +495,22 @@ void launch(const NewtonParams& p, const NewtonPlan& plan, const float* co, hipS
     q.chunks = plan.chunks;
     q.per_group = plan.per_group;
     q.tall = plan.tall ? 1 : 0;
+    q.a_scale = kAScale / (kXScale * kXScale);
+    NarrowSteps steps;
+    for (int s = 0; s < p.steps; ++s) {
+        const float c = newton_c(co + 3 * s);
+        steps.b_scale[s] = c * (kBScale / (kAScale * kAScale));
+        steps.b_linear[s] = c != 0.0f ? co[3 * s + 1] / c * kAScale : 0.0f;
+        steps.linear[s] = co[3 * s] * kBScale;
+    }
+    if (plan.groups == 0) {
+        const dim3 all((uint32_t)p.batch);
+        if (p.dtype == kOutBf16) hipLaunchKernelGGL((narrow_whole_kernel<RB, kOutBf16>), all, dim3(NT), 0, stream, q, steps);
+        else if (p.dtype == kOutF16) hipLaunchKernelGGL((narrow_whole_kernel<RB, kOutF16>), all, dim3(NT), 0, stream, q, steps);
+        else hipLaunchKernelGGL((narrow_whole_kernel<RB, kOutF32>), all, dim3(NT), 0, stream, q, steps);
+        return;
+    }
+    launch_newton_norm(p, stream);
     q.x_out = p.x[0];
     q.parts_out = (float*)p.a;
     if (p.dtype == kOutBf16) hipLaunchKernelGGL((narrow_first_kernel<RB, kOutBf16>), grid, dim3(NT), 0, stream, q);
@@ -405,14 +529,12 @@ void launch(const NewtonParams& p, const NewtonPlan& plan, const float* co, hipS
             q.parts_in = (const float*)p.b;
             q.groups_in = 1;
         }
-        const float c = newton_c(co + 3 * s);
         q.x_in = p.x[s & 1];
         q.x_out = p.x[(s + 1) & 1];
-        q.a_scale = kAScale / (kXScale * kXScale);
-        q.b_scale = c * (kBScale / (kAScale * kAScale));
-        q.b_linear = c != 0.0f ? co[3 * s + 1] / c * kAScale : 0.0f;
+        q.b_scale = steps.b_scale[s];
+        q.b_linear = steps.b_linear[s];
+        q.linear = steps.linear[s];
         q.x_scale = (last ? 1.0f / kXScale : 1.0f) / kBScale;
-        q.linear = co[3 * s] * kBScale;
         if (last) hipLaunchKernelGGL((narrow_step_kernel<RB, true>), grid, dim3(NT), 0, stream, q);
         else hipLaunchKernelGGL((narrow_step_kernel<RB, false>), grid, dim3(NT), 0, stream, q);
     }
@@ -427,6 +549,10 @@ void newton_narrow_plan(int32_t batch, int64_t r, int64_t c, NewtonPlan* plan) {
     plan->r = 32 * rb;
     plan->chunks = (int32_t)((c + CHUNK - 1) / CHUNK);
     plan->c = (int64_t)plan->chunks * CHUNK;
+    if (plan->chunks <= (rb == 2 ? kWholeChunks<2> : kWholeChunks<4>)) {
+        plan->total = 256;                               // everything in LDS; a workspace is asked for all the same
+        return;
+    }
     // a workgroup of one chunk each until they are two rounds of the chip's 256 compute units
     const int64_t total = (int64_t)plan->chunks * batch;
     plan->per_group = (int32_t)(total <= 512 ? 1 : (total + 511) / 512);
@@ -438,7 +564,6 @@ void newton_narrow_plan(int32_t batch, int64_t r, int64_t c, NewtonPlan* plan) {
 }
 
 void launch_newton_narrow(const NewtonParams& p, const NewtonPlan& plan, const float* coefficients, hipStream_t stream) {
-    launch_newton_norm(p, stream);
     if (plan.r == 64) launch<2>(p, plan, coefficients, stream);
     else launch<4>(p, plan, coefficients, stream);
 }

@@ -33,7 +33,7 @@ def test_arguments(lib):
     assert call(lib, ld=63) == INVALID and call(lib, stride=-1) == INVALID
     assert call(lib, G=P + 2) == MISALIGNED and call(lib, dt=1, G=P + 1) == MISALIGNED
     assert call(lib, out=P + 2) == MISALIGNED and call(lib, ws=P + 128) == MISALIGNED
-    assert call(lib, ws_bytes=1000) == INVALID
+    assert call(lib, ws_bytes=100) == INVALID and call(lib, m=200, n=300, ld=300, ws_bytes=100000) == INVALID
     for empty in (dict(batch=0), dict(m=0), dict(n=0)):
         assert call(lib, G=None, out=None, ws=None, **empty) == kgw.KGW_SUCCESS
 

@@ -18,7 +18,7 @@ kgw_status_t usable_device() {
 int element_size(int32_t dtype) { return dtype == KGW_OUT_FP32 ? 4 : 2; }
 
 // One wave or workgroup per item: HIP counts a grid's threads in 32 bits.
-constexpr int64_t kMaxRowItems = (int64_t)1 << 24;
+constexpr int64_t kMaxRowItems = (int64_t)1 << 23;
 
 // Checks shared by the calls that move rows.  `in` is (tokens, hidden) or (rows, hidden).
 kgw_status_t check_rows(int32_t dtype, int64_t tokens, int32_t topk, int64_t rows, int64_t hidden) {
@@ -27,7 +27,7 @@ kgw_status_t check_rows(int32_t dtype, int64_t tokens, int32_t topk, int64_t row
     if (topk > 65536 || tokens * (int64_t)topk > INT32_MAX || rows > INT32_MAX) return KGW_ERROR_UNSUPPORTED;
     if (hidden >= ((int64_t)1 << 28)) return KGW_ERROR_UNSUPPORTED;
     const int64_t segments = hidden * element_size(dtype) / 2048 + 1;     // at most this many waves a row
-    if (tokens > kMaxRowItems || tokens * segments + rows / 16 >= 2 * kMaxRowItems) return KGW_ERROR_UNSUPPORTED;
+    if (tokens > kMaxRowItems || tokens * segments + rows / 4 >= 3 * kMaxRowItems) return KGW_ERROR_UNSUPPORTED;
     return KGW_SUCCESS;
 }
 

@@ -207,11 +207,12 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(MoeSortParams p) {
 // ----------------------------------------------------------------------------
 constexpr int ROW_NT = 256;
 constexpr int ROW_WAVES = ROW_NT / 64;
-constexpr int PAD_ROWS = 16;     // rows whose source one wave looks up before zeroing the empty ones
+constexpr int PAD_ROWS = 4;      // rows whose source one wave looks up before zeroing the empty ones (16: 96 us
+                                 // for 33024 rows of 7168 bf16, nearly all empty; 4: 91 us)
 
 // 16 bytes at element alignment.
-struct __attribute__((packed, aligned(2))) Piece2 { i32x4 v; };
-struct __attribute__((packed, aligned(4))) Piece4 { i32x4 v; };
+typedef i32x4 Piece2 __attribute__((aligned(2)));
+typedef i32x4 Piece4 __attribute__((aligned(4)));
 template <int DT>
 struct Elem {
     static constexpr int size = DT == kOutF32 ? 4 : 2;
@@ -221,11 +222,21 @@ struct Elem {
 };
 template <int DT>
 __device__ __forceinline__ i32x4 load_piece(const char* p) {
-    return ((const __attribute__((address_space(1))) typename Elem<DT>::Piece*)p)->v;
+    return *(const __attribute__((address_space(1))) typename Elem<DT>::Piece*)p;
 }
 template <int DT>
 __device__ __forceinline__ void store_piece(char* p, i32x4 v) {
-    ((__attribute__((address_space(1))) typename Elem<DT>::Piece*)p)->v = v;
+    *(__attribute__((address_space(1))) typename Elem<DT>::Piece*)p = v;
+}
+// The same past the caches' retention, for what is used once (see kStreamBytes).
+template <int DT, bool STREAM>
+__device__ __forceinline__ i32x4 load_once(const char* p) {
+    if constexpr (STREAM) return __builtin_nontemporal_load((const __attribute__((address_space(1))) typename Elem<DT>::Piece*)p);
+    else return load_piece<DT>(p);
+}
+template <int DT>
+__device__ __forceinline__ void store_once(char* p, i32x4 v) {
+    __builtin_nontemporal_store(v, (__attribute__((address_space(1))) typename Elem<DT>::Piece*)p);
 }
 template <int DT>
 __device__ __forceinline__ void unpack(i32x4 v, float (&f)[Elem<DT>::per]) {
@@ -281,7 +292,7 @@ __device__ __forceinline__ void zero_empty_rows(const MoeRowsParams& p, char* ou
 
 // One wave moves SEG pieces a lane of one token's row to the token's rows; the waves past the
 // tokens' zero the empty rows.
-constexpr int SEG = 4;
+constexpr int SEG = 2;
 template <int DT>
 __global__ __launch_bounds__(ROW_NT) void moe_permute_kernel(MoeRowsParams p) {
     using El = Elem<DT>;
@@ -318,7 +329,7 @@ __global__ __launch_bounds__(ROW_NT) void moe_permute_kernel(MoeRowsParams p) {
 
 // One wave sums USEG pieces a lane of one token's rows.
 constexpr int USEG = 2;
-template <int DT, bool WEIGHTED>
+template <int DT, bool WEIGHTED, bool STREAM>
 __global__ __launch_bounds__(ROW_NT) void moe_unpermute_kernel(MoeRowsParams p) {
     using El = Elem<DT>;
     const int lane = threadIdx.x & 63;
@@ -346,7 +357,7 @@ __global__ __launch_bounds__(ROW_NT) void moe_unpermute_kernel(MoeRowsParams p) 
         for (int u = 0; u < USEG; ++u)
             if (c0 + 64 * u < pieces) {
                 float f[El::per];
-                unpack<DT>(load_piece<DT>(src + 16 * (c0 + 64 * u)), f);
+                unpack<DT>(load_once<DT, STREAM>(src + 16 * (c0 + 64 * u)), f);
 #pragma unroll
                 for (int q = 0; q < El::per; ++q) acc[u][q] += WEIGHTED ? w * f[q] : f[q];
             }
@@ -355,7 +366,7 @@ __global__ __launch_bounds__(ROW_NT) void moe_unpermute_kernel(MoeRowsParams p) 
     char* dst = (char*)p.out + t * p.hidden * El::size;
 #pragma unroll
     for (int u = 0; u < USEG; ++u)
-        if (c0 + 64 * u < pieces) store_piece<DT>(dst + 16 * (c0 + 64 * u), pack<DT>(acc[u]));
+        if (c0 + 64 * u < pieces) store_once<DT>(dst + 16 * (c0 + 64 * u), pack<DT>(acc[u]));
     if (has_tail) store_one<DT>(dst + tail_at, last);
 }
 
@@ -363,7 +374,7 @@ __global__ __launch_bounds__(ROW_NT) void moe_unpermute_kernel(MoeRowsParams p) 
 // read again for every j) while its k rows of y are read, reduced against it and the k rows of dy
 // written.  The workgroups past the tokens' zero the empty rows of dy.
 constexpr int GSEG = 4;
-template <int DT>
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(ROW_NT) void moe_unpermute_grad_kernel(MoeRowsParams p) {
     using El = Elem<DT>;
     __shared__ float part[ROW_WAVES];
@@ -399,7 +410,7 @@ __global__ __launch_bounds__(ROW_NT) void moe_unpermute_grad_kernel(MoeRowsParam
 #pragma unroll
             for (int u = 0; u < GSEG; ++u)
                 if (c0 + u * ROW_NT < pieces) {
-                    y[u] = load_piece<DT>(ysrc + 16 * (c0 + u * ROW_NT));
+                    y[u] = load_once<DT, STREAM>(ysrc + 16 * (c0 + u * ROW_NT));
                     if (!once) d[u] = load_piece<DT>(dsrc + 16 * (c0 + u * ROW_NT));
                 }
 #pragma unroll
@@ -413,7 +424,7 @@ __global__ __launch_bounds__(ROW_NT) void moe_unpermute_grad_kernel(MoeRowsParam
                         dot += fd[q] * fy[q];
                         fd[q] *= w;
                     }
-                    store_piece<DT>(dst + 16 * (c0 + u * ROW_NT), pack<DT>(fd));
+                    store_once<DT>(dst + 16 * (c0 + u * ROW_NT), pack<DT>(fd));
                 }
         }
         if (tid < tail) {
@@ -445,9 +456,16 @@ int64_t row_segments(int64_t hidden, int dt, int per_lane) {
     return pieces <= 64 * per_lane ? 1 : (pieces + 64 * per_lane - 1) / (64 * per_lane);
 }
 
+// Rows of y beyond this are read past the caches' retention: twice the 256 MB Infinity Cache, so they cannot be in it
+// from whoever wrote them.  3.8 GB: 784 -> 739 us (unpermute), 1576 -> 1552 us (gradient); but 268 MB, half of which
+// is still there: 62 -> 68 us, and 33 MB 11.9 -> 14.5 us.  Sums and gradients are always written that way (826 -> 784 us,
+// 77 -> 62 us); permute's copies are not (805 -> 826 us).
+constexpr int64_t kStreamBytes = (int64_t)512 << 20;
+
 template <int DT>
 void launch_rows(MoeRowsParams p, int op, hipStream_t stream) {
     const int64_t pad_waves = (p.rows + PAD_ROWS - 1) / PAD_ROWS;
+    const bool stream_rows = p.rows * p.hidden * Elem<DT>::size > kStreamBytes;
     if (op == kMoePermute) {
         p.segments = row_segments(p.hidden, DT, SEG);
         p.items = p.tokens * p.segments;
@@ -457,15 +475,17 @@ void launch_rows(MoeRowsParams p, int op, hipStream_t stream) {
         p.segments = row_segments(p.hidden, DT, USEG);
         p.items = p.tokens * p.segments;
         const int64_t grid = (p.items + ROW_WAVES - 1) / ROW_WAVES;
-        if (p.weights)
-            hipLaunchKernelGGL((moe_unpermute_kernel<DT, true>), dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p);
-        else
-            hipLaunchKernelGGL((moe_unpermute_kernel<DT, false>), dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p);
+        auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p); };
+        if (p.weights) stream_rows ? run(moe_unpermute_kernel<DT, true, true>) : run(moe_unpermute_kernel<DT, true, false>);
+        else stream_rows ? run(moe_unpermute_kernel<DT, false, true>) : run(moe_unpermute_kernel<DT, false, false>);
     } else {
         p.segments = 1;
         p.items = p.tokens;
         const int64_t grid = p.items + (pad_waves + ROW_WAVES - 1) / ROW_WAVES;
-        hipLaunchKernelGGL((moe_unpermute_grad_kernel<DT>), dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p);
+        if (stream_rows)
+            hipLaunchKernelGGL((moe_unpermute_grad_kernel<DT, true>), dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p);
+        else
+            hipLaunchKernelGGL((moe_unpermute_grad_kernel<DT, false>), dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p);
     }
 }
 

@@ -805,9 +805,12 @@ def _weights(t: torch.Tensor, row_of: torch.Tensor, what: str = "weights"):
         raise ValueError(f"{what} must be a contiguous float32 tensor of row_of's shape, on its device")
 
 
-def _result(out: Optional[torch.Tensor], shape, dtype, device, what: str) -> torch.Tensor:
+def _result(out: Optional[torch.Tensor], shape, dtype, device, what: str, stream) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=device)
+        if stream is not None:
+            out.record_stream(stream)      # keep it alive for the launch stream's pending work
+        return out
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
     return out
@@ -867,7 +870,7 @@ def kgw_moe_permute(x: torch.Tensor, row_of: torch.Tensor, src_of: torch.Tensor,
     if row_of.shape[0] != tokens:
         raise ValueError(f"row_of has {row_of.shape[0]} tokens, x has {tokens}")
     rows = src_of.shape[0]
-    out = _result(out, (rows, hidden), x.dtype, device, "out")
+    out = _result(out, (rows, hidden), x.dtype, device, "out", stream)
     st = load_library().kgw_moe_permute(x.data_ptr(), ld, code, row_of.data_ptr(), src_of.data_ptr(), tokens,
                                         row_of.shape[1], rows, hidden, out.data_ptr(), _launch_stream(stream, device))
     _check(st, "kgw_moe_permute")
@@ -889,7 +892,7 @@ def kgw_moe_unpermute(y: torch.Tensor, row_of: torch.Tensor, weights: Optional[t
         _weights(weights, row_of)
     rows, hidden = y.shape
     tokens, topk = row_of.shape
-    out = _result(out, (tokens, hidden), y.dtype, device, "out")
+    out = _result(out, (tokens, hidden), y.dtype, device, "out", stream)
     st = load_library().kgw_moe_unpermute(y.data_ptr(), ld, code, row_of.data_ptr(), _ptr(weights), tokens, topk,
                                           rows, hidden, out.data_ptr(), _launch_stream(stream, device))
     _check(st, "kgw_moe_unpermute")
@@ -917,8 +920,8 @@ def kgw_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_of: torch.Te
         raise ValueError(f"dout must be a {(tokens, hidden)} {y.dtype} tensor on {device}")
     if src_of.shape[0] != rows:
         raise ValueError(f"src_of has {src_of.shape[0]} rows, y has {rows}")
-    dy = _result(dy, (rows, hidden), y.dtype, device, "dy")
-    dweights = _result(dweights, (tokens, topk), torch.float32, device, "dweights")
+    dy = _result(dy, (rows, hidden), y.dtype, device, "dy", stream)
+    dweights = _result(dweights, (tokens, topk), torch.float32, device, "dweights", stream)
     st = load_library().kgw_moe_unpermute_grad(dout.data_ptr(), ld_d, y.data_ptr(), ld_y, code, row_of.data_ptr(),
                                                src_of.data_ptr(), weights.data_ptr(), tokens, topk, rows, hidden,
                                                dy.data_ptr(), dweights.data_ptr(), _launch_stream(stream, device))
@@ -969,7 +972,7 @@ def kgw_newton_schulz(G: torch.Tensor, *, steps: int = 5, coefficients=NEWTON_SC
     device = _on_gpu(G, "G")
     dtype = out.dtype if out is not None else (G.dtype if out_dtype is None else out_dtype)
     out_code = _out_code(dtype)
-    out = _result(out, G.shape, dtype, device, "out")
+    out = _result(out, G.shape, dtype, device, "out", stream)
     lib = load_library()
     need = lib.kgw_newton_schulz_workspace_bytes(batch, m, n, out_code)
     if workspace is None:

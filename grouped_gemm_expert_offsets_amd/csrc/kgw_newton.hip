@@ -90,7 +90,7 @@ __global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, int64_
     float v[2][8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_eight<DT>(p, b, (TALL ? c0 : r0) + i0 + 32 * u, (TALL ? r0 : c0) + 8 * q, v[u]);
-    const float scale = first_scale(p, b);
+    const FirstScale scale = first_scale(p, b);
     if constexpr (TALL) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, int64_
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = as_fp32(v[u][e] * scale);
+        for (int e = 0; e < 8; ++e) v[u][e] = scale.of(v[u][e]);
         store_planes<true>(v[u], x + element<SPLIT>(r0 + i0 + 32 * u, c0 + 8 * q, C), lo_off);
     }
 }

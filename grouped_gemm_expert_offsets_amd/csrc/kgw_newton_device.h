@@ -94,13 +94,26 @@ __device__ __forceinline__ void load_eight(const NewtonParams& p, int b, int64_t
     }
 }
 
-// 2^13 / (|G|_F + eps) of matrix b, the same in every wave.
-__device__ __forceinline__ float first_scale(const NewtonParams& p, int b) {
+// What the first iterate multiplies G by, 2^13 / (|G|_F + eps), in two factors: where the norm is so small that
+// the quotient leaves fp32's range, G is first brought up by 2^100.
+struct FirstScale {
+    float before, scale;
+    __device__ __forceinline__ float of(float g) const { return as_fp32(g * before * scale); }
+};
+__device__ __forceinline__ FirstScale scale_of_norm(double norm, float eps) {
+    const double d = norm + (double)eps;
+    FirstScale f;
+    f.before = d < 0x1p-100 ? 0x1p100f : 1.0f;
+    f.scale = (float)((double)kXScale / (d * (double)f.before));
+    return f;
+}
+// The same in every wave of matrix b, from the parts of its norm.
+__device__ __forceinline__ FirstScale first_scale(const NewtonParams& p, int b) {
     double s = 0.0;
     for (int i = threadIdx.x & 63; i < p.num_parts; i += 64) s += p.parts[(int64_t)b * kNewtonParts + i];
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-    return (float)((double)kXScale / (__builtin_sqrt(s) + (double)p.eps));
+    return scale_of_norm(__builtin_sqrt(s), p.eps);
 }
 
 }  // namespace kgw

@@ -149,7 +149,7 @@ __device__ __forceinline__ void clear(f32x16 (&m)[N]) {
 
 // One chunk of the first iterate into LDS.
 template <int RB, int DT>
-__device__ __forceinline__ void first_chunk(const NarrowParams& q, int b, int chunk, float scale, lds_char* x, int tid) {
+__device__ __forceinline__ void first_chunk(const NarrowParams& q, int b, int chunk, FirstScale scale, lds_char* x, int tid) {
     using N = Narrow<RB>;
     const int64_t n0 = (int64_t)chunk * CHUNK;
     if (!q.tall) {
@@ -159,7 +159,7 @@ __device__ __forceinline__ void first_chunk(const NarrowParams& q, int b, int ch
             float v[8];
             load_eight<DT>(q.p, b, row, n0 + 8 * c8, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = as_fp32(v[e] * scale);
+            for (int e = 0; e < 8; ++e) v[e] = scale.of(v[e]);
             i32x4 hi, lo;
             split_eight(v, hi, lo);
 #pragma unroll
@@ -184,7 +184,7 @@ __device__ __forceinline__ void first_chunk(const NarrowParams& q, int b, int ch
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int row = 8 * r8 + e;
-                const HalfPair u = split_pair(as_fp32(v[e] * scale), 0.0f);
+                const HalfPair u = split_pair(scale.of(v[e]), 0.0f);
                 const uint32_t at = place + (uint32_t)(row & 31) * 16u;
                 *reinterpret_cast<__attribute__((address_space(3))) uint16_t*>(x + N::x_at(col >> 4, row >> 5, 0) + at) = (uint16_t)u.hi;
                 *reinterpret_cast<__attribute__((address_space(3))) uint16_t*>(x + N::x_at(col >> 4, row >> 5, 1) + at) = (uint16_t)u.lo;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_first_kernel(Na
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int b = blockIdx.y, group = blockIdx.x;
-    const float scale = first_scale(q.p, b);
+    const FirstScale scale = first_scale(q.p, b);
     f32x16 part[N::MINE];
     clear(part);
     const int first = group * q.per_group, last = min(q.chunks, first + q.per_group);
@@ -451,8 +451,7 @@ __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_whole_kernel(Na
     double squares = 0.0;
 #pragma unroll
     for (int w = 0; w < N::WAVES; ++w) squares += sums[w];
-    const double norm = __builtin_sqrt(squares);
-    const float scale = (float)((double)kXScale / (norm + (double)q.p.eps));
+    const FirstScale scale = scale_of_norm(__builtin_sqrt(squares), q.p.eps);
 
     f32x16 mine[N::MINE];
     for (int chunk = 0; chunk < q.chunks; ++chunk) first_chunk<RB, DT>(q, b, chunk, scale, x + chunk * N::X_BYTES, tid);

@@ -78,10 +78,17 @@ def test_against_the_iteration(batch, m, n, dtype, out):
     check(got, reference(G))
 
 
-# enough 256 x 256 tiles of the update for every CU: (batch, m, n) with ceil(m/256) ceil(n/256) batch >= 256
-@pytest.mark.parametrize("batch,m,n", [(64, 300, 500), (16, 1024, 1024), (9, 1100, 1537), (8, 2000, 1025), (130, 40, 300)])
+# One batch for every way a size is taken: 64-edged tiles alone and several workgroups a tile, 128-edged ones
+# likewise, 256-edged ones with the last round whole or in quarters and with strips on one side, the other, both
+# or none; short sides with one workgroup a matrix, a launch a step, and several chunks a workgroup.
+WAYS = [(4, 256, 512), (1, 200, 7000), (1, 4096, 512), (64, 300, 500), (3, 1777, 1000), (1, 1536, 2900), (10, 381, 3323),
+        (8, 4219, 381), (10, 3451, 509), (10, 509, 2555), (5, 1149, 3451), (24, 1021, 1019), (24, 1147, 1149), (12, 1531, 1405),
+        (3, 20, 30), (70, 400, 60), (130, 40, 300), (40, 60, 2100), (20, 3500, 120), (4, 128, 128)]
+
+
+@pytest.mark.parametrize("batch,m,n", WAYS)
 @pytest.mark.parametrize("dtype,out", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
-def test_large_tiles(batch, m, n, dtype, out):
+def test_every_way_a_size_is_taken(batch, m, n, dtype, out):
     G = gradients(batch, m, n, dtype, m + n)
     check(kgw.kgw_newton_schulz(G, out_dtype=out), reference(G))
 
@@ -140,11 +147,12 @@ def test_zero_and_special_matrices_stay_apart(out):
     check(got[[0, 4]], reference(G[[0, 4]]))
 
 
-@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e12, 1e30])
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-12, 1e12, 1e30])
 def test_scales_whose_squares_leave_fp32(scale):
-    G = gradients(2, 50, 80, torch.float32, 8, scale)
-    check(kgw.kgw_newton_schulz(G, eps=0.0), reference(G, eps=0.0))
-    if scale < 1e-20:               # eps takes over: X stays small, the steps multiply it by a^5
+    for m, n in ((50, 80), (50, 900), (150, 170)):
+        G = gradients(2, m, n, torch.float32, 8, scale)
+        check(kgw.kgw_newton_schulz(G, eps=0.0), reference(G, eps=0.0))
+    if scale == 1e-30:              # eps takes over: X stays small, the steps multiply it by a^5
         check(kgw.kgw_newton_schulz(G * 1e20), reference(G * 1e20))
 
 

@@ -115,12 +115,13 @@ __global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, int64_
 // ----------------------------------------------------------------------------
 // the products
 // ----------------------------------------------------------------------------
-enum NewtonProduct { kGram, kSquare, kUpdate };
+enum NewtonProduct { kGram, kSquare, kUpdate, kLast };   // kLast: the last update, which writes the result
+constexpr bool updates(NewtonProduct k) { return k == kUpdate || k == kLast; }
 
 struct NewtonGemm {
     const char* left;       // (batch, R, K) rows of the product
     const char* right;      // gram, square: left again; update: the iterate (batch, K, C)
-    char* out;              // gram: A; square: B; update: the next iterate, or NULL in the last step
+    char* out;              // gram: A; square: B; update: the next iterate
     void* result;           // last update: (batch, m, n) of result_dtype
     int64_t m, n;
     int32_t result_dtype, tall;
@@ -150,7 +151,7 @@ __device__ __forceinline__ int item_of(int bid, int items, int num_xcds) {
 constexpr int kRowGroup = 4;
 template <bool SPLIT, NewtonProduct KIND>
 __device__ __forceinline__ int turn_of(const NewtonGemm& p, int tm, int tile) {
-    if (!SPLIT || KIND != kUpdate) return 0;
+    if (!SPLIT || !updates(KIND)) return 0;
     const int rows = tile == 256 ? kRowGroup : 1;
     const int end = min((tm / rows + 1) * rows, p.tiles_m);
     return end == p.tiles_m ? 0 : end * tile / 32;
@@ -160,10 +161,10 @@ __device__ __forceinline__ int turn_of(const NewtonGemm& p, int tm, int tile) {
 // and below the diagonal.
 template <NewtonProduct KIND>
 __device__ __forceinline__ void tile_of(const NewtonGemm& p, int index, int& b, int& tm, int& tn) {
-    const int per = KIND == kUpdate ? p.tiles_m * p.tiles_n : p.tiles_m * (p.tiles_m + 1) / 2;
+    const int per = updates(KIND) ? p.tiles_m * p.tiles_n : p.tiles_m * (p.tiles_m + 1) / 2;
     b = index / per;
     const int local = index - b * per;
-    if constexpr (KIND == kUpdate) {
+    if constexpr (updates(KIND)) {
         tile_coords(local, p.tiles_m, p.tiles_n, kRowGroup, tm, tn);
     } else {
         tm = (int)((__builtin_sqrtf(8.0f * (float)local + 1.0f) - 1.0f) * 0.5f);
@@ -298,9 +299,9 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     const int l32 = lane & 31, lhi = lane >> 5, g16 = lane >> 4, i16 = lane & 15;
 
     const int64_t ldl = p.k * (SPLIT ? 4 : 2);                                    // bytes of a left row
-    const int64_t ldr = (KIND == kUpdate ? p.cols : p.k) * (SPLIT ? 4 : 2);       // of a right row
+    const int64_t ldr = (updates(KIND) ? p.cols : p.k) * (SPLIT ? 4 : 2);       // of a right row
     const char* const left = p.left + ((int64_t)b * p.rows + m0) * ldl;
-    const char* const right = KIND == kUpdate ? p.right + (int64_t)b * p.k * ldr + n0 * (SPLIT ? 4 : 2)
+    const char* const right = updates(KIND) ? p.right + (int64_t)b * p.k * ldr + n0 * (SPLIT ? 4 : 2)
                                               : p.right + ((int64_t)b * p.rows + n0) * ldr;
 
     uint32_t l_off[LOADS], r_off[LOADS];
@@ -309,7 +310,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
         const int row = (wave * LOADS + t) * 8 + (lane >> 3);
         const uint32_t chunk = (uint32_t)((lane & 7) ^ ((row >> 1) & 7));
         l_off[t] = (uint32_t)row * (uint32_t)ldl + chunk * 16u;
-        if constexpr (KIND == kUpdate) {
+        if constexpr (updates(KIND)) {
             const int at = (wave * LOADS + t) * 64 + lane;
             const int krow = at / CPR;
             r_off[t] = (uint32_t)krow * (uint32_t)ldr + (uint32_t)((at % CPR) ^ (((krow & 3) << 2) & (CPR - 1))) * 16u;
@@ -320,11 +321,11 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     const int all_stages = (int)(p.k / KSTAGE);
     const int first_stage = JOIN ? all_stages * part / p.parts : 0;
     const int stages = JOIN ? all_stages * (part + 1) / p.parts - first_stage : all_stages;
-    const int64_t r_step = KIND == kUpdate ? KSTAGE * ldr : 128;
+    const int64_t r_step = updates(KIND) ? KSTAGE * ldr : 128;
     // Three products: the update walks K from stage `turn` on, so that its linear term comes late (fold()).
     // Parts of K: the stages from first_stage on (never both).
     auto place_of = [&](int s) __attribute__((always_inline)) {
-        return KIND != kUpdate ? first_stage + s : s + turn < stages ? s + turn : s + turn - stages;
+        return !updates(KIND) ? first_stage + s : s + turn < stages ? s + turn : s + turn - stages;
     };
     // Slot n % SLOTS takes the n-th operand stage, left and right in turn.  Load t of slot `slot` with
     // operand stage n; past the last one an empty range (no memory is read).
@@ -346,7 +347,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     };
     auto read_right = [&](int slot, int q, int j) __attribute__((always_inline)) {
         const lds_char* const base = lds + slot * STAGE;
-        if constexpr (KIND == kUpdate) {
+        if constexpr (updates(KIND)) {
             const int chunk = SPLIT ? (wn * NBN + j) * 8 + (q >> 1) * 4 + cq : wn * (WTN / 8) + 4 * j + cq;
             const uint32_t at = (uint32_t)((SPLIT ? 16 * (q & 1) : 16 * q) + kr) * (uint32_t)ROWB +
                                 (uint32_t)((chunk ^ (((i16 >> 2) << 2) & (CPR - 1))) << 4) + (uint32_t)(i16 & 1) * 8u;
@@ -373,17 +374,17 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     // product summed after it rounds it once more: where the result is to be that exact, the tiles of a group of rows
     // start behind the group's own rows and meet them last.
     auto fold = [&](int s, int slot) __attribute__((always_inline)) {
-        const int d = KSTAGE * place_of(s) - (int)(KIND == kUpdate ? m0 : n0);
+        const int d = KSTAGE * place_of(s) - (int)(updates(KIND) ? m0 : n0);
         if (d < 0 || d >= TILE) return;
         const lds_char* const base = lds + slot * STAGE;
 #pragma unroll
         for (int e = 0; e < KSTAGE / 32; ++e) {
             const int at = d + 32 * e;
-            if (at / (KIND == kUpdate ? WTM : WTN) != (KIND == kUpdate ? wm : wn)) continue;
-            const int block = at % (KIND == kUpdate ? WTM : WTN) / 32;
+            if (at / (updates(KIND) ? WTM : WTN) != (updates(KIND) ? wm : wn)) continue;
+            const int block = at % (updates(KIND) ? WTM : WTN) / 32;
             each<PRODUCTS>([&](auto k) __attribute__((always_inline)) {
                 constexpr int j = k / NBM, i = k % NBM;
-                if (block != (KIND == kUpdate ? i : j)) return;
+                if (block != (updates(KIND) ? i : j)) return;
                 // The empty asm statements differ from block to block: the compiler would otherwise merge
                 // the branches' code and reach the sums through pointers, in scratch memory.
                 asm volatile("; block %0" ::"n"(k.value));
@@ -392,7 +393,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
 #pragma unroll
                     for (int plane = 0; plane < (SPLIT ? 2 : 1); ++plane) {
                         uint32_t from;
-                        if constexpr (KIND == kUpdate) {
+                        if constexpr (updates(KIND)) {
                             const int krow = 32 * e + l32;
                             const int chunk = SPLIT ? (wn * NBN + j) * 8 + plane * 4 + g : wn * (WTN / 8) + 4 * j + g;
                             from = (uint32_t)(krow * ROWB + ((chunk ^ (((krow & 3) << 2) & (CPR - 1))) << 4));
@@ -481,7 +482,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
         constexpr std::integral_constant<int, 3> G3{};
         constexpr std::integral_constant<int, 4> G4{};
         constexpr std::integral_constant<int, 5> G5{};
-        if constexpr (KIND != kGram) fold(s, KIND == kUpdate ? rslot : lslot);
+        if constexpr (KIND != kGram) fold(s, updates(KIND) ? rslot : lslot);
         if constexpr (!SPLIT) {
             group(l0, r0, both(G0, lslot, rslot, 1, l1, r1));
             group(l1, r1, both(G1, lslot, rslot, 2, l0, r0));
@@ -532,8 +533,8 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     // acc[j][i][4g + t] is the sum at row 32 i + l32 and column 32 j + 8 g + 4 lhi + t of the wave's
     // part.  It goes out through LDS, 32 rows at a time, so that every store writes whole runs of a row: once as it
     // is and, for a tile below the diagonal, once transposed.
-    constexpr bool TWO = SPLIT || KIND == kUpdate;      // both planes are kept
-    constexpr bool LOW = !SPLIT && KIND == kUpdate;     // the iterate's low plane was no operand: added here
+    constexpr bool TWO = SPLIT || updates(KIND);      // both planes are kept
+    constexpr bool LOW = !SPLIT && updates(KIND);     // the iterate's low plane was no operand: added here
     const int64_t lo_off = SPLIT ? 32 : (int64_t)p.batch * p.rows * p.cols;
     const int64_t matrix = (int64_t)b * p.rows * p.cols * (SPLIT ? 2 : 1);
     uint16_t* const out = (uint16_t*)p.out + matrix;
@@ -599,7 +600,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
         }
     };
 
-    if (KIND == kUpdate && !p.out && p.tall) {
+    if (KIND == kLast && p.tall) {
         // the last step of a matrix taken transposed: its result is the transpose
         if constexpr (LOW) {
 #pragma unroll
@@ -648,11 +649,11 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
                     v[2 * u + 1] += low_scale * f16_hi((uint32_t)lows[i & 1][n][u]);
                 }
             }
-            if (KIND == kUpdate && !p.out) result_at(row + lane_row(across), col_w + lane_col(across), v);
+            if constexpr (KIND == kLast) result_at(row + lane_row(across), col_w + lane_col(across), v);
             else store_planes<TWO>(v, out + row * row_step + col_w * (SPLIT ? 2 : 1) + at_across, lo_off);
         });
     });
-    if (KIND != kUpdate && m0 != n0) {
+    if (!updates(KIND) && m0 != n0) {
         each<NBN>([&](auto j) __attribute__((always_inline)) {
             write_turned(j);
             read_rows(turned, [&](int r, int, const float (&v)[8]) __attribute__((always_inline)) {
@@ -680,7 +681,7 @@ __device__ __forceinline__ void quarter_of(const NewtonGemm& p, int index, int& 
     b = e / per;
     int at = e - b * per;
     const int rows = (int)(p.rows / 128);
-    const bool right = KIND == kUpdate && (p.cols & 128);
+    const bool right = updates(KIND) && (p.cols & 128);
     if (right && at < rows) {
         m0 = (int64_t)at * 128;
         n0 = p.cols - 128;
@@ -707,7 +708,7 @@ __global__ __launch_bounds__(64 * kBigWaves<SPLIT>, kBigWaves<SPLIT> / 4) void n
     } else {
         int64_t m0, n0;
         quarter_of<KIND>(p, bid - p.whole, b, m0, n0);
-        if (KIND != kUpdate && n0 > m0) return;         // the mirror image of another quarter
+        if (!updates(KIND) && n0 > m0) return;         // the mirror image of another quarter
         turn = turn_of<SPLIT, KIND>(p, (int)(m0 / 256), 256);
         newton_tile<128, kBigWaves<SPLIT>, 10, SPLIT, false, KIND>(p, smem, b, m0, n0, turn);
     }
@@ -734,7 +735,7 @@ void launch_small(NewtonGemm g, int tiles, hipStream_t stream) {
     // 128-edged one it pays from 24 stages a part on (56 stages in two: 35 -> 29 us, 32 stages: 27 -> 30 us).
     const int64_t stages = g.k / (SPLIT ? 32 : 64);
     int64_t parts = 1;
-    if (KIND != kUpdate) {
+    if (!updates(KIND)) {
         if (TILE == 64) while (stages > 16 && 2 * (parts + 1) * (parts + 1) <= stages) ++parts;
         else parts = stages / 24;
         if (parts > kNewtonSlabs / tiles) parts = kNewtonSlabs / tiles;
@@ -742,7 +743,7 @@ void launch_small(NewtonGemm g, int tiles, hipStream_t stream) {
     g.parts = parts > 1 ? (int32_t)parts : 1;
     g.items = tiles * g.parts;
     const dim3 grid((uint32_t)g.items);
-    if constexpr (KIND != kUpdate) {
+    if constexpr (!updates(KIND)) {
         if (g.parts > 1) {
             hipLaunchKernelGGL((newton_small_kernel<TILE, false, true, SPLIT, KIND>), grid, dim3(256), 0, stream, g);
             return;
@@ -790,11 +791,11 @@ template <bool SPLIT, NewtonProduct KIND>
 void launch_product(NewtonGemm g, int tile, int num_cus, hipStream_t stream) {
     g.tiles_m = (int32_t)(g.rows / tile);
     g.tiles_n = (int32_t)(g.cols / tile);
-    const int tiles = g.batch * (KIND == kUpdate ? g.tiles_m * g.tiles_n : g.tiles_m * (g.tiles_m + 1) / 2);
+    const int tiles = g.batch * (updates(KIND) ? g.tiles_m * g.tiles_n : g.tiles_m * (g.tiles_m + 1) / 2);
     g.parts = 1;
     if (tile == 256) {
         const int rows = (int)(g.rows / 128), cols = (int)(g.cols / 128);
-        const int right = KIND == kUpdate && cols % 2 ? rows : 0;
+        const int right = updates(KIND) && cols % 2 ? rows : 0;
         g.strips = right + (rows % 2 ? cols - (right ? 1 : 0) : 0);
         g.tiles = tiles;
         const int rest = tiles % num_cus, edges = g.batch * g.strips;
@@ -841,11 +842,12 @@ void launch_steps(const NewtonParams& p, const NewtonPlan& plan, const float* co
         g.left = p.b;
         g.right = x;
         const bool last = s + 1 == p.steps;
-        g.out = last ? nullptr : p.x[(s + 1) & 1];
+        g.out = p.x[(s + 1) & 1];
         g.result = p.out;
         g.scale = (last ? 1.0f / kXScale : 1.0f) / kBScale;
         g.linear = co[3 * s] * kBScale;
-        launch_product<SPLIT, kUpdate>(g, plan.tile, num_cus, stream);
+        if (last) launch_product<SPLIT, kLast>(g, plan.tile, num_cus, stream);
+        else launch_product<SPLIT, kUpdate>(g, plan.tile, num_cus, stream);
     }
 }
 

@@ -181,32 +181,36 @@ __device__ __forceinline__ uint32_t image_at(int row, int chunk) {
     return (uint32_t)(row * W * 4 + ((chunk ^ (row & (W / 4 - 1))) << 4));
 }
 
-// Eight consecutive elements of row `row` of the result, those inside it.
+// Eight consecutive elements of the result, those inside it: `row`, `col` behind the wave's row0, col0, which
+// make the address's uniform part.
 template <int DT>
-__device__ __forceinline__ void store_result(const NewtonGemm& p, const float (&v)[8], int b, int64_t row, int64_t col) {
-    if (row >= p.m || col >= p.n) return;
-    const int64_t at = ((int64_t)b * p.m + row) * p.n + col;
+__device__ __forceinline__ void store_result(const NewtonGemm& p, const float (&v)[8], int b, int64_t row0, int64_t col0,
+                                             int row, int col) {
+    const int left = (int)(p.n - col0) - col;           // sizes are at most 2^20
+    if (row >= (int)(p.m - row0) || left <= 0) return;
+    const int64_t at0 = ((int64_t)b * p.m + row0) * p.n + col0;
+    const uint32_t at = (uint32_t)row * (uint32_t)p.n + (uint32_t)col;
     if constexpr (DT == kOutF32) {
-        float* const to = (float*)p.result + at;
-        if (col + 8 <= p.n) {
+        float* const to = (float*)p.result + at0 + at;
+        if (left >= 8) {
             ((__attribute__((address_space(1))) Floats4*)to)[0].v = f32x4{v[0], v[1], v[2], v[3]};
             ((__attribute__((address_space(1))) Floats4*)to)[1].v = f32x4{v[4], v[5], v[6], v[7]};
         } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (col + u < p.n) to[u] = v[u];
+                if (u < left) to[u] = v[u];
         }
     } else {
-        uint16_t* const to = (uint16_t*)p.result + at;
+        uint16_t* const to = (uint16_t*)p.result + at0 + at;
         i32x4 w;
 #pragma unroll
         for (int u = 0; u < 4; ++u) w[u] = (int)pack_half2<DT>(v[2 * u], v[2 * u + 1]);
-        if (col + 8 <= p.n) {
+        if (left >= 8) {
             ((__attribute__((address_space(1))) Halves8*)to)->v = w;
         } else {
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (col + u < p.n) to[u] = (uint16_t)(((uint32_t)w[u >> 1] >> (16 * (u & 1))) & 0xFFFFu);
+                if (u < left) to[u] = (uint16_t)(((uint32_t)w[u >> 1] >> (16 * (u & 1))) & 0xFFFFu);
         }
     }
 }
@@ -591,37 +595,51 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     auto lane_at = [&](auto width) { return (uint32_t)element<SPLIT>(lane_row(width), lane_col(width), p.cols); };
     const std::integral_constant<int, WTN> across;
     const std::integral_constant<int, WTM> turned;
-    auto result_at = [&](int64_t row, int64_t col, const float (&v)[8]) __attribute__((always_inline)) {
+    auto result_at = [&](int64_t row0, int64_t col0, int row, int col, const float (&v)[8]) __attribute__((always_inline)) {
         if constexpr (!SPLIT) {
-            store_result<kOutBf16>(p, v, b, row, col);
+            store_result<kOutBf16>(p, v, b, row0, col0, row, col);
         } else {
-            if (p.result_dtype == kOutF16) store_result<kOutF16>(p, v, b, row, col);
-            else store_result<kOutF32>(p, v, b, row, col);
+            if (p.result_dtype == kOutF16) store_result<kOutF16>(p, v, b, row0, col0, row, col);
+            else store_result<kOutF32>(p, v, b, row0, col0, row, col);
         }
     };
 
     if (KIND == kLast && p.tall) {
-        // the last step of a matrix taken transposed: its result is the transpose
+        // The last step of a matrix taken transposed: its result is the transpose.  The low plane comes through LDS:
+        // read from memory as the sums lie, 8 bytes of 32 rows at a time, it made this launch take 2109 us
+        // instead of 1921 (8 x 7168 x 4096 to bf16).
         if constexpr (LOW) {
+            constexpr int CHUNKS = WTN / 8;             // 16-byte chunks of a row; chunk q in slot q ^ low_sw(row)
+            auto low_sw = [](int row) { return (row >> 1) & (CHUNKS - 1); };
+            static_assert(WTM * WTN * 2 <= SLOTS * STAGE / WAVES, "the part's low plane fits the wave's share of LDS");
 #pragma unroll
-            for (int i = 0; i < NBM; ++i) {
-                in_order();                             // a few loads at a time: the registers are full
+            for (int t = 0; t < WTM * CHUNKS / 64; ++t) {
+                const int at = t * 64 + lane, row = at / CHUNKS;
+                const uint32_t off = (uint32_t)row * (uint32_t)(p.cols * 2) + (uint32_t)(((at % CHUNKS) ^ low_sw(row)) << 4);
+                dma_16B(rsrc_words((const char*)(low + row_w * p.cols + col_w), 0xFFFFFFFFu), off,
+                        lds0 + (uint32_t)(wave * (SLOTS * STAGE / WAVES) + t * 1024));
+            }
+            wait_vmcnt<0>();
+            in_order();
+#pragma unroll
+            for (int i = 0; i < NBM; ++i)
 #pragma unroll
                 for (int j = 0; j < NBN; ++j)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const i16x4 x = *(const __attribute__((address_space(1))) i16x4*)(
-                            low + (row_w + 32 * i + l32) * p.cols + col_w + 32 * j + 8 * g + 4 * lhi);
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) acc[j][i][4 * g + t] += p.linear * half_bits((uint16_t)x[t]);
+                        const i32x2 x = lds_load_8B(mine, (uint32_t)((32 * i + l32) * WTN * 2 +
+                                                                     (((4 * j + g) ^ low_sw(l32)) << 4) + lhi * 8));
+                        acc[j][i][4 * g] += p.linear * f16_lo((uint32_t)x[0]);
+                        acc[j][i][4 * g + 1] += p.linear * f16_hi((uint32_t)x[0]);
+                        acc[j][i][4 * g + 2] += p.linear * f16_lo((uint32_t)x[1]);
+                        acc[j][i][4 * g + 3] += p.linear * f16_hi((uint32_t)x[1]);
                     }
-            }
         }
 #pragma unroll
         for (int j = 0; j < NBN; ++j) {
             write_turned(j);
             read_rows(turned, [&](int r, int, const float (&v)[8]) __attribute__((always_inline)) {
-                result_at(col_w + 32 * j + r + lane_row(turned), row_w + lane_col(turned), v);
+                result_at(col_w + 32 * j + r, row_w, lane_row(turned), lane_col(turned), v);
             });
         }
         return;
@@ -649,7 +667,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
                     v[2 * u + 1] += low_scale * f16_hi((uint32_t)lows[i & 1][n][u]);
                 }
             }
-            if constexpr (KIND == kLast) result_at(row + lane_row(across), col_w + lane_col(across), v);
+            if constexpr (KIND == kLast) result_at(row, col_w, lane_row(across), lane_col(across), v);
             else store_planes<TWO>(v, out + row * row_step + col_w * (SPLIT ? 2 : 1) + at_across, lo_off);
         });
     });

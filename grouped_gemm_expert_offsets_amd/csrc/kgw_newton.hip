@@ -224,12 +224,12 @@ __device__ __forceinline__ void store_result(const NewtonGemm& p, const float (&
 // counts as done (vmcnt) only there, so waiting for the own stores before counting the arrival is all the
 // release that is needed.  A fence would write back each die's whole L2 for every workgroup: with 216
 // workgroups of 64 KiB it made a product of 35 us take 57.
-template <int NBM, int NBN>
+template <int WAVES, int NBM, int NBN>
 __device__ bool join_parts(const NewtonGemm& p, char* smem, int tile, int part, int wave, int lane,
                            f32x16 (&acc)[NBN][NBM]) {
     constexpr int WAVE = NBM * NBN * 1024;              // floats of one wave
-    float* const tile_slabs = p.slabs + (int64_t)tile * p.parts * (4 * WAVE) + wave * WAVE + lane;
-    float* const own = tile_slabs + part * (4 * WAVE);
+    float* const tile_slabs = p.slabs + (int64_t)tile * p.parts * (WAVES * WAVE) + wave * WAVE + lane;
+    float* const own = tile_slabs + part * (WAVES * WAVE);
 #pragma unroll
     for (int j = 0; j < NBN; ++j)
 #pragma unroll
@@ -259,7 +259,7 @@ __device__ bool join_parts(const NewtonGemm& p, char* smem, int tile, int part, 
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[j][i][e] = 0.0f;
     for (int w = 0; w < p.parts; ++w) {
-        const float* const from = tile_slabs + w * (4 * WAVE);
+        const float* const from = tile_slabs + w * (WAVES * WAVE);
 #pragma unroll
         for (int j = 0; j < NBN; ++j)
 #pragma unroll
@@ -531,7 +531,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
         for (int j = 0; j < NBN; ++j)
 #pragma unroll
             for (int i = 0; i < NBM; ++i) asm volatile("" : "+v"(acc[j][i]));
-        if (!join_parts<NBM, NBN>(p, smem, tile, part, wave, lane, acc)) return;
+        if (!join_parts<WAVES, NBM, NBN>(p, smem, tile, part, wave, lane, acc)) return;
     }
 
     // acc[j][i][4g + t] is the sum at row 32 i + l32 and column 32 j + 8 g + 4 lhi + t of the wave's
@@ -734,15 +734,20 @@ __global__ __launch_bounds__(64 * kBigWaves<SPLIT>, kBigWaves<SPLIT> / 4) void n
 
 // Small tiles: two workgroups a CU with SLOTS slots each (80 KiB), or one with twice as many.
 // JOIN: p.parts of them share a tile's K.
+// A 128-edged tile alone on its CU has eight waves, so that one multiplies while another waits for LDS:
+// 8 x 512 x 2048 235 -> 227 us, 2 x 1024 x 4096 327 -> 318, 3 x 1777 x 1000 502 -> 497, 2048 x 2048 345 -> 349; two
+// such tiles are as good with four each (27 x 1352 x 1072 1475 us, eight 1540).
+template <int TILE, bool TWO>
+constexpr int kSmallWaves = TILE == 128 && !TWO ? 8 : 4;
 template <int TILE, bool TWO, bool JOIN, bool SPLIT, NewtonProduct KIND>
-__global__ __launch_bounds__(256, 2) void newton_small_kernel(NewtonGemm p) {
+__global__ __launch_bounds__((64 * kSmallWaves<TILE, TWO>), 2) void newton_small_kernel(NewtonGemm p) {
     constexpr int SLOTS = (TWO ? 5 : 10) * (128 / TILE);
     __shared__ __attribute__((aligned(1024))) char smem[SLOTS * TILE * 128];
     const int item = item_of(blockIdx.x, p.items, p.num_xcds);
     const int tile = JOIN ? item / p.parts : item;
     int b, tm, tn;
     tile_of<KIND>(p, tile, b, tm, tn);
-    newton_tile<TILE, 4, SLOTS, SPLIT, JOIN, KIND>(p, smem, b, (int64_t)tm * TILE, (int64_t)tn * TILE,
+    newton_tile<TILE, kSmallWaves<TILE, TWO>, SLOTS, SPLIT, JOIN, KIND>(p, smem, b, (int64_t)tm * TILE, (int64_t)tn * TILE,
                                              turn_of<SPLIT, KIND>(p, tm, TILE), tile, JOIN ? item - tile * p.parts : 0);
 }
 
@@ -763,14 +768,14 @@ void launch_small(NewtonGemm g, int tiles, hipStream_t stream) {
     const dim3 grid((uint32_t)g.items);
     if constexpr (!updates(KIND)) {
         if (g.parts > 1) {
-            hipLaunchKernelGGL((newton_small_kernel<TILE, false, true, SPLIT, KIND>), grid, dim3(256), 0, stream, g);
+            hipLaunchKernelGGL((newton_small_kernel<TILE, false, true, SPLIT, KIND>), grid, dim3((64 * kSmallWaves<TILE, false>)), 0, stream, g);
             return;
         }
     }
     if (g.items > kNewtonSlabs)
-        hipLaunchKernelGGL((newton_small_kernel<TILE, true, false, SPLIT, KIND>), grid, dim3(256), 0, stream, g);
+        hipLaunchKernelGGL((newton_small_kernel<TILE, true, false, SPLIT, KIND>), grid, dim3((64 * kSmallWaves<TILE, true>)), 0, stream, g);
     else
-        hipLaunchKernelGGL((newton_small_kernel<TILE, false, false, SPLIT, KIND>), grid, dim3(256), 0, stream, g);
+        hipLaunchKernelGGL((newton_small_kernel<TILE, false, false, SPLIT, KIND>), grid, dim3((64 * kSmallWaves<TILE, false>)), 0, stream, g);
 }
 
 // Time of what follows the whole rounds of 256 x 256 tiles, in tiles' times: `rest` tiles and `edges` quarters of

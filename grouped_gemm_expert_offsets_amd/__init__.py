@@ -945,7 +945,7 @@ def kgw_newton_schulz(G: torch.Tensor, *, steps: int = 5, coefficients=NEWTON_SC
 
     G is fp32, bf16 or fp16 with contiguous rows (any row and batch stride), as kgw_wgrad_* writes
     it.  `coefficients` is one (a, b, c) or one per step.  The result has `out_dtype` (default: G's): bf16
-    runs one fp16 product where fp32 and fp16 run three and keep fp32's precision.  `workspace`: a uint8
+    runs one fp16 product where fp32 and fp16 (and short sides up to 128) run three and keep fp32's precision.  `workspace`: a uint8
     tensor of kgw_newton_schulz_workspace_bytes bytes to reuse; allocated here when None.
     """
     code = _out_code(G.dtype)

@@ -15,6 +15,14 @@
 // address), so odd row lengths and unaligned views need no path of their own; the last
 // H % (16 / element size) elements of a row move one by one.  Sums are fp32, in the order of
 // j (unpermute) or a fixed tree over the row (dw), so results do not depend on scheduling.
+//
+// The row kernels are bound by HBM.  On this card a large copy moves 4.9 TB/s and a fill 6.9;
+// 32768 x 8 tokens, 7168 bf16:
+//   permute          4.29 GB  786 us  5.4 TB/s (7/8 of it writes)
+//   unpermute        4.23 GB  739 us  5.7 TB/s
+//   unpermute grad   8.05 GB 1560 us  5.1 TB/s
+// Small ones are bound by the launch: 4099 x 6 tokens of 1001 fp32 take 8.1 us, their 41 MB from the
+// Infinity Cache.
 #include <type_traits>
 
 #include "kgw_device.h"
@@ -48,7 +56,8 @@ __device__ __forceinline__ void clear_src(const MoeSortParams& p) {
     for (int64_t r = 4 * quads + at; r < p.rows; r += step) p.src_of[r] = -1;
 }
 
-// Workgroup b's assignments [b * chunk, (b + 1) * chunk) counted by expert into hist[b][.].
+// Workgroup b's assignments [b * chunk, (b + 1) * chunk) counted by expert into hist[b][.].  Bound by
+// latencies: 3.0 us for 262144 assignments (2 MB of ids).
 template <class ID>
 __global__ __launch_bounds__(SORT_NT) void moe_count_kernel(MoeSortParams p) {
     __shared__ int count[kMoeMaxExperts];
@@ -71,7 +80,8 @@ __global__ __launch_bounds__(SORT_NT) void moe_count_kernel(MoeSortParams p) {
 // waits between workgroups.  Within a wave the lanes of one expert find each other by
 // ballots over the bits of the id; a lane's rank is the number of earlier such lanes, and the
 // wave's own row of 16-bit counters carries the ranks on.  ALONE: one workgroup does it all,
-// with no counts from a first launch.
+// with no counts from a first launch.  Bound by latencies: 7.2 us for 262144 assignments to 32 experts
+// (128 workgroups), 5.8 us for 512 to 256 (one).
 template <class ID, bool ALONE>
 __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(MoeSortParams p) {
     __shared__ uint16_t wave_count[SORT_WAVES * kMoeMaxExperts];   // [wave][expert], at most SORT_SUB
@@ -207,8 +217,8 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(MoeSortParams p) {
 // ----------------------------------------------------------------------------
 constexpr int ROW_NT = 256;
 constexpr int ROW_WAVES = ROW_NT / 64;
-constexpr int PAD_ROWS = 2;      // rows whose source one wave looks up before zeroing the empty ones (33024 rows of 7168
-                                 // bf16, nearly all empty: 16 take 96 us, 4 91, 2 89.4, 1 89; 33024 copied ones 786 with 2, 794 with 1)
+constexpr int PAD_ROWS = 2;      // rows whose source one wave looks up before zeroing the empty ones (33024 rows of 7168 bf16, nearly
+                                 // all empty: 16 take 96 us, 4 91, 2 89.4, 1 89; 262144 copied ones 789 with 2, 794 with 1)
 
 // 16 bytes at element alignment.
 typedef i32x4 Piece2 __attribute__((aligned(2)));
@@ -291,7 +301,7 @@ __device__ __forceinline__ void zero_empty_rows(const MoeRowsParams& p, char* ou
 }
 
 // One wave moves SEG pieces a lane of one token's row to the token's rows; the waves past the
-// tokens' zero the empty rows.
+// tokens' zero the empty rows.  512 rows of 33024 copied and the others zeroed: 87 us, 5.4 TB/s.
 constexpr int SEG = 2;
 template <int DT>
 __global__ __launch_bounds__(ROW_NT) void moe_permute_kernel(MoeRowsParams p) {
@@ -327,7 +337,8 @@ __global__ __launch_bounds__(ROW_NT) void moe_permute_kernel(MoeRowsParams p) {
     }
 }
 
-// One wave sums USEG pieces a lane of one token's rows.
+// One wave sums USEG pieces a lane of one token's rows, four rows' loads on their way at a time (one
+// piece a lane, or four, were slower).
 constexpr int USEG = 2;
 template <int DT, bool WEIGHTED, bool STREAM>
 __global__ __launch_bounds__(ROW_NT) void moe_unpermute_kernel(MoeRowsParams p) {
@@ -372,7 +383,9 @@ __global__ __launch_bounds__(ROW_NT) void moe_unpermute_kernel(MoeRowsParams p) 
 
 // One workgroup a token: its dout row stays in registers (GSEG pieces a thread; longer rows are
 // read again for every j) while its k rows of y are read, reduced against it and the k rows of dy
-// written.  The workgroups past the tokens' zero the empty rows of dy.
+// written.  The workgroups past the tokens' zero the empty rows of dy.  A wave a token would need no LDS
+// for the dot products but four times the registers for the row; a workgroup moves 5.6 TB/s (16384 x 2
+// tokens, 4096 bf16: 0.69 GB in 122 us).
 constexpr int GSEG = 4;
 template <int DT, bool STREAM>
 __global__ __launch_bounds__(ROW_NT) void moe_unpermute_grad_kernel(MoeRowsParams p) {

@@ -5,8 +5,8 @@
 //     A = X X^T,   B = b A + c A A,   X <- a X + B X,   `steps` times
 //
 // The iterate is held as two fp16 planes, X = (hi + lo) / 2^13: hi is X rounded to 11 bits, lo
-// the remainder rounded again, 22 bits and more together, so the linear term a X, which multiplies
-// small singular values by a at every step, loses nothing.  The products run on the matrix cores in fp16
+// the remainder rounded again, 22 bits together, so the linear term a X, which multiplies
+// small singular values by a at every step, keeps those.  The products run on the matrix cores in fp16
 // with fp32 sums:
 //   one product each (results rounded to bf16): A = hi hi^T, B from fp16 A, B hi.  The
 //     operands' rounding (2^-12) enters only through B X, which is small where the singular values are, and
@@ -18,7 +18,15 @@
 // coefficients, below 8 allowed), A * 2^10 (below 64) and B * 2^7 (below 512).
 //
 // A and A A are symmetric: only tiles on and below the diagonal are computed and their mirror
-// images written along.
+// images written along, which leaves 3 r^2 c + r^3 multiply-adds of a step's 4 r^2 c + 2 r^3 over two.
+//
+// What bounds it: 8 x 7168 x 4096 takes 16.7 ms to bf16 (17.2 TFLOP with the halves counted, 1.03 PFLOP/s;
+// the library's 8192^3 fp16 product runs at 1.09 here) and 39 ms to fp32 (1.32 PFLOP/s).  There it is the
+// card's power: the matrix cores are busy 60 to 76% of the time at 1.6 GHz, and with matrices of zeros,
+// whose products cost less energy, the same launches take 14.4 and 28.3 ms.  Small ones are bound by
+// their 17 launches and by one tile's way through K: 4 x 256 x 512 to fp32 125 us.
+//
+// Sides up to 128 take the kernels of kgw_newton_narrow.hip.
 #include "kgw_newton_device.h"
 
 namespace kgw {
@@ -57,7 +65,7 @@ __device__ __forceinline__ void store_planes(const float (&v)[8], uint16_t* out,
 // |G|_F and the first iterate
 // ----------------------------------------------------------------------------
 // Sum of squares of this workgroup's share of one matrix, in 64 bits: gradients may be so large or
-// small that their squares leave fp32's range.
+// small that their squares leave fp32's range.  Bound by HBM: 93 us for 8 x 7168 x 4096 bf16, 5.1 TB/s.
 template <int DT>
 __global__ __launch_bounds__(NT) void newton_norm_kernel(NewtonParams p) {
     __shared__ double sums[NT / 64];
@@ -81,7 +89,8 @@ __global__ __launch_bounds__(NT) void newton_norm_kernel(NewtonParams p) {
     if (tid == 0) p.parts[(int64_t)b * kNewtonParts + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
 }
 
-// One 64 x 64 tile of the padded first iterate.
+// One 64 x 64 tile of the padded first iterate.  Bound by HBM: reads 2 bytes an element and writes 4,
+// 262 us for 8 x 7168 x 4096 bf16, 5.4 TB/s; transposed through LDS it takes as long.
 template <int DT, bool SPLIT, bool TALL>
 __global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, int64_t R, int64_t C) {
     __shared__ float tile[TALL ? 64 : 1][65];
@@ -281,7 +290,7 @@ __device__ bool join_parts(const NewtonGemm& p, char* smem, int tile, int part, 
 //
 // A stage is four (six) groups of matrix products; each group's fragments are read while the group before
 // multiplies.  Before the last group every read of the stage is done, so the barrier that hands the
-// slot over stands there, and the next stage's first fragments and the loads of the one after
+// slot over stands there, and the next stage's first fragments and the loads that refill the
 // ring go out under the last group's products.
 template <int TILE, int WAVES, int SLOTS, bool SPLIT, bool JOIN, NewtonProduct KIND>
 __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int b, int64_t m0, int64_t n0, int turn,
@@ -710,25 +719,27 @@ __device__ __forceinline__ void quarter_of(const NewtonGemm& p, int index, int& 
     }
 }
 
-template <bool SPLIT>
 constexpr int kBigWaves = 8;
 
-// 256 x 256 tiles; the items past p.whole are quarters of one.
+// 256 x 256 tiles; the items past p.whole are quarters of one.  Eight waves of 128 x 64: a wave's sums
+// take half its registers and two waves a SIMD cover each other's waits (four waves of 128 x 128 need fewer LDS
+// reads, but X X^T of 8 x 4096 x 7168 took 1184 us instead of 1046).  Now, one product: X X^T 904 us, A A 532,
+// B X 1820 (1.06 PFLOP/s), the last one 1921 transposed and 1766 not; power bounds them (see the top).
 template <bool SPLIT, NewtonProduct KIND>
-__global__ __launch_bounds__(64 * kBigWaves<SPLIT>, kBigWaves<SPLIT> / 4) void newton_big_kernel(NewtonGemm p) {
+__global__ __launch_bounds__(64 * kBigWaves, kBigWaves / 4) void newton_big_kernel(NewtonGemm p) {
     __shared__ __attribute__((aligned(1024))) char smem[5 * 256 * 128];
     const int bid = blockIdx.x;
     int b, tm, tn, turn;
     if (bid < p.whole) {
         tile_of<KIND>(p, item_of(bid, p.whole, p.num_xcds), b, tm, tn);
         turn = turn_of<SPLIT, KIND>(p, tm, 256);
-        newton_tile<256, kBigWaves<SPLIT>, 5, SPLIT, false, KIND>(p, smem, b, (int64_t)tm * 256, (int64_t)tn * 256, turn);
+        newton_tile<256, kBigWaves, 5, SPLIT, false, KIND>(p, smem, b, (int64_t)tm * 256, (int64_t)tn * 256, turn);
     } else {
         int64_t m0, n0;
         quarter_of<KIND>(p, bid - p.whole, b, m0, n0);
         if (!updates(KIND) && n0 > m0) return;         // the mirror image of another quarter
         turn = turn_of<SPLIT, KIND>(p, (int)(m0 / 256), 256);
-        newton_tile<128, kBigWaves<SPLIT>, 10, SPLIT, false, KIND>(p, smem, b, m0, n0, turn);
+        newton_tile<128, kBigWaves, 10, SPLIT, false, KIND>(p, smem, b, m0, n0, turn);
     }
 }
 
@@ -766,16 +777,20 @@ void launch_small(NewtonGemm g, int tiles, hipStream_t stream) {
     g.parts = parts > 1 ? (int32_t)parts : 1;
     g.items = tiles * g.parts;
     const dim3 grid((uint32_t)g.items);
+    constexpr uint32_t alone = 64 * kSmallWaves<TILE, false>, paired = 64 * kSmallWaves<TILE, true>;
     if constexpr (!updates(KIND)) {
         if (g.parts > 1) {
-            hipLaunchKernelGGL((newton_small_kernel<TILE, false, true, SPLIT, KIND>), grid, dim3((64 * kSmallWaves<TILE, false>)), 0, stream, g);
+            hipLaunchKernelGGL((newton_small_kernel<TILE, false, true, SPLIT, KIND>), grid, dim3(alone), 0,
+                           stream, g);
             return;
         }
     }
     if (g.items > kNewtonSlabs)
-        hipLaunchKernelGGL((newton_small_kernel<TILE, true, false, SPLIT, KIND>), grid, dim3((64 * kSmallWaves<TILE, true>)), 0, stream, g);
+        hipLaunchKernelGGL((newton_small_kernel<TILE, true, false, SPLIT, KIND>), grid, dim3(paired), 0,
+                           stream, g);
     else
-        hipLaunchKernelGGL((newton_small_kernel<TILE, false, false, SPLIT, KIND>), grid, dim3((64 * kSmallWaves<TILE, false>)), 0, stream, g);
+        hipLaunchKernelGGL((newton_small_kernel<TILE, false, false, SPLIT, KIND>), grid, dim3(alone), 0,
+                           stream, g);
 }
 
 // Time of what follows the whole rounds of 256 x 256 tiles, in tiles' times: `rest` tiles and `edges` quarters of
@@ -824,7 +839,7 @@ void launch_product(NewtonGemm g, int tile, int num_cus, hipStream_t stream) {
         const int rest = tiles % num_cus, edges = g.batch * g.strips;
         g.whole = rest_in_quarters(rest, edges, num_cus) < rest_kept(rest, edges, num_cus) ? tiles - rest : tiles;
         g.items = g.whole + 4 * (tiles - g.whole) + edges;
-        hipLaunchKernelGGL((newton_big_kernel<SPLIT, KIND>), dim3((uint32_t)g.items), dim3(64 * kBigWaves<SPLIT>), 0,
+        hipLaunchKernelGGL((newton_big_kernel<SPLIT, KIND>), dim3((uint32_t)g.items), dim3(64 * kBigWaves), 0,
                            stream, g);
     } else {
         if (tile == 128) launch_small<128, SPLIT, KIND>(g, tiles, stream);
@@ -909,9 +924,11 @@ NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
         return plan;
     }
     plan.split = out_dtype != kOutBf16;
-    // 256 x 256 tiles where the update alone has one for every CU, smaller ones where it has less
+    // 64-edged tiles while 128-edged ones would leave a quarter of the CUs idle in the update (their number: 2 x 1024 x
+    // 1024, 128 of them: 171 against 194 us; 3 x 900 x 900 to fp32, 192: 340 against 364; 1700 x 1700, 196:
+    // 286 against 283, to fp32 537 against 513); above, what step_cost() puts lower of 256 and 128.
     auto tiles = [&](int64_t edge) { return ((r + edge - 1) / edge) * ((c + edge - 1) / edge) * batch; };
-    plan.tile = tiles(128) < 256 ? 64 : r >= 256 && step_cost(batch, r, c, 256) < step_cost(batch, r, c, 128) ? 256 : 128;
+    plan.tile = tiles(128) <= 192 ? 64 : r >= 256 && step_cost(batch, r, c, 256) < step_cost(batch, r, c, 128) ? 256 : 128;
     const int64_t edge = plan.tile == 64 ? 64 : 128;    // an odd half tile at an end is taken in quarters
     plan.r = (r + edge - 1) / edge * edge;
     plan.c = (c + edge - 1) / edge * edge;

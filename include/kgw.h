@@ -626,11 +626,13 @@ kgw_status_t kgw_moe_unpermute_grad(const void* dout, int64_t ld_dout, const voi
  *   G        (batch, m, n) of `dtype`, rows contiguous, `ld` >= n elements apart, matrices
  *            `stride` elements apart (any ld and stride; the dense gradient has n and m * n).
  *   out      (batch, m, n) of `out_dtype`, contiguous; may not overlap G.
- *   workspace  kgw_newton_schulz_workspace_bytes() bytes, 256-byte aligned, no initial contents.
+ *   workspace  kgw_newton_schulz_workspace_bytes() bytes, 256-byte aligned, no initial contents; not
+ *            to be used by another call that may run at the same time.
  *
  * Precision follows out_dtype.  KGW_OUT_BF16: operands of the products are rounded to fp16 and the
- * linear term a X keeps 22 bits, which leaves errors below bf16's own rounding.  KGW_OUT_FP32 and
- * KGW_OUT_FP16: every operand keeps 22 bits, with the errors of fp32 arithmetic, at three times the products.
+ * linear term a X keeps 22 bits, which leaves errors of the size of bf16's own rounding.  KGW_OUT_FP32
+ * and KGW_OUT_FP16, and every type where min(m, n) <= 128: every operand keeps 22 bits, with the errors of
+ * fp32 arithmetic, at three times the products.
  * Sums are fp32, the norm's 64 bits.  The iterates' singular values must stay below 8
  * (the usual coefficients keep them below 1.3).  A zero matrix gives zeros (eps > 0); infinities or NaN
  * in a matrix give NaN in that matrix alone.  Deterministic.

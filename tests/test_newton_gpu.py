@@ -83,7 +83,8 @@ def test_against_the_iteration(batch, m, n, dtype, out):
 # or none; short sides with one workgroup a matrix, a launch a step, and several chunks a workgroup.
 WAYS = [(4, 256, 512), (1, 200, 7000), (1, 4096, 512), (64, 300, 500), (3, 1777, 1000), (1, 1536, 2900), (10, 381, 3323),
         (8, 4219, 381), (10, 3451, 509), (10, 509, 2555), (5, 1149, 3451), (24, 1021, 1019), (24, 1147, 1149), (12, 1531, 1405),
-        (3, 20, 30), (70, 400, 60), (130, 40, 300), (40, 60, 2100), (20, 3500, 120), (4, 128, 128)]
+        (3, 20, 30), (70, 400, 60), (130, 40, 300), (40, 60, 2100), (20, 3500, 120), (4, 128, 128), (1, 1700, 1690),
+        (1, 1690, 1700)]
 
 
 @pytest.mark.parametrize("batch,m,n", WAYS)

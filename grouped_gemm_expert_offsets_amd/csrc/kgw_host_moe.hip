@@ -53,9 +53,13 @@ int64_t kgw_moe_rows(int64_t tokens, int32_t topk, int32_t num_experts, int32_t 
 
 size_t kgw_moe_sort_workspace_bytes(int64_t tokens, int32_t topk, int32_t num_experts) {
     if (tokens < 0 || topk < 1 || num_experts < 1 || tokens > INT32_MAX / topk) return 0;
-    int32_t groups;
+    const int64_t assignments = tokens * topk;
+    int32_t groups, fewer;
     int64_t chunk;
-    kgw::moe_sort_plan(tokens * topk, &groups, &chunk);
+    kgw::moe_sort_plan(assignments, &groups, &chunk);
+    // never less than for fewer tokens, so that a workspace for the most serves all
+    kgw::moe_sort_plan(assignments < kgw::kMoeSortShort ? assignments : kgw::kMoeSortShort, &fewer, &chunk);
+    if (fewer > groups) groups = fewer;
     return groups > 1 ? (size_t)groups * (size_t)num_experts * sizeof(int32_t) : 0;
 }
 

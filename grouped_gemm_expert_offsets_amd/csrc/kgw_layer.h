@@ -48,6 +48,7 @@ struct MoeRowsParams {
 constexpr int kMoePermute = 0, kMoeUnpermute = 1, kMoeUnpermuteGrad = 2;
 
 // Workgroups of the sort and the assignments of each.
+constexpr int64_t kMoeSortShort = 65536;    // up to here smaller shares, so that up to 64 workgroups have one
 void moe_sort_plan(int64_t assignments, int32_t* groups, int64_t* chunk);
 hipError_t launch_moe_sort(const MoeSortParams& p, bool wide_ids, hipStream_t stream);
 hipError_t launch_moe_rows(const MoeRowsParams& p, int op, int dtype, hipStream_t stream);

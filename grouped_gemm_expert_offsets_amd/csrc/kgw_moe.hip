@@ -36,8 +36,12 @@ namespace {
 // ----------------------------------------------------------------------------
 constexpr int SORT_NT = 1024;
 constexpr int SORT_WAVES = SORT_NT / 64;
-constexpr int SORT_PER_LANE = 2;
-constexpr int SORT_SUB = SORT_NT * SORT_PER_LANE;   // assignments ranked at a time by one workgroup
+// Assignments a lane that one workgroup ranks at a time.  Up to 2048 assignments one workgroup does it all (2048 to 256
+// experts: 7.1 us, two launches 7.7; 4096 in two rounds 10.4, two launches 7.6).  Beyond, one a lane
+// makes more workgroups (32768 to 64 experts: 7.6 us, with two 8.5) until each has several rounds: 131072 to 256
+// experts 11.2 us with one, 10.9 with two.
+constexpr int64_t kSortAlone = 2 * SORT_NT;
+constexpr int sort_per_lane(int64_t assignments) { return assignments > kSortAlone && assignments <= kMoeSortShort ? 1 : 2; }
 
 // Expert of assignment i, or -1 when it is not one of the num_experts held here.
 template <class ID>
@@ -82,9 +86,10 @@ __global__ __launch_bounds__(SORT_NT) void moe_count_kernel(MoeSortParams p) {
 // wave's own row of 16-bit counters carries the ranks on.  ALONE: one workgroup does it all,
 // with no counts from a first launch.  Bound by latencies: 7.2 us for 262144 assignments to 32 experts
 // (128 workgroups), 5.8 us for 512 to 256 (one).
-template <class ID, bool ALONE>
+template <class ID, int PER_LANE, bool ALONE>
 __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(MoeSortParams p) {
-    __shared__ uint16_t wave_count[SORT_WAVES * kMoeMaxExperts];   // [wave][expert], at most SORT_SUB
+    constexpr int SUB = SORT_NT * PER_LANE;
+    __shared__ uint16_t wave_count[SORT_WAVES * kMoeMaxExperts];   // [wave][expert], at most SUB
     __shared__ int base[kMoeMaxExperts];                           // next row of every expert
     __shared__ int total[kMoeMaxExperts];
     __shared__ int wave_sum[SORT_WAVES];
@@ -154,20 +159,22 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(MoeSortParams p) {
         start += padded[u];
     }
 
-    for (int64_t sub = first; sub < last; sub += SORT_SUB) {
+    for (int64_t sub = first; sub < last; sub += SUB) {
         for (int i = tid; i < SORT_WAVES * E; i += SORT_NT) wave_count[i] = 0;
         __syncthreads();
-        // each wave ranks SORT_PER_LANE runs of 64 consecutive assignments
-        int expert[SORT_PER_LANE], rank[SORT_PER_LANE];
+        // each wave ranks PER_LANE runs of 64 consecutive assignments
+        int expert[PER_LANE], rank[PER_LANE];
         uint16_t* const mine = wave_count + wave * E;
 #pragma unroll
-        for (int u = 0; u < SORT_PER_LANE; ++u) {
-            const int64_t i = sub + (wave * SORT_PER_LANE + u) * 64 + lane;
+        for (int u = 0; u < PER_LANE; ++u) {
+            const int64_t i = sub + (wave * PER_LANE + u) * 64 + lane;
             expert[u] = i < last ? expert_of((const ID*)p.ids, i, E) : -1;
         }
 #pragma unroll
-        for (int u = 0; u < SORT_PER_LANE; ++u) {
+        for (int u = 0; u < PER_LANE; ++u) {
             const int e = expert[u];
+            rank[u] = 0;
+            if (sub + (wave * PER_LANE + u) * 64 >= last) continue;
             uint64_t peers = __ballot(e >= 0);
             for (int bit = 0; bit < p.id_bits; ++bit) {
                 const uint64_t ones = __ballot((e >> bit) & 1);
@@ -195,8 +202,8 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(MoeSortParams p) {
         }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < SORT_PER_LANE; ++u) {
-            const int64_t i = sub + (wave * SORT_PER_LANE + u) * 64 + lane;
+        for (int u = 0; u < PER_LANE; ++u) {
+            const int64_t i = sub + (wave * PER_LANE + u) * 64 + lane;
             if (i >= last) continue;
             int row = -1;
             if (expert[u] >= 0) {
@@ -456,11 +463,14 @@ __global__ __launch_bounds__(ROW_NT) void moe_unpermute_grad_kernel(MoeRowsParam
 template <class ID>
 void launch_sort(const MoeSortParams& p, hipStream_t stream) {
     if (p.groups == 1) {
-        hipLaunchKernelGGL((moe_place_kernel<ID, true>), dim3(1), dim3(SORT_NT), 0, stream, p);
-    } else {
-        hipLaunchKernelGGL((moe_count_kernel<ID>), dim3(p.groups), dim3(SORT_NT), 0, stream, p);
-        hipLaunchKernelGGL((moe_place_kernel<ID, false>), dim3(p.groups), dim3(SORT_NT), 0, stream, p);
+        hipLaunchKernelGGL((moe_place_kernel<ID, 2, true>), dim3(1), dim3(SORT_NT), 0, stream, p);
+        return;
     }
+    hipLaunchKernelGGL((moe_count_kernel<ID>), dim3(p.groups), dim3(SORT_NT), 0, stream, p);
+    if (sort_per_lane(p.assignments) == 1)
+        hipLaunchKernelGGL((moe_place_kernel<ID, 1, false>), dim3(p.groups), dim3(SORT_NT), 0, stream, p);
+    else
+        hipLaunchKernelGGL((moe_place_kernel<ID, 2, false>), dim3(p.groups), dim3(SORT_NT), 0, stream, p);
 }
 
 // Pieces of a row, at least one so that a short row's tail has a wave.
@@ -505,11 +515,11 @@ void launch_rows(MoeRowsParams p, int op, hipStream_t stream) {
 }  // namespace
 
 void moe_sort_plan(int64_t assignments, int32_t* groups, int64_t* chunk) {
-    int64_t g = (assignments + SORT_SUB - 1) / SORT_SUB;
-    if (g <= 2) g = 1;
+    const int64_t sub = SORT_NT * sort_per_lane(assignments);
+    int64_t g = assignments <= kSortAlone ? 1 : (assignments + sub - 1) / sub;
     if (g > kMoeSortGroups) g = kMoeSortGroups;
     const int64_t per = (assignments + g - 1) / g;
-    *chunk = (per + SORT_SUB - 1) / SORT_SUB * SORT_SUB;
+    *chunk = (per + sub - 1) / sub * sub;
     *groups = (int32_t)g;
 }
 

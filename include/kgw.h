@@ -554,7 +554,7 @@ kgw_status_t kgw_device_info(int32_t* num_cus, int32_t* is_gfx950, int32_t* num_
  */
 int64_t kgw_moe_rows(int64_t tokens, int32_t topk, int32_t num_experts, int32_t alignment);
 
-/* Device scratch of kgw_moe_sort, 4-byte aligned, no initial contents (0: none). */
+/* Device scratch of kgw_moe_sort, 4-byte aligned, no initial contents (0: none); enough for fewer tokens too. */
 size_t kgw_moe_sort_workspace_bytes(int64_t tokens, int32_t topk, int32_t num_experts);
 
 /*

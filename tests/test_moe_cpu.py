@@ -33,6 +33,8 @@ def test_sort_workspace(lib):
     assert lib.kgw_moe_sort_workspace_bytes(32768, 8, 32) == 128 * 32 * 4
     assert lib.kgw_moe_sort_workspace_bytes(10 ** 7, 8, 32) == 128 * 32 * 4      # never more workgroups
     assert lib.kgw_moe_sort_workspace_bytes(-1, 8, 32) == 0
+    sizes = [lib.kgw_moe_sort_workspace_bytes(t, 2, 7) for t in range(0, 200000, 331)]
+    assert sizes == sorted(sizes)                                                # enough for fewer tokens too
 
 
 def sort(lib, ids=P, id_bytes=8, tokens=64, k=8, E=16, align=128, rows=4096, counts=P, offsets=P, row_of=P, src_of=P,

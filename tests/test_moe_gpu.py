@@ -72,7 +72,8 @@ def random_ids(tokens, k, E, seed, dtype=torch.int64, spread=None):
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 @pytest.mark.parametrize("tokens,k,E,align", [(1, 1, 1, 128), (1, 8, 8, 128), (7, 3, 5, 1), (63, 1, 2, 256), (64, 8, 256, 128),
                                               (500, 8, 33, 128), (2049, 2, 64, 256), (5000, 3, 7, 128),
-                                              (20011, 2, 300, 128), (3000, 4, 2048, 128)])
+                                              (20011, 2, 300, 128), (3000, 4, 2048, 128), (512, 4, 40, 128),
+                                              (683, 3, 40, 128), (8192, 8, 70, 128), (8193, 8, 70, 128)])
 def test_sort(tokens, k, E, align, dtype):
     check_sort(random_ids(tokens, k, E, tokens + E, dtype), E, align)
 

@@ -838,21 +838,19 @@ def kgw_moe_sort(ids: torch.Tensor, num_experts: int, *, alignment: int = FP8_TO
     device = _on_gpu(ids, "ids")
     lib = load_library()
     need = lib.kgw_moe_sort_workspace_bytes(tokens, topk, E)
-    # one allocation for all results: four would take a third of a short call's time
+    # one allocation for all results and the workspace: five would take a third of a short call's time
     n = tokens * topk
-    results = torch.empty(rows + n + 2 * E, dtype=torch.int32, device=device)
-    src_of, row_of, counts, offsets = results.split((rows, n, E, E))
-    row_of = row_of.view(tokens, topk)
-    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    results = torch.empty(rows + n + 2 * E + need // 4, dtype=torch.int32, device=device)
+    src_of, row_of, counts, offsets, _ = results.split((rows, n, E, E, need // 4))
     if stream is not None:
         results.record_stream(stream)
-        if ws is not None:
-            ws.record_stream(stream)
-    st = lib.kgw_moe_sort(ids.data_ptr(), ids.element_size(), tokens, topk, E, int(alignment), rows,
-                          counts.data_ptr(), offsets.data_ptr(), row_of.data_ptr(), src_of.data_ptr(), _ptr(ws), need,
+    at = results.data_ptr()
+    counts_at = at + 4 * (rows + n)
+    st = lib.kgw_moe_sort(ids.data_ptr(), ids.element_size(), tokens, topk, E, int(alignment), rows, counts_at,
+                          counts_at + 4 * E, at + 4 * rows, at, counts_at + 8 * E if need else None, need,
                           _launch_stream(stream, device))
     _check(st, "kgw_moe_sort")
-    return counts, offsets, row_of, src_of
+    return counts, offsets, row_of.view(tokens, topk), src_of
 
 
 def kgw_moe_permute(x: torch.Tensor, row_of: torch.Tensor, src_of: torch.Tensor,

@@ -173,6 +173,29 @@ def _workspace(E: int, hidden: int, n: int, T: int, fp8: bool, device, stream, s
     return ws, nbytes
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory that a call on `stream` (None: the current one) writes first.
+
+    It has to be that stream's: a block that the allocator hands out for the current stream may
+    still be in use by work queued there, which `stream` does not wait for.
+    """
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(caller)        # whose work uses the result next
+    return t
+
+
+def _used_on(stream, *tensors: Optional[torch.Tensor]):
+    """Keeps the caller's tensors alive for the pending work of the launch stream."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else int(t.data_ptr())
 
@@ -807,10 +830,7 @@ def _weights(t: torch.Tensor, row_of: torch.Tensor, what: str = "weights"):
 
 def _result(out: Optional[torch.Tensor], shape, dtype, device, what: str, stream) -> torch.Tensor:
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-        if stream is not None:
-            out.record_stream(stream)      # keep it alive for the launch stream's pending work
-        return out
+        return _empty(shape, dtype, device, stream)
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
     return out
@@ -840,10 +860,9 @@ def kgw_moe_sort(ids: torch.Tensor, num_experts: int, *, alignment: int = FP8_TO
     need = lib.kgw_moe_sort_workspace_bytes(tokens, topk, E)
     # one allocation for all results and the workspace: five would take a third of a short call's time
     n = tokens * topk
-    results = torch.empty(rows + n + 2 * E + need // 4, dtype=torch.int32, device=device)
+    results = _empty(rows + n + 2 * E + need // 4, torch.int32, device, stream)
     src_of, row_of, counts, offsets, _ = results.split((rows, n, E, E, need // 4))
-    if stream is not None:
-        results.record_stream(stream)
+    _used_on(stream, ids)
     at = results.data_ptr()
     counts_at = at + 4 * (rows + n)
     st = lib.kgw_moe_sort(ids.data_ptr(), ids.element_size(), tokens, topk, E, int(alignment), rows, counts_at,
@@ -869,6 +888,7 @@ def kgw_moe_permute(x: torch.Tensor, row_of: torch.Tensor, src_of: torch.Tensor,
         raise ValueError(f"row_of has {row_of.shape[0]} tokens, x has {tokens}")
     rows = src_of.shape[0]
     out = _result(out, (rows, hidden), x.dtype, device, "out", stream)
+    _used_on(stream, x, row_of, src_of, out)
     st = load_library().kgw_moe_permute(x.data_ptr(), ld, code, row_of.data_ptr(), src_of.data_ptr(), tokens,
                                         row_of.shape[1], rows, hidden, out.data_ptr(), _launch_stream(stream, device))
     _check(st, "kgw_moe_permute")
@@ -891,6 +911,7 @@ def kgw_moe_unpermute(y: torch.Tensor, row_of: torch.Tensor, weights: Optional[t
     rows, hidden = y.shape
     tokens, topk = row_of.shape
     out = _result(out, (tokens, hidden), y.dtype, device, "out", stream)
+    _used_on(stream, y, row_of, weights, out)
     st = load_library().kgw_moe_unpermute(y.data_ptr(), ld, code, row_of.data_ptr(), _ptr(weights), tokens, topk,
                                           rows, hidden, out.data_ptr(), _launch_stream(stream, device))
     _check(st, "kgw_moe_unpermute")
@@ -920,6 +941,7 @@ def kgw_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_of: torch.Te
         raise ValueError(f"src_of has {src_of.shape[0]} rows, y has {rows}")
     dy = _result(dy, (rows, hidden), y.dtype, device, "dy", stream)
     dweights = _result(dweights, (tokens, topk), torch.float32, device, "dweights", stream)
+    _used_on(stream, dout, y, row_of, src_of, weights, dy, dweights)
     st = load_library().kgw_moe_unpermute_grad(dout.data_ptr(), ld_d, y.data_ptr(), ld_y, code, row_of.data_ptr(),
                                                src_of.data_ptr(), weights.data_ptr(), tokens, topk, rows, hidden,
                                                dy.data_ptr(), dweights.data_ptr(), _launch_stream(stream, device))
@@ -974,11 +996,10 @@ def kgw_newton_schulz(G: torch.Tensor, *, steps: int = 5, coefficients=NEWTON_SC
     lib = load_library()
     need = lib.kgw_newton_schulz_workspace_bytes(batch, m, n, out_code)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _empty(need, torch.uint8, device, stream)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
         raise ValueError("workspace must be a contiguous uint8 tensor on G's device")
+    _used_on(stream, G, out, workspace)
     st = lib.kgw_newton_schulz(G.data_ptr(), ld, stride, code, batch, m, n, steps,
                                (ctypes.c_float * (3 * steps))(*values), eps, out.data_ptr(), out_code,
                                workspace.data_ptr(), workspace.numel(), _launch_stream(stream, device))

@@ -167,10 +167,7 @@ def _workspace(E: int, hidden: int, n: int, T: int, fp8: bool, device, stream, s
     nbytes = kgw_workspace_bytes(E, hidden, n, T, fp8)
     if nbytes == 0:
         return None, 0
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)   # keep it alive for the launch stream's pending work
-    return ws, nbytes
+    return _empty(nbytes, torch.uint8, device, stream), nbytes
 
 
 def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
@@ -210,11 +207,11 @@ def _out_code(dtype: torch.dtype) -> int:
     raise ValueError(f"output dtype must be float32, bfloat16 or float16, got {dtype}")
 
 
-def _prepare_out(out, E, hidden, n, out_dtype, accumulate, device):
+def _prepare_out(out, E, hidden, n, out_dtype, accumulate, device, stream):
     if out is None:
         if accumulate:
             raise ValueError("accumulate=True needs an initialised `out`")
-        return torch.empty((E, hidden, n), dtype=out_dtype, device=device)
+        return _empty((E, hidden, n), out_dtype, device, stream)
     if tuple(out.shape) != (E, hidden, n):
         raise ValueError(f"out must have shape {(E, hidden, n)}, got {tuple(out.shape)}")
     if not out.is_contiguous() or out.device != device:
@@ -274,10 +271,11 @@ def kgw_wgrad_bf16(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out:
     if out is not None:
         out_dtype = out.dtype
     code = _out_code(out_dtype)
-    out = _prepare_out(out, E, hidden, n, out_dtype, accumulate, device)
+    out = _prepare_out(out, E, hidden, n, out_dtype, accumulate, device, stream)
     if validate:
         kgw_validate_offsets(offsets, T, BF16_TOKEN_ALIGN, stream=stream)
     ws, ws_bytes = _workspace(E, hidden, n, T, False, device, stream, split_k)
+    _used_on(stream, A, B, offsets, out)
     st = load_library().kgw_wgrad_bf16(_ptr(A), _ptr(B), _ptr(offsets), E, hidden, n, T, _ptr(out), code,
                                        int(bool(accumulate)), _ptr(ws), ws_bytes, _stream_ptr(stream))
     _check(st, "kgw_wgrad_bf16")
@@ -305,7 +303,8 @@ def kgw_wgrad_bf16_noalloc(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tens
     n = B.shape[1]
     E = offsets.numel()
     code = _out_code(out.dtype)
-    out = _prepare_out(out, E, hidden, n, out.dtype, accumulate, device)
+    out = _prepare_out(out, E, hidden, n, out.dtype, accumulate, device, stream)
+    _used_on(stream, A, B, offsets, out)
     st = load_library().kgw_wgrad_bf16_noalloc(_ptr(A), _ptr(B), _ptr(offsets), E, hidden, n, T, _ptr(out), code,
                                                int(bool(accumulate)), _stream_ptr(stream))
     _check(st, "kgw_wgrad_bf16_noalloc")
@@ -358,6 +357,7 @@ def kgw_wgrad_bf16_ex(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, *
     if validate:
         kgw_validate_offsets(offsets, T, BF16_TOKEN_ALIGN, stream=stream)
     ws, ws_bytes = _workspace(E, hidden, n, T, False, device, stream, split_k)
+    _used_on(stream, A, B, offsets, out, *(outs or ()))
     st = load_library().kgw_wgrad_bf16_ex(_ptr(A), _ptr(B), layout, _ptr(offsets), E, hidden, n, T, _ptr(out),
                                           _ptr(ptrs), code, int(bool(accumulate)), _ptr(ws), ws_bytes,
                                           _stream_ptr(stream))
@@ -380,7 +380,7 @@ def _outputs(out, outs, E, hidden, n, out_dtype, accumulate, device, stream):
     if out is not None:
         out_dtype = out.dtype
     code = _out_code(out_dtype)
-    return _prepare_out(out, E, hidden, n, out_dtype, accumulate, device), None, None, code
+    return _prepare_out(out, E, hidden, n, out_dtype, accumulate, device, stream), None, None, code
 
 
 def kgw_wgrad_fp8(A: torch.Tensor, sfa: torch.Tensor, B: torch.Tensor, sfb: torch.Tensor, offsets: torch.Tensor,
@@ -451,6 +451,7 @@ def kgw_wgrad_fp4(A: torch.Tensor, sfa: torch.Tensor, B: torch.Tensor, sfb: torc
     if validate:
         kgw_validate_offsets(offsets, T, FP4_TOKEN_ALIGN, stream=stream)
     ws, ws_bytes = _workspace(E, hidden, n, T, True, device, stream, split_k)
+    _used_on(stream, A, sfa, B, sfb, offsets, out, *(outs or ()))
     st = load_library().kgw_wgrad_fp4(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(offsets), E, hidden, n, T,
                                       _ptr(out), _ptr(ptrs), code, int(bool(accumulate)), _ptr(ws), ws_bytes,
                                       _stream_ptr(stream))
@@ -510,6 +511,7 @@ def _fp8_call(name, A, sfa, B, sfb, offsets, out, out_dtype, accumulate, validat
         kgw_validate_offsets(offsets, T, FP8_TOKEN_ALIGN, stream=stream)
     fn = getattr(load_library(), name)
     ws, ws_bytes = _workspace(E, hidden, n, T, True, device, stream, split_k)
+    _used_on(stream, A, sfa, B, sfb, offsets, out, *(outs or ()))
     if native is None:
         st = fn(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(offsets), E, hidden, n, T, _ptr(out), code,
                 int(bool(accumulate)), _ptr(ws), ws_bytes, _stream_ptr(stream))
@@ -540,8 +542,9 @@ def kgw_quantize_fp8(x: torch.Tensor, token_axis: int, stream=None,
     if tokens % FP8_TOKEN_ALIGN != 0:
         raise ValueError(f"the token length ({tokens}) must be a multiple of {FP8_TOKEN_ALIGN}")
     shape, sdtype = scale_shape(tokens, other, scale_format)
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    s = torch.empty(shape, dtype=sdtype, device=x.device)
+    q = _empty((rows, cols), torch.uint8, x.device, stream)
+    s = _empty(shape, sdtype, x.device, stream)
+    _used_on(stream, x)
     st = load_library().kgw_quantize_fp8(_ptr(x), rows, cols, int(token_axis), int(scale_format), _ptr(q), _ptr(s),
                                          _stream_ptr(stream))
     _check(st, "kgw_quantize_fp8")
@@ -572,8 +575,9 @@ def kgw_quantize_fp4(x: torch.Tensor, token_axis: int, stream=None,
         shape, sdtype = (tokens // 32, other), torch.uint8
     else:
         shape, sdtype = scale_shape(tokens, other, scale_format)
-    q = torch.empty((other, tokens // 2), dtype=torch.uint8, device=x.device)
-    s = torch.empty(shape, dtype=sdtype, device=x.device)
+    q = _empty((other, tokens // 2), torch.uint8, x.device, stream)
+    s = _empty(shape, sdtype, x.device, stream)
+    _used_on(stream, x)
     st = load_library().kgw_quantize_fp4(_ptr(x), rows, cols, int(token_axis), int(scale_format), _ptr(q), _ptr(s),
                                          _stream_ptr(stream))
     _check(st, "kgw_quantize_fp4")
@@ -616,9 +620,10 @@ def kgw_mgrouped_bf16(A: torch.Tensor, W: torch.Tensor, *, offsets: Optional[tor
     if out is None:
         if accumulate:
             raise ValueError("accumulate=True needs an initialised `out`")
-        out = torch.empty((M, N), dtype=out_dtype, device=device)
+        out = _empty((M, N), out_dtype, device, stream)
     elif tuple(out.shape) != (M, N) or not out.is_contiguous() or out.device != device:
         raise ValueError(f"out must be a contiguous {(M, N)} tensor on the operands' device")
+    _used_on(stream, A, W, idx, out)
     st = load_library().kgw_mgrouped_bf16(_ptr(A), _ptr(W), KGW_LAYOUT_NT if layout == "nt" else KGW_LAYOUT_NN,
                                           _ptr(offsets), _ptr(m_indices), E, M, K, N, _ptr(out), code,
                                           int(bool(accumulate)), _stream_ptr(stream))
@@ -674,9 +679,10 @@ def kgw_mgrouped_fp8(A: torch.Tensor, sa: torch.Tensor, W: torch.Tensor, sw: tor
     if out is None:
         if accumulate:
             raise ValueError("accumulate=True needs an initialised `out`")
-        out = torch.empty((M, N), dtype=out_dtype, device=device)
+        out = _empty((M, N), out_dtype, device, stream)
     elif tuple(out.shape) != (M, N) or not out.is_contiguous() or out.device != device:
         raise ValueError(f"out must be a contiguous {(M, N)} tensor on the operands' device")
+    _used_on(stream, A, sa, W, sw, idx, out)
     st = load_library().kgw_mgrouped_fp8(_ptr(A), _ptr(sa), _ptr(W), _ptr(sw),
                                          KGW_LAYOUT_NT if layout == "nt" else KGW_LAYOUT_NN, _ptr(offsets),
                                          _ptr(m_indices), E, M, K, N, _ptr(out), code, int(bool(accumulate)),
@@ -716,9 +722,10 @@ def kgw_check_offsets(offsets: torch.Tensor, tokens_sum: int, alignment: int,
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous 1-D int32 tensor")
     if result is None:
-        result = torch.empty(1, dtype=torch.int32, device=offsets.device)
+        result = _empty(1, torch.int32, offsets.device, stream)
     elif result.dtype != torch.int32 or result.numel() < 1 or result.device != offsets.device:
         raise ValueError("result must be an int32 tensor on the offsets' device")
+    _used_on(stream, offsets, result)
     st = load_library().kgw_check_offsets(_ptr(offsets), offsets.numel(), int(tokens_sum), int(alignment),
                                           _ptr(result), _stream_ptr(stream))
     _check(st, "kgw_check_offsets")
@@ -732,8 +739,9 @@ def kgw_mfma_ceiling(src: torch.Tensor, kind: int, iters: int = 20000, workgroup
     at).  A measurement helper: it synchronises."""
     if not src.is_cuda or not src.is_contiguous():
         raise ValueError("src must be a contiguous device tensor")
-    cycles = torch.zeros(2 * workgroups, dtype=torch.int64, device=src.device)
     s = torch.cuda.current_stream(src.device) if stream is None else stream
+    with torch.cuda.stream(s):
+        cycles = torch.zeros(2 * workgroups, dtype=torch.int64, device=src.device)
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     start.record(s)
     st = load_library().kgw_mfma_ceiling(_ptr(src), src.numel() * src.element_size(), int(kind), int(iters),

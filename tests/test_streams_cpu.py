@@ -89,6 +89,56 @@ def test_memory_comes_from_the_launch_stream(watch, name):
         assert "launch" in recorded[inputs[k].untyped_storage().data_ptr()], k
 
 
+def operands():
+    offsets = torch.tensor([256, 512], dtype=torch.int32)
+    bytes_ = lambda *shape: torch.zeros(shape, dtype=torch.uint8)  # noqa: E731
+    return dict(a=torch.zeros((32, 512), dtype=torch.bfloat16), b=torch.zeros((512, 64), dtype=torch.bfloat16),
+                a8=bytes_(32, 512), b8=bytes_(512, 64), sa=bytes_(4, 32), sb=bytes_(4, 64), offsets=offsets,
+                a4=bytes_(32, 256), b4=bytes_(64, 256), sa4=index(4, 32), sb4=index(4, 64),
+                rows=torch.zeros((256, 64), dtype=torch.bfloat16), w=torch.zeros((2, 64, 64), dtype=torch.bfloat16),
+                rows8=bytes_(256, 128), w8=bytes_(2, 64, 128), srows=bytes_(1, 256), sw=bytes_(2, 1, 64),
+                out=torch.zeros((2, 32, 64)), one=torch.zeros((32, 64)))
+
+
+# call, the caller's tensors it reads or writes, allocations
+PRODUCT_CALLS = {
+    "wgrad_bf16": (lambda s, t: kgw.kgw_wgrad_bf16(t["a"], t["b"], t["offsets"], stream=s), ("a", "b", "offsets"), 2),
+    "wgrad_bf16_noalloc": (lambda s, t: kgw.kgw_wgrad_bf16_noalloc(t["a"], t["b"], t["offsets"], t["out"], stream=s),
+                           ("a", "b", "offsets", "out"), 0),
+    "wgrad_bf16_ex": (lambda s, t: kgw.kgw_wgrad_bf16_ex(t["a"], t["b"], t["offsets"], stream=s), ("a", "b", "offsets"), 2),
+    "wgrad_bf16_ex outs": (lambda s, t: kgw.kgw_wgrad_bf16_ex(t["a"], t["b"], t["offsets"], outs=[t["one"], None], stream=s),
+                           ("a", "b", "offsets", "one"), 1),
+    "wgrad_fp8": (lambda s, t: kgw.kgw_wgrad_fp8(t["a8"], t["sa"], t["b8"], t["sb"], t["offsets"], stream=s),
+                  ("a8", "sa", "b8", "sb", "offsets"), 2),
+    "wgrad_fp8_native": (lambda s, t: kgw.kgw_wgrad_fp8_native(t["a8"], t["sa"], t["b8"], t["sb"], t["offsets"], stream=s),
+                         ("a8", "sa", "b8", "sb", "offsets"), 2),
+    "wgrad_fp8_ex": (lambda s, t: kgw.kgw_wgrad_fp8_ex(t["a8"], t["sa"], t["b8"], t["sb"], t["offsets"], out=t["out"],
+                                                       stream=s), ("a8", "sa", "b8", "sb", "offsets", "out"), 1),
+    "wgrad_fp4": (lambda s, t: kgw.kgw_wgrad_fp4(t["a4"], t["sa4"], t["b4"], t["sb4"], t["offsets"], stream=s),
+                  ("a4", "sa4", "b4", "sb4", "offsets"), 2),
+    "quantize_fp8": (lambda s, t: kgw.kgw_quantize_fp8(t["a"], 1, stream=s), ("a",), 2),
+    "quantize_fp4": (lambda s, t: kgw.kgw_quantize_fp4(t["a"], 1, stream=s), ("a",), 2),
+    "mgrouped_bf16": (lambda s, t: kgw.kgw_mgrouped_bf16(t["rows"], t["w"], offsets=t["offsets"], stream=s),
+                      ("rows", "w", "offsets"), 1),
+    "mgrouped_fp8": (lambda s, t: kgw.kgw_mgrouped_fp8(t["rows8"], t["srows"], t["w8"], t["sw"], offsets=t["offsets"],
+                                                       stream=s), ("rows8", "srows", "w8", "sw", "offsets"), 1),
+    "check_offsets": (lambda s, t: kgw.kgw_check_offsets(t["offsets"], 512, 256, stream=s), ("offsets",), 1),
+}
+
+
+@pytest.mark.parametrize("name", PRODUCT_CALLS)
+def test_products_take_memory_from_the_launch_stream(watch, name):
+    launch, made, recorded = watch
+    call, used, count = PRODUCT_CALLS[name]
+    inputs = operands()
+    call(launch, inputs)
+    assert [who for who, _ in made] == ["launch"] * count
+    for _, t in made:
+        assert "caller" in recorded[t.untyped_storage().data_ptr()]
+    for k in used:
+        assert "launch" in recorded[inputs[k].untyped_storage().data_ptr()], k
+
+
 @pytest.mark.parametrize("name", LAYER_CALLS)
 def test_without_a_stream_nothing_changes_hands(watch, monkeypatch, name):
     launch, made, recorded = watch

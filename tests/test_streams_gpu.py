@@ -38,7 +38,23 @@ def gradients(*shape):
     return torch.randn(shape, generator=torch.Generator().manual_seed(7)).to(DEV)
 
 
-CASES = {"layer": (layer, layer_inputs), "newton short": (newton, lambda: (gradients(2, 100, 300),)),
+def products(a, b, rows, w, offsets, stream=None):
+    q = kgw.kgw_quantize_fp8(a, 1, stream=stream) + kgw.kgw_quantize_fp8(b, 0, stream=stream)
+    return (kgw.kgw_wgrad_bf16(a, b, offsets, stream=stream), kgw.kgw_wgrad_bf16_ex(a, b, offsets, stream=stream),
+            kgw.kgw_mgrouped_bf16(rows, w, offsets=offsets, stream=stream), *q,
+            kgw.kgw_wgrad_fp8(q[0], q[1], q[2], q[3], offsets, stream=stream),
+            kgw.kgw_check_offsets(offsets, a.shape[1], 256, stream=stream))
+
+
+def product_inputs():
+    g = torch.Generator().manual_seed(5)
+    counts = torch.tensor([4096, 0, 8192, 256])
+    tokens = int(counts.sum())
+    new = lambda *shape: torch.randn(shape, generator=g).bfloat16().to(DEV)  # noqa: E731
+    return new(256, tokens), new(tokens, 384), new(tokens, 64), new(4, 128, 64), torch.cumsum(counts, 0).int().to(DEV)
+
+
+CASES = {"products": (products, product_inputs), "layer": (layer, layer_inputs), "newton short": (newton, lambda: (gradients(2, 100, 300),)),
          "newton": (newton, lambda: (gradients(3, 200, 300),))}
 
 

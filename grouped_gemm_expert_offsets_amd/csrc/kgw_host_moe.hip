@@ -17,18 +17,19 @@ kgw_status_t usable_device() {
 
 int element_size(int32_t dtype) { return dtype == KGW_OUT_FP32 ? 4 : 2; }
 
-// One wave or workgroup per item: HIP counts a grid's threads in 32 bits.
-constexpr int64_t kMaxRowItems = (int64_t)1 << 23;
+constexpr int64_t kMaxRowTokens = (int64_t)1 << 23;
 
-// Checks shared by the calls that move rows.  `in` is (tokens, hidden) or (rows, hidden).
-kgw_status_t check_rows(int32_t dtype, int64_t tokens, int32_t topk, int64_t rows, int64_t hidden) {
+// Checks shared by the calls that move rows.
+kgw_status_t check_rows(int op, int32_t dtype, int64_t tokens, int32_t topk, int64_t rows, int64_t hidden) {
     if (dtype != KGW_OUT_FP32 && dtype != KGW_OUT_BF16 && dtype != KGW_OUT_FP16) return KGW_ERROR_INVALID_VALUE;
     if (tokens < 0 || topk < 1 || rows < 0 || hidden < 0) return KGW_ERROR_INVALID_VALUE;
-    if (topk > 65536 || tokens * (int64_t)topk > INT32_MAX || rows > INT32_MAX) return KGW_ERROR_UNSUPPORTED;
+    if (tokens > kMaxRowTokens || topk > 65536 || tokens * (int64_t)topk > INT32_MAX || rows > INT32_MAX)
+        return KGW_ERROR_UNSUPPORTED;
     if (hidden >= ((int64_t)1 << 28)) return KGW_ERROR_UNSUPPORTED;
-    const int64_t segments = hidden * element_size(dtype) / 2048 + 1;     // at most this many waves a row
-    if (tokens > kMaxRowItems || tokens * segments + rows / 4 >= 3 * kMaxRowItems) return KGW_ERROR_UNSUPPORTED;
-    return KGW_SUCCESS;
+    // HIP counts a grid's threads in 32 bits
+    return kgw::moe_rows_grid(op, dtype, tokens, rows, hidden) < ((int64_t)1 << 32) / kgw::kMoeRowThreads
+               ? KGW_SUCCESS
+               : KGW_ERROR_UNSUPPORTED;
 }
 
 bool rows_aligned(const void* p, int32_t dtype) { return aligned_to(p, (uintptr_t)element_size(dtype)); }
@@ -102,7 +103,7 @@ kgw_status_t kgw_moe_sort(const void* ids, int32_t id_bytes, int64_t tokens, int
 kgw_status_t kgw_moe_permute(const void* x, int64_t ld_x, int32_t dtype, const int32_t* row_of,
                              const int32_t* src_of, int64_t tokens, int32_t topk, int64_t rows, int64_t hidden,
                              void* out, void* stream) {
-    const kgw_status_t st = check_rows(dtype, tokens, topk, rows, hidden);
+    const kgw_status_t st = check_rows(kgw::kMoePermute, dtype, tokens, topk, rows, hidden);
     if (st != KGW_SUCCESS) return st;
     if (rows == 0 || hidden == 0) return KGW_SUCCESS;
     if (!src_of || !out || (tokens > 0 && (!x || !row_of || ld_x < hidden))) return KGW_ERROR_INVALID_VALUE;
@@ -124,7 +125,7 @@ kgw_status_t kgw_moe_permute(const void* x, int64_t ld_x, int32_t dtype, const i
 kgw_status_t kgw_moe_unpermute(const void* y, int64_t ld_y, int32_t dtype, const int32_t* row_of,
                                const float* weights, int64_t tokens, int32_t topk, int64_t rows, int64_t hidden,
                                void* out, void* stream) {
-    const kgw_status_t st = check_rows(dtype, tokens, topk, rows, hidden);
+    const kgw_status_t st = check_rows(kgw::kMoeUnpermute, dtype, tokens, topk, rows, hidden);
     if (st != KGW_SUCCESS) return st;
     if (tokens == 0 || hidden == 0) return KGW_SUCCESS;
     if (!row_of || !out || (rows > 0 && (!y || ld_y < hidden))) return KGW_ERROR_INVALID_VALUE;
@@ -147,7 +148,7 @@ kgw_status_t kgw_moe_unpermute_grad(const void* dout, int64_t ld_dout, const voi
                                     const int32_t* row_of, const int32_t* src_of, const float* weights,
                                     int64_t tokens, int32_t topk, int64_t rows, int64_t hidden, void* dy,
                                     float* dweights, void* stream) {
-    const kgw_status_t st = check_rows(dtype, tokens, topk, rows, hidden);
+    const kgw_status_t st = check_rows(kgw::kMoeUnpermuteGrad, dtype, tokens, topk, rows, hidden);
     if (st != KGW_SUCCESS) return st;
     if (tokens == 0 && (rows == 0 || hidden == 0)) return KGW_SUCCESS;
     if (tokens > 0 && (!row_of || !weights || !dweights)) return KGW_ERROR_INVALID_VALUE;

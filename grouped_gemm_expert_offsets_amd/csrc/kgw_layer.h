@@ -46,11 +46,14 @@ struct MoeRowsParams {
 };
 
 constexpr int kMoePermute = 0, kMoeUnpermute = 1, kMoeUnpermuteGrad = 2;
+constexpr int kMoeRowThreads = 256;     // of a workgroup of the row kernels
 
 // Workgroups of the sort and the assignments of each.
 constexpr int64_t kMoeSortShort = 65536;    // up to here smaller shares, so that up to 64 workgroups have one
 void moe_sort_plan(int64_t assignments, int32_t* groups, int64_t* chunk);
 hipError_t launch_moe_sort(const MoeSortParams& p, bool wide_ids, hipStream_t stream);
+// Workgroups that launch_moe_rows() starts.
+int64_t moe_rows_grid(int op, int dtype, int64_t tokens, int64_t rows, int64_t hidden);
 hipError_t launch_moe_rows(const MoeRowsParams& p, int op, int dtype, hipStream_t stream);
 
 // ----------------------------------------------------------------------------

@@ -222,7 +222,7 @@ __global__ __launch_bounds__(SORT_NT) void moe_place_kernel(MoeSortParams p) {
 // ----------------------------------------------------------------------------
 // rows
 // ----------------------------------------------------------------------------
-constexpr int ROW_NT = 256;
+constexpr int ROW_NT = kMoeRowThreads;
 constexpr int ROW_WAVES = ROW_NT / 64;
 constexpr int PAD_ROWS = 2;      // rows whose source one wave looks up before zeroing the empty ones (33024 rows of 7168 bf16, nearly
                                  // all empty: 16 take 96 us, 4 91, 2 89.4, 1 89; 262144 copied ones 789 with 2, 794 with 1)
@@ -479,6 +479,11 @@ int64_t row_segments(int64_t hidden, int dt, int per_lane) {
     return pieces <= 64 * per_lane ? 1 : (pieces + 64 * per_lane - 1) / (64 * per_lane);
 }
 
+// Waves of one token's row; the gradient has a workgroup a token.
+int64_t segments_of(int op, int dt, int64_t hidden) {
+    return op == kMoePermute ? row_segments(hidden, dt, SEG) : op == kMoeUnpermute ? row_segments(hidden, dt, USEG) : 1;
+}
+
 // Rows of y beyond this are read past the caches' retention: twice the 256 MB Infinity Cache, so they cannot be in it
 // from whoever wrote them.  3.8 GB: 784 -> 739 us (unpermute), 1576 -> 1552 us (gradient); but 268 MB, half of which
 // is still there: 62 -> 68 us, and 33 MB 11.9 -> 14.5 us.  Sums and gradients are always written that way (826 -> 784 us,
@@ -487,32 +492,28 @@ constexpr int64_t kStreamBytes = (int64_t)512 << 20;
 
 template <int DT>
 void launch_rows(MoeRowsParams p, int op, hipStream_t stream) {
-    const int64_t pad_waves = (p.rows + PAD_ROWS - 1) / PAD_ROWS;
     const bool stream_rows = p.rows * p.hidden * Elem<DT>::size > kStreamBytes;
+    p.segments = segments_of(op, DT, p.hidden);
+    p.items = p.tokens * p.segments;
+    const dim3 grid((uint32_t)moe_rows_grid(op, DT, p.tokens, p.rows, p.hidden));
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(ROW_NT), 0, stream, p); };
     if (op == kMoePermute) {
-        p.segments = row_segments(p.hidden, DT, SEG);
-        p.items = p.tokens * p.segments;
-        const int64_t grid = (p.items + pad_waves + ROW_WAVES - 1) / ROW_WAVES;
-        hipLaunchKernelGGL((moe_permute_kernel<DT>), dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p);
+        run(moe_permute_kernel<DT>);
     } else if (op == kMoeUnpermute) {
-        p.segments = row_segments(p.hidden, DT, USEG);
-        p.items = p.tokens * p.segments;
-        const int64_t grid = (p.items + ROW_WAVES - 1) / ROW_WAVES;
-        auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p); };
         if (p.weights) stream_rows ? run(moe_unpermute_kernel<DT, true, true>) : run(moe_unpermute_kernel<DT, true, false>);
         else stream_rows ? run(moe_unpermute_kernel<DT, false, true>) : run(moe_unpermute_kernel<DT, false, false>);
     } else {
-        p.segments = 1;
-        p.items = p.tokens;
-        const int64_t grid = p.items + (pad_waves + ROW_WAVES - 1) / ROW_WAVES;
-        if (stream_rows)
-            hipLaunchKernelGGL((moe_unpermute_grad_kernel<DT, true>), dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p);
-        else
-            hipLaunchKernelGGL((moe_unpermute_grad_kernel<DT, false>), dim3((uint32_t)grid), dim3(ROW_NT), 0, stream, p);
+        stream_rows ? run(moe_unpermute_grad_kernel<DT, true>) : run(moe_unpermute_grad_kernel<DT, false>);
     }
 }
 
 }  // namespace
+
+int64_t moe_rows_grid(int op, int dtype, int64_t tokens, int64_t rows, int64_t hidden) {
+    const int64_t pad_waves = op == kMoeUnpermute ? 0 : (rows + PAD_ROWS - 1) / PAD_ROWS;
+    if (op == kMoeUnpermuteGrad) return tokens + (pad_waves + ROW_WAVES - 1) / ROW_WAVES;
+    return (tokens * segments_of(op, dtype, hidden) + pad_waves + ROW_WAVES - 1) / ROW_WAVES;
+}
 
 void moe_sort_plan(int64_t assignments, int32_t* groups, int64_t* chunk) {
     const int64_t sub = SORT_NT * sort_per_lane(assignments);

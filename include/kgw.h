@@ -544,7 +544,10 @@ kgw_status_t kgw_device_info(int32_t* num_cus, int32_t* is_gfx950, int32_t* num_
  * gradients of both.  `dtype` is the element type of the rows (KGW_OUT_FP32,
  * KGW_OUT_BF16 or KGW_OUT_FP16); row strides (ld_*) count elements and are at
  * least `hidden`; hidden is any size and rows may start at any element.
- * tokens * topk < 2^31, rows < 2^31, hidden < 2^28.
+ * tokens * topk < 2^31, rows < 2^31, hidden < 2^28.  The calls that move rows also take
+ * tokens <= 2^23, topk <= 65536, and as many waves as one launch can hold: one for every 2048
+ * bytes of a token's row (the gradient: four a token) and, but for unpermute, one for every two of
+ * the `rows`, together at most 2^26 - 4.  Beyond any of these: KGW_ERROR_UNSUPPORTED.
  * ------------------------------------------------------------------------ */
 
 /*

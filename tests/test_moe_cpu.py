@@ -118,3 +118,22 @@ def test_binding_refuses_cpu_tensors():
                  lambda: kgw.kgw_moe_unpermute_grad(x, x, row_of, src_of, w)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_launches_that_do_not_fit_are_refused(lib):
+    # a launch holds fewer than 2^24 workgroups of four waves; empty rows take a wave for two of them
+    assert grad(lib, tokens=2 ** 23, k=1, rows=2 ** 26 - 1) == UNSUPPORTED
+    assert grad(lib, tokens=2 ** 23, k=1, rows=2 ** 26 - 7) == UNSUPPORTED
+    assert permute(lib, tokens=2 ** 23, k=1, rows=2 ** 27 - 2 ** 24) == UNSUPPORTED
+    assert permute(lib, tokens=2 ** 23, k=1, rows=256, hidden=8192, ld=8192) == UNSUPPORTED       # 8 waves a token
+    assert unpermute(lib, tokens=2 ** 23, k=1, rows=2 ** 30, hidden=8192, ld=8192) == UNSUPPORTED
+    assert grad(lib, tokens=2 ** 62, k=4) == UNSUPPORTED                         # tokens * topk passes 64 bits
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers are not real")
+def test_launches_that_just_fit_reach_the_device(lib):
+    device = kgw.KGW_ERROR_DEVICE
+    assert grad(lib, tokens=2 ** 23, k=1, rows=2 ** 26 - 8) == device
+    assert permute(lib, tokens=2 ** 23, k=1, rows=2 ** 27 - 2 ** 24 - 8) == device
+    assert permute(lib, tokens=2 ** 23 - 1, k=1, rows=8, hidden=8192, ld=8192) == device
+    assert unpermute(lib, tokens=2 ** 23, k=1, rows=2 ** 30) == device

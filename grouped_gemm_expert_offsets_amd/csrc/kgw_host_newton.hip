@@ -68,6 +68,8 @@ kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_
     char* const slabs = p.b + plan.b_bytes + plan.parts_bytes;
     p.slabs = plan.slab_bytes ? (float*)slabs : nullptr;
     p.arrived = plan.slab_bytes ? (uint32_t*)(slabs + plan.slab_bytes - kgw::kNewtonSlabs * sizeof(uint32_t)) : nullptr;
+    p.scales = (kgw::StepScales*)(slabs + plan.slab_bytes);
+    p.planes = (int32_t*)(p.scales + (size_t)batch * kgw::kNewtonMaxSteps);
     return kgw::launch_newton(p, plan, coefficients, num_cus, num_xcds, (hipStream_t)stream) == hipSuccess
                ? KGW_SUCCESS
                : KGW_ERROR_DEVICE;

@@ -64,6 +64,90 @@ constexpr int kNewtonParts = 256;       // partial sums of squares per matrix, a
 
 constexpr int kNewtonSlabs = 256;       // workgroups that may share tiles: one for every CU
 
+// One step of one matrix, in the planes' powers of two: B = square (A A + square_linear A), then
+// X = update (B X + update_linear X).
+struct alignas(16) StepScales {
+    float square, square_linear, update, update_linear;
+};
+
+struct NewtonCoefficients {
+    float v[3 * kNewtonMaxSteps];       // a, b, c of every step
+    StepScales unit[kNewtonMaxSteps];   // the scales of a matrix whose norm is nothing beside eps
+    int32_t measured;                   // the scales come from the norm of every step's A instead
+};
+
+// An upper bound on an iterate's singular values, m 2^e with m in [1, 2), and what its planes hold: it times
+// 2^(13 - plane).  The largest of the singular values is at least ratio times the bound.
+struct SingularBound {
+    float m;
+    int e, plane;
+    float ratio;
+};
+__host__ __device__ inline SingularBound unit_bound(float ratio) { return {1.0f + 0x1p-20f, 0, 0, ratio}; }
+
+// The scales of the step X <- a X + (b A + c A A) X for a matrix of bound s, which becomes the bound of the next.
+//
+// Singular values go through f(x) = x (a + b x^2 + c x^4), those of B are b x^2 + c x^4: with x = s t, u = t^2,
+// their largest values for t in [0, 1] are at t = 1 or where the derivatives vanish, 5 g u^2 + 3 h u + a = 0 and
+// 2 g u + h = 0 (h = b s^2, g = c s^4).  Everything is taken times 2^-q, which brings the largest of a, h and g near 1,
+// so that no size of coefficients or matrix leaves fp32's range here.  B's power follows the larger of B and a: what
+// a B far below a loses does not matter beside a X.
+__host__ __device__ inline StepScales step_scales(SingularBound& s, const float* co, bool last) {
+    const float a = co[0], b = co[1], c = co[2];
+    auto exponent = [](float x) {                           // 2^exponent <= |x|; far below all others for zero
+        int e = 0;
+        __builtin_frexpf(x, &e);
+        return x != 0.0f ? e - 1 : -100000;
+    };
+    auto at_most = [](float x, float y) { return x < y ? x : y; };
+    auto at_least = [](float x, float y) { return x > y ? x : y; };      // y for a NaN x
+    const int ea = exponent(a), eb = exponent(b) + 2 * s.e, ec = exponent(c) + 4 * s.e;
+    const int q = ea > eb ? (ea > ec ? ea : ec) : (eb > ec ? eb : ec);
+    const float m2 = s.m * s.m;
+    const float b0 = __builtin_ldexpf(b, 2 * s.e - q), c0 = __builtin_ldexpf(c, 4 * s.e - q);
+    const float al = __builtin_ldexpf(a, -q), h = b0 * m2, g = c0 * m2 * m2;
+    auto inner = [&](float u) { return al + u * (h + g * u); };
+    auto value = [&](float u) { return __builtin_sqrtf(u) * __builtin_fabsf(inner(u)); };
+    auto inside = [&](float u, float from) { return at_most(at_least(u, from), 1.0f); };
+    const float root = __builtin_sqrtf(at_least(9.0f * h * h - 20.0f * al * g, 0.0f));
+    const float w = -0.5f * (3.0f * h + __builtin_copysignf(root, h));
+    const float flat0 = w / (5.0f * g), flat1 = al / w, turn = -0.5f * h / g;
+    const float gain = at_least(value(1.0f), at_least(value(inside(flat0, 0.0f)), value(inside(flat1, 0.0f))));
+    const float in = inside(turn, 0.0f);
+    const float of_b = at_least(__builtin_fabsf(h + g), __builtin_fabsf(in * (h + g * in)));
+    const float largest = at_least(of_b, __builtin_fabsf(al));
+    const int lg = largest > 0.0f ? exponent(largest) : 0;
+    const int b_power = 8 - lg - q;                         // the planes hold B times 2^b_power
+    // c A A + b A = c (A A + b / c A); a c that is nothing beside b is made 2^-60 b, which still is
+    const int below = s.plane - s.e;                        // the planes' powers of two above the bound's
+    const float b1 = __builtin_ldexpf(b0, 2 * below - 2 - lg);
+    float c1 = __builtin_ldexpf(c0, 4 * below - 12 - lg);
+    if (__builtin_fabsf(c1) <= __builtin_fabsf(b1) * 0x1p-60f) c1 = b1 * 0x1p-60f;
+    StepScales r;
+    r.square = c1;
+    r.square_linear = c1 != 0.0f ? b1 / c1 : 0.0f;
+    // the least that the largest singular value, from ratio to 1 of the bound, may become
+    const float from = s.ratio * s.ratio;
+    const float least = at_most(at_most(value(from), value(1.0f)),
+                                at_most(value(inside(flat0, from)), value(inside(flat1, from))));
+    const float p0 = inner(from), p1 = inner(1.0f), p2 = inner(inside(turn, from));
+    s.ratio = p0 * p1 > 0.0f && p0 * p2 > 0.0f && gain > 0.0f ? least / gain : 0.0f;      // a zero in between: anything
+    const float next = s.m * gain;
+    const bool any = next > 0.0f && next < 0x1p100f;
+    int e = any ? s.e + q + exponent(next) : 0;
+    e = e < -2000 ? -2000 : e > 2000 ? 2000 : e;            // past fp32's range either way
+    r.update = __builtin_ldexpf(1.0f, s.plane - b_power - (last ? 13 : e));
+    r.update_linear = __builtin_ldexpf(a, b_power);
+    s.m = any ? __builtin_ldexpf(next, -exponent(next)) : 1.0f;
+    s.e = s.plane = e;
+    return r;
+}
+
+// Whether the scales may follow the bounds alone: the bounds stay about as near the singular values as |G|_F is (within
+// its square root of r), as they do for coefficients that bring singular values below 1 together.  Where they part (f
+// grows steeply towards 1, or vanishes in between), planes made for the bound would leave the iterate too few bits.
+constexpr float kBoundLoss = 1.0f / 16.0f;
+
 struct NewtonParams {
     const void* G;          // (batch, m, n), rows contiguous
     void* out;              // (batch, m, n), contiguous
@@ -81,14 +165,9 @@ struct NewtonParams {
     char* b;
     float* slabs;           // (kNewtonSlabs, tile, tile), small tiles only
     uint32_t* arrived;      // (kNewtonSlabs,), or NULL
+    StepScales* scales;     // (batch, kNewtonMaxSteps)
+    int32_t* planes;        // (2, batch): SingularBound::plane of even and odd steps, for measured scales
 };
-
-// The factor c of one step's (a, b, c), for c A A + b A = c (A A + b / c A): one that is nothing beside b
-// is made 2^-60 b, which still is.
-inline float newton_c(const float* co) {
-    const float least = co[1] < 0.0f ? -co[1] * 0x1p-60f : co[1] * 0x1p-60f;
-    return co[2] > least || co[2] < -least ? co[2] : co[1] * 0x1p-60f;
-}
 
 // How a batch is computed, and the layout of its workspace.
 struct NewtonPlan {
@@ -100,13 +179,13 @@ struct NewtonPlan {
     int32_t chunks;         // narrow: 128-column chunks of a matrix
     int32_t per_group;      // narrow: chunks of one workgroup
     int32_t groups;         // narrow: workgroups of a matrix (0: one that runs all steps)
-    size_t x_bytes, a_bytes, b_bytes, parts_bytes, slab_bytes, total;
+    size_t x_bytes, a_bytes, b_bytes, parts_bytes, slab_bytes, scales_bytes, total;
 };
 constexpr int64_t kNarrowMax = 128;
 NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype);
 void newton_narrow_plan(int32_t batch, int64_t r, int64_t c, NewtonPlan* plan);
 void launch_newton_norm(const NewtonParams& p, hipStream_t stream);
-void launch_newton_narrow(const NewtonParams& p, const NewtonPlan& plan, const float* coefficients, hipStream_t stream);
+void launch_newton_narrow(const NewtonParams& p, const NewtonPlan& plan, const NewtonCoefficients& co, hipStream_t stream);
 hipError_t launch_newton(const NewtonParams& p, const NewtonPlan& plan, const float* coefficients, int num_cus,
                          int num_xcds, hipStream_t stream);
 

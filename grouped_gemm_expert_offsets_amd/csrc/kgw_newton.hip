@@ -4,7 +4,7 @@
 //     X_0 = G / (|G|_F + eps)                     (transposed when m > n, so r <= c)
 //     A = X X^T,   B = b A + c A A,   X <- a X + B X,   `steps` times
 //
-// The iterate is held as two fp16 planes, X = (hi + lo) / 2^13: hi is X rounded to 11 bits, lo
+// The iterate is held as two fp16 planes, X = (hi + lo) / 2^(13 - e): hi is X rounded to 11 bits, lo
 // the remainder rounded again, 22 bits together, so the linear term a X, which multiplies
 // small singular values by a at every step, keeps those.  The products run on the matrix cores in fp16
 // with fp32 sums:
@@ -14,8 +14,10 @@
 //     bf16 operands would leave 4e-3 .. 2e-2.
 //   three products each (fp32 and fp16 results): every matrix as hi + lo, hi hi + hi lo + lo hi;
 //     the dropped lo lo is 2^-24 of the product.  1e-6 .. 1e-5, what fp32 arithmetic leaves.
-// Powers of two keep the planes inside fp16's range: X * 2^13 (|X| <= 1.2 with the usual
-// coefficients, below 8 allowed), A * 2^10 (below 64) and B * 2^7 (below 512).
+// Powers of two keep the planes inside fp16's range, chosen for every matrix and step from a bound 2^e on its singular
+// values (step_scales()): 1 for the first iterate, less where eps outweighs the norm, then the largest value the
+// step's polynomial takes up to there.  Where bounds say too little (kBoundLoss) A's norm is measured in every step, by two
+// more launches.
 //
 // A and A A are symmetric: only tiles on and below the diagonal are computed and their mirror
 // images written along, which leaves 3 r^2 c + r^3 multiply-adds of a step's 4 r^2 c + 2 r^3 over two.
@@ -92,10 +94,12 @@ __global__ __launch_bounds__(NT) void newton_norm_kernel(NewtonParams p) {
 // One 64 x 64 tile of the padded first iterate.  Bound by HBM: reads 2 bytes an element and writes 4,
 // 262 us for 8 x 7168 x 4096 bf16, 5.4 TB/s; transposed through LDS it takes as long.
 template <int DT, bool SPLIT, bool TALL>
-__global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, int64_t R, int64_t C) {
+__global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, NewtonCoefficients co, int64_t R, int64_t C) {
     __shared__ float tile[TALL ? 64 : 1][65];
     const int b = blockIdx.z, i0 = threadIdx.x >> 3, q = threadIdx.x & 7;
     const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+    const bool writes = blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 64;
+    if (writes) write_unit_scales(p, co, b);
     float v[2][8];
 #pragma unroll
     for (int u = 0; u < 2; ++u) load_eight<DT>(p, b, (TALL ? c0 : r0) + i0 + 32 * u, (TALL ? r0 : c0) + 8 * q, v[u]);
@@ -119,12 +123,54 @@ __global__ __launch_bounds__(NT) void newton_first_kernel(NewtonParams p, int64_
         for (int e = 0; e < 8; ++e) v[u][e] = scale.of(v[u][e]);
         store_planes<true>(v[u], x + element<SPLIT>(r0 + i0 + 32 * u, c0 + 8 * q, C), lo_off);
     }
+    if (writes) write_scales(p, co, b, scale);
+}
+
+// Scales measured on A, for coefficients whose bounds say too little (kBoundLoss): the sum of squares of A's high plane in
+// parts, and from them the step's scales.
+template <bool SPLIT>
+__global__ __launch_bounds__(NT) void newton_measure_kernel(NewtonParams p, int64_t R, int32_t parts) {
+    __shared__ double sums[NT / 64];
+    const int tid = threadIdx.x, b = blockIdx.y;
+    const uint16_t* const a = (const uint16_t*)p.a + (int64_t)b * R * R * (SPLIT ? 2 : 1);
+    const int per_row = (int)(R / 8);
+    double s = 0.0;
+    for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < R * per_row; i += (int64_t)parts * NT) {
+        const int64_t row = i / per_row;
+        const i32x4 x = *(const gbl_i32x4*)(a + element<SPLIT>(row, 8 * (i - row * per_row), R));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const double lo = f16_lo((uint32_t)x[u]), hi = f16_hi((uint32_t)x[u]);
+            s += lo * lo + hi * hi;
+        }
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    if ((tid & 63) == 0) sums[tid >> 6] = s;
+    __syncthreads();
+    if (tid == 0) p.parts[(int64_t)b * kNewtonParts + blockIdx.x] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+}
+__global__ __launch_bounds__(64) void newton_scales_kernel(NewtonParams p, NewtonCoefficients co, int32_t step, int32_t parts) {
+    const int b = blockIdx.x;
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 64) s += p.parts[(int64_t)b * kNewtonParts + i];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    SingularBound bound = measured_bound(s, p.planes[(int64_t)(step & 1) * p.batch + b]);
+    const StepScales r = step_scales(bound, co.v + 3 * step, step + 1 == p.steps);
+    if (threadIdx.x == 0) {
+        p.scales[(int64_t)b * kNewtonMaxSteps + step] = r;
+        p.planes[(int64_t)(~step & 1) * p.batch + b] = bound.plane;
+    }
 }
 
 // ----------------------------------------------------------------------------
 // the products
 // ----------------------------------------------------------------------------
 enum NewtonProduct { kGram, kSquare, kUpdate, kLast };   // kLast: the last update, which writes the result
+__device__ __forceinline__ float as_uniform(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
 constexpr bool updates(NewtonProduct k) { return k == kUpdate || k == kLast; }
 
 struct NewtonGemm {
@@ -134,8 +180,8 @@ struct NewtonGemm {
     void* result;           // last update: (batch, m, n) of result_dtype
     int64_t m, n;
     int32_t result_dtype, tall;
-    float scale;            // out = scale * (product + linear * (square: A; update: the iterate))
-    float linear;
+    const StepScales* scales;  // of this step, every kNewtonMaxSteps-th one: out = scale * (product + linear * (square: A;
+                               // update: the iterate)); gram: kGramScale * product
     int64_t rows, cols, k;  // padded sizes of the product
     int32_t batch, tiles_m, tiles_n;
     int32_t items;          // workgroups with work
@@ -317,6 +363,13 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     const char* const right = updates(KIND) ? p.right + (int64_t)b * p.k * ldr + n0 * (SPLIT ? 4 : 2)
                                               : p.right + ((int64_t)b * p.rows + n0) * ldr;
 
+    float scale = kGramScale, linear = 0.0f;
+    if constexpr (KIND != kGram) {
+        const float* const at = (const float*)(p.scales + (int64_t)b * kNewtonMaxSteps) + (updates(KIND) ? 2 : 0);
+        scale = as_uniform(at[0]);
+        linear = as_uniform(at[1]);
+    }
+
     uint32_t l_off[LOADS], r_off[LOADS];
 #pragma unroll
     for (int t = 0; t < LOADS; ++t) {
@@ -415,10 +468,10 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
                             from = l_row + (uint32_t)i * 4096u + (uint32_t)((chunk ^ sw) << 4);
                         }
                         const i32x2 x = lds_load_8B(base, from + (uint32_t)lhi * 8u);
-                        acc[j][i][4 * g] += p.linear * f16_lo((uint32_t)x[0]);
-                        acc[j][i][4 * g + 1] += p.linear * f16_hi((uint32_t)x[0]);
-                        acc[j][i][4 * g + 2] += p.linear * f16_lo((uint32_t)x[1]);
-                        acc[j][i][4 * g + 3] += p.linear * f16_hi((uint32_t)x[1]);
+                        acc[j][i][4 * g] += linear * f16_lo((uint32_t)x[0]);
+                        acc[j][i][4 * g + 1] += linear * f16_hi((uint32_t)x[0]);
+                        acc[j][i][4 * g + 2] += linear * f16_lo((uint32_t)x[1]);
+                        acc[j][i][4 * g + 3] += linear * f16_hi((uint32_t)x[1]);
                     }
                 asm volatile("; block %0" ::"n"(k.value));
             });
@@ -466,6 +519,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
         for (int t = 0; t < LOADS; ++t) load_one(n, n, t);
     wait_vmcnt<(SLOTS - 4) * LOADS>();
     barrier_no_fence();
+    asm volatile("" ::"s"(scale), "s"(linear));         // both are there: the loop's waits count LDS reads alone
     Left l0, l1;
     Right r0, r1;
     each<BOTH>([&](auto t) __attribute__((always_inline)) { read_both(0, 1, 0, l0, r0, t); });
@@ -552,7 +606,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
     const int64_t matrix = (int64_t)b * p.rows * p.cols * (SPLIT ? 2 : 1);
     uint16_t* const out = (uint16_t*)p.out + matrix;
     const uint16_t* const low = (const uint16_t*)p.right + matrix + lo_off;
-    const float low_scale = p.linear * p.scale;
+    const float low_scale = linear * scale;
     const int64_t row_w = m0 + wm * WTM, col_w = n0 + wn * WTN;
     lds_char* const mine = lds + wave * (SLOTS * STAGE / WAVES);
     static_assert(32 * (WTM > WTN ? WTM : WTN) * 4 <= SLOTS * STAGE / WAVES, "the image fits the wave's share of LDS");
@@ -592,7 +646,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
             const f32x4 w = __builtin_bit_cast(f32x4, lds_load_16B(mine, image_at<W>(r, 2 * c + 1)));
             float v[8] = {u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]};
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] *= p.scale;
+            for (int q = 0; q < 8; ++q) v[q] *= scale;
             store(n * RPI, n, v);
         });
     };
@@ -638,10 +692,10 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
                     for (int g = 0; g < 4; ++g) {
                         const i32x2 x = lds_load_8B(mine, (uint32_t)((32 * i + l32) * WTN * 2 +
                                                                      (((4 * j + g) ^ low_sw(l32)) << 4) + lhi * 8));
-                        acc[j][i][4 * g] += p.linear * f16_lo((uint32_t)x[0]);
-                        acc[j][i][4 * g + 1] += p.linear * f16_hi((uint32_t)x[0]);
-                        acc[j][i][4 * g + 2] += p.linear * f16_lo((uint32_t)x[1]);
-                        acc[j][i][4 * g + 3] += p.linear * f16_hi((uint32_t)x[1]);
+                        acc[j][i][4 * g] += linear * f16_lo((uint32_t)x[0]);
+                        acc[j][i][4 * g + 1] += linear * f16_hi((uint32_t)x[0]);
+                        acc[j][i][4 * g + 2] += linear * f16_lo((uint32_t)x[1]);
+                        acc[j][i][4 * g + 3] += linear * f16_hi((uint32_t)x[1]);
                     }
         }
 #pragma unroll
@@ -848,7 +902,7 @@ void launch_product(NewtonGemm g, int tile, int num_cus, hipStream_t stream) {
 }
 
 template <bool SPLIT>
-void launch_steps(const NewtonParams& p, const NewtonPlan& plan, const float* co, int num_cus, int num_xcds,
+void launch_steps(const NewtonParams& p, const NewtonPlan& plan, const NewtonCoefficients& co, int num_cus, int num_xcds,
                   hipStream_t stream) {
     NewtonGemm g = {};
     g.batch = p.batch;
@@ -862,41 +916,41 @@ void launch_steps(const NewtonParams& p, const NewtonPlan& plan, const float* co
     g.tall = plan.tall ? 1 : 0;
     for (int s = 0; s < p.steps; ++s) {
         const char* const x = p.x[s & 1];
+        g.scales = p.scales + s;
         g.cols = plan.r;
         g.k = plan.c;
         g.left = g.right = x;
         g.out = p.a;
-        g.scale = kAScale / (kXScale * kXScale);
         launch_product<SPLIT, kGram>(g, plan.tile, num_cus, stream);
-        // c A A + b A = c (A A + b / c A)
-        const float b = co[3 * s + 1], c = newton_c(co + 3 * s);
+        if (co.measured) {
+            const int64_t share = (plan.r * plan.r + 8191) / 8192;
+            const int32_t parts = (int32_t)(share < kNewtonParts ? share : kNewtonParts);
+            hipLaunchKernelGGL((newton_measure_kernel<SPLIT>), dim3((uint32_t)parts, (uint32_t)p.batch), dim3(NT), 0, stream, p,
+                               plan.r, parts);
+            hipLaunchKernelGGL(newton_scales_kernel, dim3((uint32_t)p.batch), dim3(64), 0, stream, p, co, s, parts);
+        }
         g.k = plan.r;
         g.left = g.right = p.a;
         g.out = p.b;
-        g.scale = c * (kBScale / (kAScale * kAScale));
-        g.linear = c != 0.0f ? b / c * kAScale : 0.0f;
         launch_product<SPLIT, kSquare>(g, plan.tile, num_cus, stream);
         g.cols = plan.c;
         g.left = p.b;
         g.right = x;
-        const bool last = s + 1 == p.steps;
         g.out = p.x[(s + 1) & 1];
         g.result = p.out;
-        g.scale = (last ? 1.0f / kXScale : 1.0f) / kBScale;
-        g.linear = co[3 * s] * kBScale;
-        if (last) launch_product<SPLIT, kLast>(g, plan.tile, num_cus, stream);
+        if (s + 1 == p.steps) launch_product<SPLIT, kLast>(g, plan.tile, num_cus, stream);
         else launch_product<SPLIT, kUpdate>(g, plan.tile, num_cus, stream);
     }
 }
 
 template <bool SPLIT, bool TALL>
-void launch_all(const NewtonParams& p, const NewtonPlan& plan, const float* co, int num_cus, int num_xcds,
+void launch_all(const NewtonParams& p, const NewtonPlan& plan, const NewtonCoefficients& co, int num_cus, int num_xcds,
                 hipStream_t stream) {
     launch_newton_norm(p, stream);
     const dim3 tiles((uint32_t)(plan.c / 64), (uint32_t)(plan.r / 64), (uint32_t)p.batch);
     auto first = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        hipLaunchKernelGGL((newton_first_kernel<DT, SPLIT, TALL>), tiles, dim3(NT), 0, stream, p, plan.r, plan.c);
+        hipLaunchKernelGGL((newton_first_kernel<DT, SPLIT, TALL>), tiles, dim3(NT), 0, stream, p, co, plan.r, plan.c);
     };
     if (p.dtype == kOutBf16) first(std::integral_constant<int, kOutBf16>{});
     else if (p.dtype == kOutF16) first(std::integral_constant<int, kOutF16>{});
@@ -918,6 +972,7 @@ NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
     const int64_t r = m < n ? m : n, c = m < n ? n : m;
     plan.tall = m > n;
     plan.parts_bytes = ((size_t)batch * kNewtonParts * sizeof(double) + 1023) / 1024 * 1024;
+    plan.scales_bytes = (size_t)batch * (kNewtonMaxSteps * sizeof(StepScales) + 2 * sizeof(int32_t));
     plan.narrow = r <= kNarrowMax;
     if (plan.narrow) {
         newton_narrow_plan(batch, r, c, &plan);
@@ -937,20 +992,28 @@ NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
     plan.b_bytes = plan.a_bytes;
     // sums of parts of K (kNewtonSlabs of them at most, one a workgroup) and their counters
     plan.slab_bytes = plan.tile == 256 ? 0 : (size_t)kNewtonSlabs * (plan.tile * plan.tile * 4 + 4);
-    plan.total = plan.parts_bytes + 2 * plan.x_bytes + plan.a_bytes + plan.b_bytes + plan.slab_bytes;
+    plan.total = plan.parts_bytes + 2 * plan.x_bytes + plan.a_bytes + plan.b_bytes + plan.slab_bytes + plan.scales_bytes;
     return plan;
 }
 
 hipError_t launch_newton(const NewtonParams& p, const NewtonPlan& plan, const float* coefficients, int num_cus,
                          int num_xcds, hipStream_t stream) {
+    NewtonCoefficients co = {};
+    for (int i = 0; i < 3 * p.steps; ++i) co.v[i] = coefficients[i];
+    const float ratio = 1.0f / __builtin_sqrtf((float)(p.m < p.n ? p.m : p.n));
+    SingularBound bound = unit_bound(ratio);
+    for (int s = 0; s < p.steps; ++s) {
+        if (!(bound.ratio >= ratio * kBoundLoss)) co.measured = 1;
+        co.unit[s] = step_scales(bound, co.v + 3 * s, s + 1 == p.steps);
+    }
     if (plan.narrow) {
-        launch_newton_narrow(p, plan, coefficients, stream);
+        launch_newton_narrow(p, plan, co, stream);
     } else if (plan.split) {
-        if (plan.tall) launch_all<true, true>(p, plan, coefficients, num_cus, num_xcds, stream);
-        else launch_all<true, false>(p, plan, coefficients, num_cus, num_xcds, stream);
+        if (plan.tall) launch_all<true, true>(p, plan, co, num_cus, num_xcds, stream);
+        else launch_all<true, false>(p, plan, co, num_cus, num_xcds, stream);
     } else {
-        if (plan.tall) launch_all<false, true>(p, plan, coefficients, num_cus, num_xcds, stream);
-        else launch_all<false, false>(p, plan, coefficients, num_cus, num_xcds, stream);
+        if (plan.tall) launch_all<false, true>(p, plan, co, num_cus, num_xcds, stream);
+        else launch_all<false, false>(p, plan, co, num_cus, num_xcds, stream);
     }
     return hipGetLastError();
 }

@@ -9,7 +9,11 @@
 
 namespace kgw {
 
-constexpr float kXScale = 8192.0f, kAScale = 1024.0f, kBScale = 128.0f;
+// The planes of X, A = X X^T and B = b A + c A A hold them times powers of two, chosen per matrix and step so that
+// a matrix as large as its bound allows comes to 2^13 .. 2^14, 2^10 .. 2^12 and 2^8 .. 2^9: well inside fp16's range
+// above, and with as much room as there is below, where planes lose bits from 2^-3 on.  The power of A is that of X
+// squared times this.
+constexpr float kGramScale = 0x1p-16f;
 
 typedef __attribute__((__vector_size__(8 * sizeof(_Float16)))) _Float16 f16x8;
 __device__ __forceinline__ f32x16 mfma_f16_32x32x16(i32x4 a, i32x4 b, f32x16 c) {
@@ -94,17 +98,29 @@ __device__ __forceinline__ void load_eight(const NewtonParams& p, int b, int64_t
     }
 }
 
-// What the first iterate multiplies G by, 2^13 / (|G|_F + eps), in two factors: where the norm is so small that
-// the quotient leaves fp32's range, G is first brought up by 2^100.
+// What the first iterate multiplies G by, 2^(13 - e) / (|G|_F + eps), in two factors: where the norm is near either end
+// of fp32's range the quotient may leave it, and G is first brought nearer by a power of two.
 struct FirstScale {
     float before, scale;
+    bool unit;              // |X_0| is 1 but for rounding: the scales that the host made hold
+    SingularBound bound;
     __device__ __forceinline__ float of(float g) const { return as_fp32(g * before * scale); }
 };
 __device__ __forceinline__ FirstScale scale_of_norm(double norm, float eps) {
-    const double d = norm + (double)eps;
+    const double d = norm + (double)eps, inverse = 1.0 / d;
     FirstScale f;
-    f.before = d < 0x1p-100 ? 0x1p100f : 1.0f;
-    f.scale = (float)((double)kXScale / (d * (double)f.before));
+    // |X_0| = norm / d, far below 1 where eps is what counts; a zero matrix, infinities and NaN go with the usual ones
+    const double first = norm * inverse;
+    f.unit = __builtin_amdgcn_readfirstlane(!(first > 0.0 && first < 1.0 - 0x1p-20));       // the same in all lanes
+    f.bound = unit_bound(1.0f);
+    if (!f.unit) {
+        f.bound.m = 2.0f * (float)__builtin_frexp(first, &f.bound.e);
+        f.bound.plane = --f.bound.e;
+    }
+    const int nearer = norm < 0x1p-100 ? 100 : norm > 0x1p100 ? -60 : 0;
+    f.before = __builtin_ldexpf(1.0f, nearer);
+    f.scale = (float)__builtin_ldexp(inverse, 13 - f.bound.e - nearer);
+    if (norm == 0.0 && d > 0.0) f.scale = 1.0f;             // zeros stay zeros, however small eps is
     return f;
 }
 // The same in every wave of matrix b, from the parts of its norm.
@@ -114,6 +130,40 @@ __device__ __forceinline__ FirstScale first_scale(const NewtonParams& p, int b) 
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
     return scale_of_norm(__builtin_sqrt(s), p.eps);
+}
+
+// The usual scales of all steps of matrix b, by one wave, as early as it can: loading kernel arguments lane by lane takes long.
+__device__ __forceinline__ void write_unit_scales(const NewtonParams& p, const NewtonCoefficients& co, int b) {
+    const int lane = threadIdx.x & 63;
+    if (lane < p.steps) p.scales[(int64_t)b * kNewtonMaxSteps + lane] = co.unit[lane];
+}
+// The others, by the same wave afterwards.
+__device__ __forceinline__ void write_scales(const NewtonParams& p, const NewtonCoefficients& co, int b, const FirstScale& scale) {
+    const int lane = threadIdx.x & 63;
+    if (co.measured) {
+        if (lane == 0) p.planes[b] = scale.bound.plane;
+        return;
+    }
+    if (scale.unit) return;
+    SingularBound s = scale.bound;
+    for (int step = 0; step < p.steps; ++step) {
+        const StepScales r = step_scales(s, co.v + 3 * step, step + 1 == p.steps);
+        if (lane == 0) p.scales[(int64_t)b * kNewtonMaxSteps + step] = r;
+    }
+}
+
+// The bound that the plane of A gives, from the sum of its squares: the largest singular value is at most the square
+// root of |A|_F, and at least r^(-1/4) of that.
+__device__ __forceinline__ SingularBound measured_bound(double squares, int plane) {
+    // the plane holds A times 2^(10 - 2 plane)
+    const double s = __builtin_sqrt(__builtin_sqrt(squares));
+    SingularBound f = unit_bound(1.0f);
+    f.e = f.plane = plane;                                  // of zeros, infinities and NaN
+    if (s > 0.0 && s < 0x1p100) {
+        f.m = 2.0f * (float)__builtin_frexp(s, &f.e);
+        f.e += plane - 6;
+    }
+    return f;
 }
 
 }  // namespace kgw

@@ -40,14 +40,8 @@ struct NarrowParams {
     int32_t groups_in;      // parts of A to be added up
     int32_t groups, chunks, per_group;
     int32_t tall;
-    float a_scale;          // 2^10 A = a_scale * sum of the parts
-    float b_scale, b_linear;// 2^7 B = b_scale * (A A + b_linear * A), in the planes' scales
-    float x_scale, linear;  // X = x_scale * (B X + linear * X)
-};
-
-// The scales of every step, for the kernel that runs all of them.
-struct NarrowSteps {
-    float b_scale[kNewtonMaxSteps], b_linear[kNewtonMaxSteps], linear[kNewtonMaxSteps];
+    int32_t step;
+    float co[3];            // a, b, c of the step
 };
 
 // 8 sums of one lane -> its 16 bytes of a fragment, high and low plane.
@@ -214,36 +208,60 @@ __device__ __forceinline__ void write_blocks(lds_char* a, int wave, int lane, co
         }
 }
 
-// B = b_scale (A A + b_linear A) as fragments in LDS, from the blocks of sums / a_scale that each wave has.
+// Scales measured on A (kBoundLoss): from the sum of its squares, the same in every workgroup of the matrix.
+template <int RB>
+__device__ __forceinline__ StepScales measured_scales(const f32x16 (&mine)[Narrow<RB>::MINE], double* sums, SingularBound& bound,
+                                                      const float* co, bool last, int wave, int lane) {
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < Narrow<RB>::MINE; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const double x = (double)(mine[j][e] * kGramScale);
+            s += x * x;
+        }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    if (lane == 0) sums[wave] = s;
+    __syncthreads();
+    double squares = 0.0;
+#pragma unroll
+    for (int w = 0; w < Narrow<RB>::WAVES; ++w) squares += sums[w];
+    __syncthreads();
+    bound = measured_bound(squares, bound.plane);
+    return step_scales(bound, co, last);
+}
+
+// B = square (A A + square_linear A) as fragments in LDS, from the blocks of X X^T that each wave has.
 // The caller's barriers: no one reads `a` any more before, all have written it after.
 template <int RB>
-__device__ __forceinline__ void make_b(const NarrowParams& q, lds_char* a, int wave, int lane,
+__device__ __forceinline__ void make_b(const StepScales& scales, lds_char* a, int wave, int lane,
                                        f32x16 (&mine)[Narrow<RB>::MINE]) {
     using N = Narrow<RB>;
 #pragma unroll
     for (int j = 0; j < N::MINE; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mine[j][e] *= q.a_scale;
+        for (int e = 0; e < 16; ++e) mine[j][e] *= kGramScale;
     write_blocks<RB>(a, wave, lane, mine);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < N::MINE; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mine[j][e] *= q.b_linear;
+        for (int e = 0; e < 16; ++e) mine[j][e] *= scales.square_linear;
     add_gram<RB, 2 * RB>(a, wave, lane, mine);
 #pragma unroll
     for (int j = 0; j < N::MINE; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mine[j][e] *= q.b_scale;
+        for (int e = 0; e < 16; ++e) mine[j][e] *= scales.square;
     __syncthreads();
     write_blocks<RB>(a, wave, lane, mine);
 }
 
-// acc = x_scale (B X + linear X) in this wave's 32 columns of a chunk: columns down the registers, rows
+// acc = update (B X + update_linear X) in this wave's 32 columns of a chunk: columns down the registers, rows
 // over the lanes.
 template <int RB>
-__device__ __forceinline__ void update_chunk(const NarrowParams& q, const lds_char* x, const lds_char* a, int wave, int lane,
-                                             float x_scale, f32x16 (&acc)[Narrow<RB>::ROWS]) {
+__device__ __forceinline__ void update_chunk(const StepScales& scales, const lds_char* x, const lds_char* a, int wave, int lane,
+                                             f32x16 (&acc)[Narrow<RB>::ROWS]) {
     using N = Narrow<RB>;
     const int g16 = lane >> 4, i16 = lane & 15;
     clear(acc);
@@ -275,10 +293,10 @@ __device__ __forceinline__ void update_chunk(const NarrowParams& q, const lds_ch
             const i32x4 lo = lds_load_16B(x, N::x_at(2 * N::columns(wave) + s, N::rows(wave) + i, 1) + lane * 16u);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const float x0 = acc[i][8 * s + 2 * u] + q.linear * f16_lo((uint32_t)lo[u]);
-                const float x1 = acc[i][8 * s + 2 * u + 1] + q.linear * f16_hi((uint32_t)lo[u]);
-                acc[i][8 * s + 2 * u] = x_scale * (x0 + q.linear * f16_lo((uint32_t)hi[u]));
-                acc[i][8 * s + 2 * u + 1] = x_scale * (x1 + q.linear * f16_hi((uint32_t)hi[u]));
+                const float x0 = acc[i][8 * s + 2 * u] + scales.update_linear * f16_lo((uint32_t)lo[u]);
+                const float x1 = acc[i][8 * s + 2 * u + 1] + scales.update_linear * f16_hi((uint32_t)lo[u]);
+                acc[i][8 * s + 2 * u] = scales.update * (x0 + scales.update_linear * f16_lo((uint32_t)hi[u]));
+                acc[i][8 * s + 2 * u + 1] = scales.update * (x1 + scales.update_linear * f16_hi((uint32_t)hi[u]));
             }
         }
 }
@@ -335,14 +353,16 @@ __device__ __forceinline__ void store_result(const NarrowParams& q, int b, int c
 
 // The first iterate's chunks and their parts of A: 12.4 us for 8 x 128 x 4096 bf16 (8 MB in, 17 MB out), 5.3 us for 24 x 5000.
 template <int RB, int DT>
-__global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_first_kernel(NarrowParams q) {
+__global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_first_kernel(NarrowParams q, NewtonCoefficients co) {
     using N = Narrow<RB>;
     __shared__ __attribute__((aligned(1024))) char smem[N::X_BYTES];
     lds_char* const x = (lds_char*)smem;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int b = blockIdx.y, group = blockIdx.x;
+    if (group == 0 && wave == 0) write_unit_scales(q.p, co, b);
     const FirstScale scale = first_scale(q.p, b);
+    if (group == 0 && wave == 0) write_scales(q.p, co, b, scale);
     f32x16 part[N::MINE];
     clear(part);
     const int first = group * q.per_group, last = min(q.chunks, first + q.per_group);
@@ -361,10 +381,11 @@ __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_first_kernel(Na
 // 8 x 128 x 4096: 18 us for 17 MB read and 17 written (L2 and Infinity Cache) and 9.7 GFLOP of fp16 products, all
 // of them one after the other in a workgroup of its own chunk: latencies bound it, as they do the
 // 5.6 us of a step of 24 x 5000 or 6.5 us of 8 x 64 x 512.
-template <int RB, bool LAST>
+template <int RB, bool LAST, bool MEASURED>
 __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_step_kernel(NarrowParams q) {
     using N = Narrow<RB>;
     __shared__ __attribute__((aligned(1024))) char smem[N::X_BYTES + N::A_BYTES];
+    __shared__ double sums[N::WAVES];
     lds_char* const x = (lds_char*)smem;
     lds_char* const a = x + N::X_BYTES;
     const uint32_t x_addr = lds_addr(smem);
@@ -382,6 +403,8 @@ __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_step_kernel(Nar
         }
     };
     load_chunk(first);
+    StepScales scales;
+    if constexpr (!MEASURED) scales = q.p.scales[(int64_t)b * kNewtonMaxSteps + q.step];
 
     // A: this wave's blocks, added up in the order of the parts
     f32x16 mine[N::MINE];
@@ -399,7 +422,13 @@ __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_step_kernel(Nar
             }
         }
     }
-    make_b<RB>(q, a, wave, lane, mine);
+    if constexpr (MEASURED) {
+        SingularBound bound = unit_bound(1.0f);
+        bound.plane = q.p.planes[(int64_t)(q.step & 1) * q.p.batch + b];
+        scales = measured_scales<RB>(mine, sums, bound, q.co, LAST, wave, lane);
+        if (group == 0 && tid == 0) q.p.planes[(int64_t)(~q.step & 1) * q.p.batch + b] = bound.plane;
+    }
+    make_b<RB>(scales, a, wave, lane, mine);
 
     f32x16 part[N::MINE];
     clear(part);
@@ -407,7 +436,7 @@ __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_step_kernel(Nar
         wait_vmcnt<0>();
         __syncthreads();                                // the chunk and B are in LDS
         f32x16 acc[N::ROWS];
-        update_chunk<RB>(q, x, a, wave, lane, q.x_scale, acc);
+        update_chunk<RB>(scales, x, a, wave, lane, acc);
         __syncthreads();                                // all have read the chunk
         if constexpr (LAST) {
             if (chunk + 1 < last) load_chunk(chunk + 1);
@@ -430,8 +459,8 @@ __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_step_kernel(Nar
 template <int RB>
 constexpr int kWholeChunks = RB == 2 ? 4 : 1;
 
-template <int RB, int DT>
-__global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_whole_kernel(NarrowParams q, NarrowSteps steps) {
+template <int RB, int DT, bool MEASURED>
+__global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_whole_kernel(NarrowParams q, NewtonCoefficients co) {
     using N = Narrow<RB>;
     __shared__ __attribute__((aligned(1024))) char smem[kWholeChunks<RB> * N::X_BYTES + N::A_BYTES];
     __shared__ double sums[N::WAVES];
@@ -459,23 +488,33 @@ __global__ __launch_bounds__(Narrow<RB>::THREADS, 1) void narrow_whole_kernel(Na
     for (int w = 0; w < N::WAVES; ++w) squares += sums[w];
     const FirstScale scale = scale_of_norm(__builtin_sqrt(squares), q.p.eps);
 
+    SingularBound bound = scale.bound;
+    __shared__ StepScales table[MEASURED ? 1 : kNewtonMaxSteps];
+    if (!MEASURED && wave == 0) {
+        if (scale.unit) {
+            if (lane < q.p.steps) table[lane] = co.unit[lane];
+        } else {
+            for (int step = 0; step < q.p.steps; ++step) table[step] = step_scales(bound, co.v + 3 * step, step + 1 == q.p.steps);
+        }
+    }
+
     f32x16 mine[N::MINE];
     for (int chunk = 0; chunk < q.chunks; ++chunk) first_chunk<RB, DT>(q, b, chunk, scale, x + chunk * N::X_BYTES, tid);
     __syncthreads();
     clear(mine);
     for (int chunk = 0; chunk < q.chunks; ++chunk) add_gram<RB, SLICES>(x + chunk * N::X_BYTES, wave, lane, mine);
     for (int step = 0; step < q.p.steps; ++step) {
-        q.b_scale = steps.b_scale[step];
-        q.b_linear = steps.b_linear[step];
-        q.linear = steps.linear[step];
         const bool last = step + 1 == q.p.steps;
-        make_b<RB>(q, a, wave, lane, mine);
+        StepScales scales;
+        if constexpr (MEASURED) scales = measured_scales<RB>(mine, sums, bound, co.v + 3 * step, last, wave, lane);
+        else scales = table[step];
+        make_b<RB>(scales, a, wave, lane, mine);
         __syncthreads();
         clear(mine);
         for (int chunk = 0; chunk < q.chunks; ++chunk) {
             lds_char* const at = x + chunk * N::X_BYTES;
             f32x16 acc[N::ROWS];
-            update_chunk<RB>(q, at, a, wave, lane, (last ? 1.0f / kXScale : 1.0f) / kBScale, acc);
+            update_chunk<RB>(scales, at, a, wave, lane, acc);
             if (last) {
                 store_result<RB>(q, b, chunk, wave, lane, acc);
                 continue;
@@ -505,7 +544,7 @@ __global__ __launch_bounds__(NT) void narrow_sum_kernel(const float* in, float* 
 constexpr int kOwnSums = 4;
 
 template <int RB>
-void launch(const NewtonParams& p, const NewtonPlan& plan, const float* co, hipStream_t stream) {
+void launch(const NewtonParams& p, const NewtonPlan& plan, const NewtonCoefficients& co, hipStream_t stream) {
     const dim3 grid((uint32_t)plan.groups, (uint32_t)p.batch);
     const dim3 threads(Narrow<RB>::THREADS);
     const int floats = RB * RB * 1024;
@@ -515,27 +554,24 @@ void launch(const NewtonParams& p, const NewtonPlan& plan, const float* co, hipS
     q.chunks = plan.chunks;
     q.per_group = plan.per_group;
     q.tall = plan.tall ? 1 : 0;
-    q.a_scale = kAScale / (kXScale * kXScale);
-    NarrowSteps steps;
-    for (int s = 0; s < p.steps; ++s) {
-        const float c = newton_c(co + 3 * s);
-        steps.b_scale[s] = c * (kBScale / (kAScale * kAScale));
-        steps.b_linear[s] = c != 0.0f ? co[3 * s + 1] / c * kAScale : 0.0f;
-        steps.linear[s] = co[3 * s] * kBScale;
-    }
     if (plan.groups == 0) {
         const dim3 all((uint32_t)p.batch);
-        if (p.dtype == kOutBf16) hipLaunchKernelGGL((narrow_whole_kernel<RB, kOutBf16>), all, threads, 0, stream, q, steps);
-        else if (p.dtype == kOutF16) hipLaunchKernelGGL((narrow_whole_kernel<RB, kOutF16>), all, threads, 0, stream, q, steps);
-        else hipLaunchKernelGGL((narrow_whole_kernel<RB, kOutF32>), all, threads, 0, stream, q, steps);
+        auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, all, threads, 0, stream, q, co); };
+        auto whole = [&](auto dt) {
+            constexpr int DT = decltype(dt)::value;
+            co.measured ? run(narrow_whole_kernel<RB, DT, true>) : run(narrow_whole_kernel<RB, DT, false>);
+        };
+        if (p.dtype == kOutBf16) whole(std::integral_constant<int, kOutBf16>{});
+        else if (p.dtype == kOutF16) whole(std::integral_constant<int, kOutF16>{});
+        else whole(std::integral_constant<int, kOutF32>{});
         return;
     }
     launch_newton_norm(p, stream);
     q.x_out = p.x[0];
     q.parts_out = (float*)p.a;
-    if (p.dtype == kOutBf16) hipLaunchKernelGGL((narrow_first_kernel<RB, kOutBf16>), grid, threads, 0, stream, q);
-    else if (p.dtype == kOutF16) hipLaunchKernelGGL((narrow_first_kernel<RB, kOutF16>), grid, threads, 0, stream, q);
-    else hipLaunchKernelGGL((narrow_first_kernel<RB, kOutF32>), grid, threads, 0, stream, q);
+    if (p.dtype == kOutBf16) hipLaunchKernelGGL((narrow_first_kernel<RB, kOutBf16>), grid, threads, 0, stream, q, co);
+    else if (p.dtype == kOutF16) hipLaunchKernelGGL((narrow_first_kernel<RB, kOutF16>), grid, threads, 0, stream, q, co);
+    else hipLaunchKernelGGL((narrow_first_kernel<RB, kOutF32>), grid, threads, 0, stream, q, co);
     // the parts of one step are read while the next ones are written: two sets in turn
     const size_t half = plan.a_bytes / 2;
     for (int s = 0; s < p.steps; ++s) {
@@ -551,12 +587,11 @@ void launch(const NewtonParams& p, const NewtonPlan& plan, const float* co, hipS
         }
         q.x_in = p.x[s & 1];
         q.x_out = p.x[(s + 1) & 1];
-        q.b_scale = steps.b_scale[s];
-        q.b_linear = steps.b_linear[s];
-        q.linear = steps.linear[s];
-        q.x_scale = (last ? 1.0f / kXScale : 1.0f) / kBScale;
-        if (last) hipLaunchKernelGGL((narrow_step_kernel<RB, true>), grid, threads, 0, stream, q);
-        else hipLaunchKernelGGL((narrow_step_kernel<RB, false>), grid, threads, 0, stream, q);
+        q.step = s;
+        for (int u = 0; u < 3; ++u) q.co[u] = co.v[3 * s + u];
+        auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, threads, 0, stream, q); };
+        if (co.measured) last ? run(narrow_step_kernel<RB, true, true>) : run(narrow_step_kernel<RB, false, true>);
+        else last ? run(narrow_step_kernel<RB, true, false>) : run(narrow_step_kernel<RB, false, false>);
     }
 }
 
@@ -582,12 +617,12 @@ void newton_narrow_plan(int32_t batch, int64_t r, int64_t c, NewtonPlan* plan) {
     plan->x_bytes = (size_t)batch * plan->chunks * SLICES * rb * 2048;
     plan->a_bytes = (size_t)2 * batch * plan->groups * rb * rb * 4096;
     plan->b_bytes = (size_t)batch * rb * rb * 4096;
-    plan->total = plan->parts_bytes + 2 * plan->x_bytes + plan->a_bytes + plan->b_bytes;
+    plan->total = plan->parts_bytes + 2 * plan->x_bytes + plan->a_bytes + plan->b_bytes + plan->scales_bytes;
 }
 
-void launch_newton_narrow(const NewtonParams& p, const NewtonPlan& plan, const float* coefficients, hipStream_t stream) {
-    if (plan.r == 64) launch<2>(p, plan, coefficients, stream);
-    else launch<4>(p, plan, coefficients, stream);
+void launch_newton_narrow(const NewtonParams& p, const NewtonPlan& plan, const NewtonCoefficients& co, hipStream_t stream) {
+    if (plan.r == 64) launch<2>(p, plan, co, stream);
+    else launch<4>(p, plan, co, stream);
 }
 
 }  // namespace kgw

@@ -636,9 +636,13 @@ kgw_status_t kgw_moe_unpermute_grad(const void* dout, int64_t ld_dout, const voi
  * linear term a X keeps 22 bits, which leaves errors of the size of bf16's own rounding.  KGW_OUT_FP32
  * and KGW_OUT_FP16, and every type where min(m, n) <= 128: every operand keeps 22 bits, with the errors of
  * fp32 arithmetic, at three times the products.
- * Sums are fp32, the norm's 64 bits.  The iterates' singular values must stay below 8
- * (the usual coefficients keep them below 1.3).  A zero matrix gives zeros (eps > 0); infinities or NaN
- * in a matrix give NaN in that matrix alone.  Deterministic.
+ * Sums are fp32, the norm's 64 bits.  The operands' bits count from an upper bound on the iterate's
+ * singular values, which follows from the norm, eps and the coefficients of the steps before, for every matrix;
+ * for coefficients that let the bound and the singular values part (a polynomial that grows steeply
+ * towards 1, or vanishes below it) from the norm of each step's A.  So neither the size of G against eps nor that
+ * of the coefficients matters, as long as every |a|, |b|, |c| is zero or between 2^-100 and 2^100 and no bound, nor
+ * a result, passes 2^120: past that, infinities and NaN.  A zero matrix gives zeros (eps > 0); infinities or NaN in
+ * a matrix give NaN in that matrix alone.  Deterministic.
  * batch <= 65535; m, n <= 2^20; 1 <= steps <= 64; eps >= 0.
  */
 kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_t dtype, int32_t batch, int64_t m,

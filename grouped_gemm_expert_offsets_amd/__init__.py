@@ -788,10 +788,21 @@ def wgrad(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, *, sfa: Optio
 # ----------------------------------------------------------------------------
 # tokens sorted by expert and back
 # ----------------------------------------------------------------------------
+_MOE_MAX_EXPERTS = 2048     # of one kgw_moe_sort
+
+
+def _int32(value: int, what: str) -> int:
+    """The C calls' 32-bit arguments: a number that does not fit would be cut to another one."""
+    if not -2 ** 31 <= int(value) < 2 ** 31:
+        raise ValueError(f"{what} must fit 32 bits, got {value}")
+    return int(value)
+
+
 def kgw_moe_rows(tokens: int, topk: int, num_experts: int, alignment: int = FP8_TOKEN_ALIGN) -> int:
     """Rows that always hold `tokens` tokens of `topk` experts each, every expert's rows padded
     to a multiple of `alignment`."""
-    rows = load_library().kgw_moe_rows(int(tokens), int(topk), int(num_experts), int(alignment))
+    rows = load_library().kgw_moe_rows(int(tokens), _int32(topk, "topk"), _int32(num_experts, "num_experts"),
+                                       _int32(alignment, "alignment"))
     if rows < 0:
         raise ValueError(f"no row count for tokens={tokens}, topk={topk}, num_experts={num_experts}, "
                          f"alignment={alignment}")
@@ -853,16 +864,18 @@ def kgw_moe_sort(ids: torch.Tensor, num_experts: int, *, alignment: int = FP8_TO
     `alignment`), row_of (tokens, topk) and src_of (rows,).  An id outside [0, num_experts)
     gets row -1.  `rows` (default: kgw_moe_rows, which always suffices) bounds the sorted rows; the
     assignments past it get row -1.
+
+    The four are views of one buffer: clone() a small one to keep it without the others, and
+    write to none in place while autograd holds another.
     """
     if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous 2-D int32 or int64 tensor")
     tokens, topk = ids.shape
     E = int(num_experts)
-    if rows is None:
-        rows = kgw_moe_rows(tokens, topk, E, alignment)
-    rows = int(rows)
-    if E < 1 or topk < 1 or rows < 0:
-        raise ValueError("need at least one expert, one expert per token and a non-negative row count")
+    if not 1 <= E <= _MOE_MAX_EXPERTS or topk < 1 or not 1 <= alignment < 2 ** 31 or not (rows is None or 0 <= rows < 2 ** 31):
+        raise ValueError(f"need 1 .. {_MOE_MAX_EXPERTS} experts, one expert per token, an alignment of 1 or more and "
+                         "0 .. 2^31 - 1 rows")
+    rows = kgw_moe_rows(tokens, topk, E, alignment) if rows is None else int(rows)
     device = _on_gpu(ids, "ids")
     lib = load_library()
     need = lib.kgw_moe_sort_workspace_bytes(tokens, topk, E)
@@ -884,7 +897,7 @@ def kgw_moe_permute(x: torch.Tensor, row_of: torch.Tensor, src_of: torch.Tensor,
                     out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
     """x (tokens, hidden) -> out (rows, hidden): out[row_of[t][j]] = x[t], every other row zero.
 
-    fp32, bf16 or fp16; x may have any row stride.  Gradient: kgw_moe_unpermute without weights.
+    fp32, bf16 or fp16; x may have any row stride that keeps its rows apart.  Gradient: kgw_moe_unpermute without weights.
     """
     code = _out_code(x.dtype)
     ld = _rows_2d(x, "x")
@@ -979,7 +992,7 @@ def kgw_newton_schulz(G: torch.Tensor, *, steps: int = 5, coefficients=NEWTON_SC
     code = _out_code(G.dtype)
     if G.dim() not in (2, 3):
         raise ValueError(f"G must be (m, n) or (batch, m, n), got {tuple(G.shape)}")
-    batch = 1 if G.dim() == 2 else G.shape[0]
+    batch = 1 if G.dim() == 2 else _int32(G.shape[0], "the batch")
     m, n = G.shape[-2:]
     if n > 1 and G.stride(-1) != 1:
         raise ValueError("G needs contiguous rows (stride 1 along the last axis)")

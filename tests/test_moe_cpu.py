@@ -137,3 +137,20 @@ def test_launches_that_just_fit_reach_the_device(lib):
     assert permute(lib, tokens=2 ** 23, k=1, rows=2 ** 27 - 2 ** 24 - 8) == device
     assert permute(lib, tokens=2 ** 23 - 1, k=1, rows=8, hidden=8192, ld=8192) == device
     assert unpermute(lib, tokens=2 ** 23, k=1, rows=2 ** 30) == device
+
+
+@pytest.mark.parametrize("kw", [dict(num_experts=2 ** 30), dict(num_experts=2 ** 32 + 4), dict(num_experts=2049),
+                                dict(alignment=2 ** 32 + 128), dict(alignment=2 ** 32 + 128, rows=256), dict(rows=2 ** 31),
+                                dict(rows=-128), dict(num_experts=0, rows=128)])
+def test_binding_refuses_before_it_allocates(monkeypatch, kw):
+    # numbers that do not fit the C call's arguments are not cut to ones that do
+    monkeypatch.setattr(kgw, "_on_gpu", lambda t, what: t.device)
+    monkeypatch.setattr(kgw, "_empty", lambda *a: pytest.fail("memory was asked for"))
+    with pytest.raises(ValueError):
+        kgw.kgw_moe_sort(torch.zeros((4, 2), dtype=torch.int32), **{"num_experts": 4, **kw})
+
+
+def test_rows_arguments_are_not_cut():
+    for bad in [(4, 2, 2 ** 32 + 4, 128), (4, 2, 4, 2 ** 32 + 128), (4, 2 ** 32 + 2, 4, 128)]:
+        with pytest.raises(ValueError):
+            kgw.kgw_moe_rows(*bad)

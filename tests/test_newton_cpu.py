@@ -55,3 +55,10 @@ def test_binding_refuses_without_a_gpu():
         kgw.kgw_newton_schulz(torch.zeros((4, 8), dtype=torch.float64))
     with pytest.raises(ValueError):
         kgw.kgw_newton_schulz(torch.zeros((4, 8)), coefficients=(1.0,))
+
+
+def test_binding_does_not_cut_the_batch(monkeypatch):
+    monkeypatch.setattr(kgw, "_on_gpu", lambda t, what: t.device)
+    monkeypatch.setattr(kgw, "_empty", lambda *a: pytest.fail("memory was asked for"))
+    with pytest.raises(ValueError):
+        kgw.kgw_newton_schulz(torch.zeros((1, 1, 1)).expand(2 ** 32 + 1, 1, 1))

@@ -41,9 +41,8 @@ class MoeLayer:
         counts, offsets, row_of, src_of = kgw.kgw_moe_sort(ids, self.router.shape[1], alignment=ALIGN)
         rows = kgw.kgw_moe_permute(x, row_of, src_of)
         w1, w2 = self.w1.bfloat16(), self.w2.bfloat16()
-        # the weight gradients want as many rows as the offsets say: one number read back a step
-        rows = rows[:int(offsets[-1])]
-        src_of = src_of[:rows.shape[0]]
+        # rows past the last offset belong to no expert: the products neither read nor write them, and nothing has to
+        # be read back to the host
         h = torch.empty((rows.shape[0], w1.shape[2]), dtype=torch.bfloat16, device=x.device)
         kgw.kgw_mgrouped_bf16(rows, w1, offsets=offsets, layout="nn", out=h)
         act = torch.relu(h).square()

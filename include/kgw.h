@@ -26,8 +26,9 @@
  *    Every argument check happens on the host before anything is enqueued, so
  *    a failed call leaves the output untouched.
  *  - Offsets are NOT read on the host by kgw_wgrad_*.  Malformed offsets
- *    (decreasing, unaligned counts, last value != tokens_sum) are the caller's
- *    to rule out, e.g. with kgw_validate_offsets.  The kernels clamp every
+ *    (decreasing, unaligned counts, last value beyond tokens_sum) are the caller's
+ *    to rule out, e.g. with kgw_validate_offsets (which asks for a last value
+ *    equal to tokens_sum).  The kernels clamp every
  *    token range into [0, tokens_sum) and round it down to the kernel's K
  *    step, so malformed offsets can give wrong values for the experts they
  *    touch but never an out-of-bounds access.
@@ -108,7 +109,10 @@ typedef enum {
  *   B        bf16 (tokens_sum, n), row-major (the page's N-major B, stride (n, 1)).
  *   offsets  int32 (num_experts,), inclusive cumulative token counts.
  *            Contract: non-decreasing, every count a multiple of 256,
- *            offsets[num_experts-1] == tokens_sum.
+ *            offsets[num_experts-1] <= tokens_sum.  Tokens from the last offset
+ *            on belong to no expert, whatever A, B and their scales hold there:
+ *            a buffer of fixed size, as kgw_moe_sort fills it, needs no look at
+ *            the offsets on the host.
  *   out      dense (num_experts, hidden, n), row-major, element type out_dtype.
  *   accumulate  1: out[e] += Wgrad[e] (out must be initialised; an empty expert is
  *                  left untouched, bit for bit);

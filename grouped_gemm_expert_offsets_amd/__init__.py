@@ -29,7 +29,7 @@ __all__ = [
     "kgw_wgrad_fp4", "FP4_TOKEN_ALIGN",
     "kgw_quantize_fp8", "kgw_quantize_fp4", "kgw_mgrouped_bf16", "kgw_mgrouped_fp8", "kgw_workspace_bytes",
     "kgw_moe_rows", "kgw_moe_sort", "kgw_moe_permute", "kgw_moe_unpermute", "kgw_moe_unpermute_grad",
-    "kgw_newton_schulz", "NEWTON_SCHULZ_COEFFICIENTS",
+    "kgw_newton_schulz", "NEWTON_SCHULZ_COEFFICIENTS", "KGW_NEWTON_PRECISE",
     "KGW_LAYOUT_NT",
     "KGW_LAYOUT_NN",
     "KGW_A_M_MAJOR", "KGW_B_K_MAJOR", "KGW_RAGGED",
@@ -55,6 +55,7 @@ KGW_B_K_MAJOR = 2          # weight-gradient B stored (n, tokens_sum)
 KGW_RAGGED = 4             # per-expert K-contiguous blocks back to back (with KGW_B_K_MAJOR)
 KGW_LAYOUT_NT = 0          # m-grouped forward: W (E, N, K)
 KGW_LAYOUT_NN = 1          # m-grouped dgrad:   W (E, K, N)
+KGW_NEWTON_PRECISE = 0x100 # with an out_dtype of kgw_newton_schulz: fp32's precision for bf16 results too
 KGW_SCALES_U8 = 0          # uint8 (tokens/128, mn)
 KGW_SCALES_PACKED = 1      # int32 (ceil(tokens/512), mn): four 128-token blocks per word
 KGW_SCALES_PACKED_32 = 2   # int32 (tokens/128, mn): four 32-token blocks per word
@@ -980,14 +981,16 @@ NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 def kgw_newton_schulz(G: torch.Tensor, *, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps: float = 1e-7,
                       out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
-                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                      precise: bool = False, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Orthogonalise G (m, n) or a batch (batch, m, n) by `steps` Newton-Schulz steps:
     X = G / (|G|_F + eps), then X <- a X + (b A + c A A) X with A = X X^T.
 
     G is fp32, bf16 or fp16 with contiguous rows (any row and batch stride), as kgw_wgrad_* writes
-    it.  `coefficients` is one (a, b, c) or one per step.  The result has `out_dtype` (default: G's): bf16
-    runs one fp16 product where fp32 and fp16 (and short sides up to 128) run three and keep fp32's precision.  `workspace`: a uint8
-    tensor of kgw_newton_schulz_workspace_bytes bytes to reuse; allocated here when None.
+    it.  `coefficients` is one (a, b, c) or one per step.  The result has `out_dtype` (default: G's).
+    fp32 and fp16 results, and those of short sides up to 128, take three fp16 products and keep fp32's precision.  Other bf16 results
+    take one and are 1.7e-3 to 2.5e-3 off (of the norm, their own rounding's 1.66e-3 included), unless `precise`, which
+    costs 1.3 to 2.4 times as much and leaves that rounding alone.  `workspace`: a uint8 tensor of
+    kgw_newton_schulz_workspace_bytes bytes to reuse; allocated here when None.
     """
     code = _out_code(G.dtype)
     if G.dim() not in (2, 3):
@@ -1012,7 +1015,7 @@ def kgw_newton_schulz(G: torch.Tensor, *, steps: int = 5, coefficients=NEWTON_SC
         raise ValueError("coefficients must be (a, b, c), or one such triple per step")
     device = _on_gpu(G, "G")
     dtype = out.dtype if out is not None else (G.dtype if out_dtype is None else out_dtype)
-    out_code = _out_code(dtype)
+    out_code = _out_code(dtype) | (KGW_NEWTON_PRECISE if precise else 0)
     out = _result(out, G.shape, dtype, device, "out", stream)
     lib = load_library()
     need = lib.kgw_newton_schulz_workspace_bytes(batch, m, n, out_code)

@@ -8,10 +8,16 @@
 
 namespace {
 
+// The result's type without its flag.
+int32_t result_type(int32_t out_dtype) { return out_dtype & ~KGW_NEWTON_PRECISE; }
+
 bool known_dtype(int32_t d) { return d == KGW_OUT_FP32 || d == KGW_OUT_BF16 || d == KGW_OUT_FP16; }
 
+// Three products of 16-bit halves rather than one.
+bool split(int32_t out_dtype) { return result_type(out_dtype) != KGW_OUT_BF16 || (out_dtype & KGW_NEWTON_PRECISE); }
+
 kgw_status_t check_sizes(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
-    if (batch < 0 || m < 0 || n < 0 || !known_dtype(out_dtype)) return KGW_ERROR_INVALID_VALUE;
+    if (batch < 0 || m < 0 || n < 0 || !known_dtype(result_type(out_dtype))) return KGW_ERROR_INVALID_VALUE;
     // a tile's rows are addressed with 32-bit byte offsets, a grid has 16-bit y and z extents
     if (batch > 65535 || m > ((int64_t)1 << 20) || n > ((int64_t)1 << 20)) return KGW_ERROR_UNSUPPORTED;
     const int64_t r = (m < n ? m : n) + 256, c = (m < n ? n : m) + 256;
@@ -25,7 +31,7 @@ extern "C" {
 
 size_t kgw_newton_schulz_workspace_bytes(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
     if (check_sizes(batch, m, n, out_dtype) != KGW_SUCCESS || batch == 0 || m == 0 || n == 0) return 0;
-    return kgw::newton_plan(batch, m, n, out_dtype).total;
+    return kgw::newton_plan(batch, m, n, split(out_dtype)).total;
 }
 
 kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_t dtype, int32_t batch, int64_t m,
@@ -37,10 +43,10 @@ kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_
     if (steps > kgw::kNewtonMaxSteps) return KGW_ERROR_UNSUPPORTED;
     if (batch == 0 || m == 0 || n == 0) return KGW_SUCCESS;
     if (!G || !out || !workspace || ld < n || (batch > 1 && stride < 0)) return KGW_ERROR_INVALID_VALUE;
-    if (((uintptr_t)G & (dtype == KGW_OUT_FP32 ? 3u : 1u)) || ((uintptr_t)out & (out_dtype == KGW_OUT_FP32 ? 3u : 1u)) ||
+    if (((uintptr_t)G & (dtype == KGW_OUT_FP32 ? 3u : 1u)) || ((uintptr_t)out & (result_type(out_dtype) == KGW_OUT_FP32 ? 3u : 1u)) ||
         ((uintptr_t)workspace & 255u))
         return KGW_ERROR_MISALIGNED;
-    const kgw::NewtonPlan plan = kgw::newton_plan(batch, m, n, out_dtype);
+    const kgw::NewtonPlan plan = kgw::newton_plan(batch, m, n, split(out_dtype));
     if (workspace_bytes < plan.total) return KGW_ERROR_INVALID_VALUE;
     int32_t num_cus = 0, is_gfx950 = 0, num_xcds = 1;
     if (kgw_device_info(&num_cus, &is_gfx950, &num_xcds) != KGW_SUCCESS || !is_gfx950) return KGW_ERROR_DEVICE;
@@ -53,7 +59,7 @@ kgw_status_t kgw_newton_schulz(const void* G, int64_t ld, int64_t stride, int32_
     p.n = n;
     p.batch = batch;
     p.dtype = dtype;
-    p.out_dtype = out_dtype;
+    p.out_dtype = result_type(out_dtype);
     p.steps = steps;
     p.eps = eps;
     char* ws = (char*)workspace;

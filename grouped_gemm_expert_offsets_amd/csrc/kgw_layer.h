@@ -182,7 +182,7 @@ struct NewtonPlan {
     size_t x_bytes, a_bytes, b_bytes, parts_bytes, slab_bytes, scales_bytes, total;
 };
 constexpr int64_t kNarrowMax = 128;
-NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype);
+NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, bool split);
 void newton_narrow_plan(int32_t batch, int64_t r, int64_t c, NewtonPlan* plan);
 void launch_newton_norm(const NewtonParams& p, hipStream_t stream);
 void launch_newton_narrow(const NewtonParams& p, const NewtonPlan& plan, const NewtonCoefficients& co, hipStream_t stream);

@@ -10,9 +10,9 @@
 // with fp32 sums:
 //   one product each (results rounded to bf16): A = hi hi^T, B from fp16 A, B hi.  The
 //     operands' rounding (2^-12) enters only through B X, which is small where the singular values are, and
-//     leaves 0.5e-3 .. 1.7e-3 of the result's norm, at most bf16's own rounding (1.7e-3 rms);
-//     bf16 operands would leave 4e-3 .. 2e-2.
-//   three products each (fp32 and fp16 results): every matrix as hi + lo, hi hi + hi lo + lo hi;
+//     leaves 0.3e-3 (4096 x 7168, power law) to 1.8e-3 (129 x 129, normal) of the result's norm beside bf16's own
+//     rounding of 1.66e-3: 1.69e-3 to 2.45e-3 in all.  bf16 operands would leave 4e-3 .. 2e-2.
+//   three products each (fp32 and fp16 results, bf16 ones where asked for): every matrix as hi + lo, hi hi + hi lo + lo hi;
 //     the dropped lo lo is 2^-24 of the product.  1e-6 .. 1e-5, what fp32 arithmetic leaves.
 // Powers of two keep the planes inside fp16's range, chosen for every matrix and step from a bound 2^e on its singular
 // values (step_scales()): 1 for the first iterate, less where eps outweighs the norm, then the largest value the
@@ -663,6 +663,7 @@ __device__ __forceinline__ void newton_tile(const NewtonGemm& p, char* smem, int
             store_result<kOutBf16>(p, v, b, row0, col0, row, col);
         } else {
             if (p.result_dtype == kOutF16) store_result<kOutF16>(p, v, b, row0, col0, row, col);
+            else if (p.result_dtype == kOutBf16) store_result<kOutBf16>(p, v, b, row0, col0, row, col);
             else store_result<kOutF32>(p, v, b, row0, col0, row, col);
         }
     };
@@ -967,7 +968,7 @@ void launch_newton_norm(const NewtonParams& p, hipStream_t stream) {
     else hipLaunchKernelGGL((newton_norm_kernel<kOutF32>), grid, dim3(NT), 0, stream, p);
 }
 
-NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
+NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, bool split) {
     NewtonPlan plan = {};
     const int64_t r = m < n ? m : n, c = m < n ? n : m;
     plan.tall = m > n;
@@ -978,7 +979,7 @@ NewtonPlan newton_plan(int32_t batch, int64_t m, int64_t n, int32_t out_dtype) {
         newton_narrow_plan(batch, r, c, &plan);
         return plan;
     }
-    plan.split = out_dtype != kOutBf16;
+    plan.split = split;
     // 64-edged tiles while 128-edged ones would leave a quarter of the CUs idle in the update (their number: 2 x 1024 x
     // 1024, 128 of them: 171 against 194 us; 3 x 900 x 900 to fp32, 192: 340 against 364; 1700 x 1700, 196:
     // 286 against 283, to fp32 537 against 513); above, what step_cost() puts lower of 256 and 128.

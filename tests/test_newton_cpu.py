@@ -62,3 +62,13 @@ def test_binding_does_not_cut_the_batch(monkeypatch):
     monkeypatch.setattr(kgw, "_empty", lambda *a: pytest.fail("memory was asked for"))
     with pytest.raises(ValueError):
         kgw.kgw_newton_schulz(torch.zeros((1, 1, 1)).expand(2 ** 32 + 1, 1, 1))
+
+
+def test_precise_results(lib):
+    size, precise = lib.kgw_newton_schulz_workspace_bytes, kgw.KGW_NEWTON_PRECISE
+    assert size(3, 200, 300, kgw.KGW_OUT_BF16 | precise) == size(3, 200, 300, kgw.KGW_OUT_FP32)
+    assert size(3, 200, 300, kgw.KGW_OUT_FP32 | precise) == size(3, 200, 300, kgw.KGW_OUT_FP32)
+    assert size(3, 200, 300, 3 | precise) == 0 and size(3, 200, 300, 1 | 0x200) == 0
+    assert call(lib, odt=3 | precise) == INVALID and call(lib, odt=1 | 0x200) == INVALID
+    assert call(lib, odt=precise, out=P + 2) == MISALIGNED
+    assert call(lib, odt=1 | precise, ws_bytes=100) == INVALID

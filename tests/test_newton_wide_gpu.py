@@ -153,3 +153,11 @@ def test_zero_and_special_matrices_stay_apart(m, n, out):
     assert got[2].isnan().all() and got[3].isnan().all()
     keep = [k for k in range(batch) if k not in (1, 2, 3)]
     check(got[keep], G[keep], triples(CO, 5))
+
+
+@pytest.mark.parametrize("batch,m,n", SHAPES + [(2, 100, 300)])
+def test_precise_bf16_results_are_the_fp32_ones_rounded(batch, m, n):
+    G = gradients(batch, m, n, torch.bfloat16, 8)
+    want = kgw.kgw_newton_schulz(G, out_dtype=torch.float32)
+    assert torch.equal(kgw.kgw_newton_schulz(G, precise=True), want.bfloat16())
+    assert torch.equal(kgw.kgw_newton_schulz(G, precise=True, out_dtype=torch.float32), want)

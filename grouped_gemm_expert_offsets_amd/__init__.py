@@ -882,9 +882,11 @@ def kgw_moe_sort(ids: torch.Tensor, num_experts: int, *, alignment: int = FP8_TO
     need = lib.kgw_moe_sort_workspace_bytes(tokens, topk, E)
     # one allocation for all results and the workspace: five would take a third of a short call's time
     n = tokens * topk
-    results = _empty(rows + n + 2 * E + need // 4, torch.int32, device, stream)
+    size = rows + n + 2 * E + need // 4
+    results = torch.empty(size, dtype=torch.int32, device=device) if stream is None else _empty(size, torch.int32, device, stream)
     src_of, row_of, counts, offsets, _ = results.split((rows, n, E, E, need // 4))
-    _used_on(stream, ids)
+    if stream is not None:
+        _used_on(stream, ids)
     at = results.data_ptr()
     counts_at = at + 4 * (rows + n)
     st = lib.kgw_moe_sort(ids.data_ptr(), ids.element_size(), tokens, topk, E, int(alignment), rows, counts_at,
@@ -910,7 +912,8 @@ def kgw_moe_permute(x: torch.Tensor, row_of: torch.Tensor, src_of: torch.Tensor,
         raise ValueError(f"row_of has {row_of.shape[0]} tokens, x has {tokens}")
     rows = src_of.shape[0]
     out = _result(out, (rows, hidden), x.dtype, device, "out", stream)
-    _used_on(stream, x, row_of, src_of, out)
+    if stream is not None:
+        _used_on(stream, x, row_of, src_of, out)
     st = load_library().kgw_moe_permute(x.data_ptr(), ld, code, row_of.data_ptr(), src_of.data_ptr(), tokens,
                                         row_of.shape[1], rows, hidden, out.data_ptr(), _launch_stream(stream, device))
     _check(st, "kgw_moe_permute")
@@ -933,7 +936,8 @@ def kgw_moe_unpermute(y: torch.Tensor, row_of: torch.Tensor, weights: Optional[t
     rows, hidden = y.shape
     tokens, topk = row_of.shape
     out = _result(out, (tokens, hidden), y.dtype, device, "out", stream)
-    _used_on(stream, y, row_of, weights, out)
+    if stream is not None:
+        _used_on(stream, y, row_of, weights, out)
     st = load_library().kgw_moe_unpermute(y.data_ptr(), ld, code, row_of.data_ptr(), _ptr(weights), tokens, topk,
                                           rows, hidden, out.data_ptr(), _launch_stream(stream, device))
     _check(st, "kgw_moe_unpermute")
@@ -963,7 +967,8 @@ def kgw_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_of: torch.Te
         raise ValueError(f"src_of has {src_of.shape[0]} rows, y has {rows}")
     dy = _result(dy, (rows, hidden), y.dtype, device, "dy", stream)
     dweights = _result(dweights, (tokens, topk), torch.float32, device, "dweights", stream)
-    _used_on(stream, dout, y, row_of, src_of, weights, dy, dweights)
+    if stream is not None:
+        _used_on(stream, dout, y, row_of, src_of, weights, dy, dweights)
     st = load_library().kgw_moe_unpermute_grad(dout.data_ptr(), ld_d, y.data_ptr(), ld_y, code, row_of.data_ptr(),
                                                src_of.data_ptr(), weights.data_ptr(), tokens, topk, rows, hidden,
                                                dy.data_ptr(), dweights.data_ptr(), _launch_stream(stream, device))
@@ -1023,7 +1028,8 @@ def kgw_newton_schulz(G: torch.Tensor, *, steps: int = 5, coefficients=NEWTON_SC
         workspace = _empty(need, torch.uint8, device, stream)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
         raise ValueError("workspace must be a contiguous uint8 tensor on G's device")
-    _used_on(stream, G, out, workspace)
+    if stream is not None:
+        _used_on(stream, G, out, workspace)
     st = lib.kgw_newton_schulz(G.data_ptr(), ld, stride, code, batch, m, n, steps,
                                (ctypes.c_float * (3 * steps))(*values), eps, out.data_ptr(), out_code,
                                workspace.data_ptr(), workspace.numel(), _launch_stream(stream, device))

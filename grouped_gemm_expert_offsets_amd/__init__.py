@@ -980,7 +980,7 @@ def kgw_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_of: torch.Te
 # weight gradients made orthogonal
 # ----------------------------------------------------------------------------
 # a, b, c of X <- a X + (b A + c A A) X: steep at zero, so five steps bring singular values
-# from 0.01 of the norm on into [0.7, 1.2].
+# from 0.01 of the norm on into [0.7, 1.2].  Published with the Muon optimiser (K. Jordan et al., 2024).
 NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 

@@ -623,7 +623,7 @@ kgw_status_t kgw_moe_unpermute_grad(const void* dout, int64_t ld_dout, const voi
 
 /*
  * kgw_newton_schulz -- orthogonalises a batch of matrices, the update that a weight gradient
- * gives an optimiser which moves along orthogonal matrices:
+ * gives an optimiser which moves along orthogonal matrices (published as Muon, K. Jordan et al., 2024):
  *
  *     X = G / (|G|_F + eps);   `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X
  *

@@ -148,7 +148,7 @@ __device__ __forceinline__ void write_scales(const NewtonParams& p, const Newton
     SingularBound s = scale.bound;
     for (int step = 0; step < p.steps; ++step) {
         const StepScales r = step_scales(s, co.v + 3 * step, step + 1 == p.steps);
-        if (lane == 0) p.scales[(int64_t)b * kNewtonMaxSteps + step] = r;
+        if (lane == step) p.scales[(int64_t)b * kNewtonMaxSteps + step] = r;     // the lane that wrote the usual ones
     }
 }
 

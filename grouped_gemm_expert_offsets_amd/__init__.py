@@ -26,8 +26,9 @@ import torch
 
 __all__ = [
     "kgw_wgrad_bf16", "kgw_wgrad_bf16_noalloc", "kgw_wgrad_bf16_ex", "kgw_wgrad_fp8", "kgw_wgrad_fp8_native", "kgw_wgrad_fp8_ex",
-    "kgw_wgrad_fp4", "FP4_TOKEN_ALIGN",
+    "kgw_wgrad_fp4", "FP4_TOKEN_ALIGN", "kgw_wgrad_fp8_rows",
     "kgw_quantize_fp8", "kgw_quantize_fp4", "kgw_mgrouped_bf16", "kgw_mgrouped_fp8", "kgw_workspace_bytes",
+    "kgw_moe_route", "kgw_moe_route_grad", "kgw_moe_act_fp8", "kgw_moe_act_fp8_grad",
     "kgw_moe_rows", "kgw_moe_sort", "kgw_moe_permute", "kgw_moe_unpermute", "kgw_moe_unpermute_grad",
     "kgw_newton_schulz", "NEWTON_SCHULZ_COEFFICIENTS", "KGW_NEWTON_PRECISE",
     "KGW_LAYOUT_NT",
@@ -56,6 +57,10 @@ KGW_RAGGED = 4             # per-expert K-contiguous blocks back to back (with K
 KGW_LAYOUT_NT = 0          # m-grouped forward: W (E, N, K)
 KGW_LAYOUT_NN = 1          # m-grouped dgrad:   W (E, K, N)
 KGW_NEWTON_PRECISE = 0x100 # with an out_dtype of kgw_newton_schulz: fp32's precision for bf16 results too
+KGW_SCORE_SOFTMAX = 0      # the router's shares: softmax of a token's scores
+KGW_SCORE_SIGMOID = 1      # sigmoids, divided by their sum for the balance loss
+KGW_ACT_SWIGLU = 0         # silu(g) * u of rows [g | u]
+KGW_ACT_RELU2 = 1          # relu(h)^2
 KGW_SCALES_U8 = 0          # uint8 (tokens/128, mn)
 KGW_SCALES_PACKED = 1      # int32 (ceil(tokens/512), mn): four 128-token blocks per word
 KGW_SCALES_PACKED_32 = 2   # int32 (tokens/128, mn): four 32-token blocks per word
@@ -73,7 +78,9 @@ EXPORTED_SYMBOLS = ("kgw_wgrad_bf16", "kgw_wgrad_bf16_noalloc", "kgw_wgrad_bf16_
                     "kgw_mgrouped_fp8", "kgw_workspace_bytes", "kgw_validate_offsets_host", "kgw_validate_offsets", "kgw_check_offsets",
                     "kgw_mfma_ceiling", "kgw_status_string", "kgw_device_info", "kgw_moe_rows",
                     "kgw_moe_sort_workspace_bytes", "kgw_moe_sort", "kgw_moe_permute", "kgw_moe_unpermute",
-                    "kgw_moe_unpermute_grad", "kgw_newton_schulz", "kgw_newton_schulz_workspace_bytes")
+                    "kgw_moe_unpermute_grad", "kgw_newton_schulz", "kgw_newton_schulz_workspace_bytes", "kgw_wgrad_fp8_rows",
+                    "kgw_moe_route_workspace_bytes", "kgw_moe_route", "kgw_moe_route_grad", "kgw_moe_act_fp8",
+                    "kgw_moe_act_fp8_grad")
 
 
 def load_library():
@@ -135,6 +142,19 @@ def load_library():
                                       ctypes.c_float, p, i32, p, sz, p]
     lib.kgw_newton_schulz_workspace_bytes.restype = sz
     lib.kgw_newton_schulz_workspace_bytes.argtypes = [i32, i64, i64, i32]
+    f32 = ctypes.c_float
+    lib.kgw_wgrad_fp8_rows.restype = ctypes.c_int
+    lib.kgw_wgrad_fp8_rows.argtypes = [p, p, p, p, p, i32, i64, i64, i64, p, p, i32, i32, p, sz, p]
+    lib.kgw_moe_route_workspace_bytes.restype = sz
+    lib.kgw_moe_route_workspace_bytes.argtypes = [i64, i32]
+    lib.kgw_moe_route.restype = ctypes.c_int
+    lib.kgw_moe_route.argtypes = [p, i64, i32, p, p, i32, i64, i32, i32, i32, i32, f32, p, p, p, p, p, p, sz, p]
+    lib.kgw_moe_route_grad.restype = ctypes.c_int
+    lib.kgw_moe_route_grad.argtypes = [p, i64, i32, p, p, i32, p, p, p, i64, i32, i32, i32, i32, f32, p, p]
+    lib.kgw_moe_act_fp8.restype = ctypes.c_int
+    lib.kgw_moe_act_fp8.argtypes = [p, i64, i32, i32, p, i32, i64, i64, p, p, p, p, p]
+    lib.kgw_moe_act_fp8_grad.restype = ctypes.c_int
+    lib.kgw_moe_act_fp8_grad.argtypes = [p, i64, i32, i32, p, p, p, i32, i64, i64, p, p, p, p, p]
     lib.kgw_status_string.restype = ctypes.c_char_p
     lib.kgw_status_string.argtypes = [ctypes.c_int]
     lib.kgw_device_info.restype = ctypes.c_int
@@ -523,6 +543,43 @@ def _fp8_call(name, A, sfa, B, sfb, offsets, out, out_dtype, accumulate, validat
                 hidden, n, T, _ptr(out), _ptr(ptrs), code,
                 int(bool(accumulate)), _ptr(ws), ws_bytes, _stream_ptr(stream))
     _check(st, name)
+    return out if outs is None else outs
+
+
+def kgw_wgrad_fp8_rows(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, *,
+                       sb: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, outs=None,
+                       out_dtype: torch.dtype = torch.float32, accumulate: bool = False, validate: bool = False,
+                       stream=None, split_k: bool = True):
+    """Weight gradients from 8-bit token rows, scaled along the rows as the forward products take them:
+    e4m3 A (T, hidden) with UE8M0 sa (ceil(hidden/128), T), and B (T, n) bf16, or e4m3 with sb
+    (ceil(n/128), T).  Counts are multiples of 128; exact products, fp32 sums; outputs as for kgw_wgrad_bf16_ex."""
+    fp8_types = (torch.uint8, torch.float8_e4m3fn)
+    if A.dtype not in fp8_types or B.dtype not in (fp8_types if sb is not None else (torch.bfloat16,)):
+        raise ValueError("kgw_wgrad_fp8_rows takes e4m3fn (or raw uint8) A, and B bfloat16 without or e4m3fn with sb")
+    if A.dim() != 2 or B.dim() != 2 or A.shape[0] != B.shape[0]:
+        raise ValueError(f"A must be (T, hidden) and B (T, n), got {tuple(A.shape)} and {tuple(B.shape)}")
+    T, hidden = A.shape
+    n = B.shape[1]
+    device = A.device
+    for s, cols, what in ((sa, hidden, "sa"), (sb, n, "sb")):
+        if s is None and what == "sb":
+            continue
+        shape = (-(-cols // FP8_TOKEN_ALIGN), T)
+        if s is None or s.dtype != torch.uint8 or tuple(s.shape) != shape or not s.is_contiguous() or s.device != device:
+            raise ValueError(f"{what} must be a contiguous uint8 {shape} tensor on the operands' device")
+    if not (A.is_contiguous() and B.is_contiguous()) or B.device != device:
+        raise ValueError("A and B must be contiguous, on the same device")
+    _check_offsets(offsets, device)
+    E = offsets.numel()
+    out, outs, ptrs, code = _outputs(out, outs, E, hidden, n, out_dtype, accumulate, device, stream)
+    if validate:
+        kgw_validate_offsets(offsets, T, FP8_TOKEN_ALIGN, stream=stream)
+    ws, ws_bytes = _workspace(E, hidden, n, T, False, device, stream, split_k)
+    _used_on(stream, A, sa, B, sb, offsets, out, *(outs or ()))
+    st = load_library().kgw_wgrad_fp8_rows(_ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(offsets), E, hidden, n, T, _ptr(out),
+                                           _ptr(ptrs), code, int(bool(accumulate)), _ptr(ws), ws_bytes,
+                                           _stream_ptr(stream))
+    _check(st, "kgw_wgrad_fp8_rows")
     return out if outs is None else outs
 
 
@@ -974,6 +1031,199 @@ def kgw_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_of: torch.Te
                                                dy.data_ptr(), dweights.data_ptr(), _launch_stream(stream, device))
     _check(st, "kgw_moe_unpermute_grad")
     return dy, dweights
+
+
+# ----------------------------------------------------------------------------
+# the router
+# ----------------------------------------------------------------------------
+_ROUTE_MAX_TOPK = 64
+_SCORES = {"softmax": KGW_SCORE_SOFTMAX, "sigmoid": KGW_SCORE_SIGMOID}
+
+
+def _route_args(scores: torch.Tensor, topk: int, mask, score: str):
+    """Checks what the router and its gradient share: (device, type code, row stride, score code)."""
+    code = _out_code(scores.dtype)
+    ld = _rows_2d(scores, "scores")
+    device = _on_gpu(scores, "scores")
+    tokens, E = scores.shape
+    if not 1 <= E <= _MOE_MAX_EXPERTS or not 1 <= topk <= min(E, _ROUTE_MAX_TOPK):
+        raise ValueError(f"need 1 .. {_MOE_MAX_EXPERTS} experts and 1 .. min(experts, {_ROUTE_MAX_TOPK}) a token, got {E}, {topk}")
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (tokens,) or
+                             mask.device != device or not mask.is_contiguous()):
+        raise ValueError(f"mask must be a contiguous bool ({tokens},) tensor on {device}")
+    if score not in _SCORES:
+        raise ValueError(f"score is 'softmax' or 'sigmoid', got {score!r}")
+    return device, code, ld, _SCORES[score]
+
+
+def _route_ids(ids: torch.Tensor, tokens: int, device):
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2 or ids.shape[0] != tokens or \
+            not ids.is_contiguous() or ids.device != device:
+        raise ValueError(f"ids must be a contiguous int32 or int64 ({tokens}, topk) tensor on {device}")
+
+
+def kgw_moe_route(scores: torch.Tensor, topk: int, *, ids: Optional[torch.Tensor] = None,
+                  mask: Optional[torch.Tensor] = None, score: str = "softmax", renormalize: bool = True,
+                  scale: float = 1.0, stream=None):
+    """Route tokens by their scores (tokens, experts), fp32, bf16 or fp16 with any row stride.
+
+    Returns (ids, weights, counts, loss, slope): int32 ids (tokens, topk) of the largest scores (ties to the lowest
+    index), what kgw_moe_sort takes; float32 weights (tokens, topk), what kgw_moe_unpermute takes; int32 counts
+    (experts,); the balance loss, a float32 scalar that is 1 where all experts are used alike; and slope (experts,), its
+    derivative by every token's shares, for kgw_moe_route_grad.
+
+    Shares are softmax(scores), or sigmoids divided by their sum; weights are the chosen shares (score="sigmoid": the
+    sigmoids), divided by their sum if `renormalize`, times `scale`.  A score of -inf is an expert that its token may not
+    take, a False in `mask` (tokens,) a token that takes none: id -1, weight 0, no part in the loss.  `ids`
+    (int32 or int64, (tokens, topk)) are experts chosen elsewhere.
+
+    ids and counts are views of one buffer, weights, loss and slope of another.
+    """
+    topk = int(topk)
+    device, code, ld, score_code = _route_args(scores, topk, mask, score)
+    tokens, E = scores.shape
+    if ids is not None:
+        _route_ids(ids, tokens, device)
+        if ids.shape[1] != topk:
+            raise ValueError(f"ids has {ids.shape[1]} experts a token, topk is {topk}")
+    lib = load_library()
+    n = tokens * topk
+    need = lib.kgw_moe_route_workspace_bytes(tokens, E)
+    whole = _empty(n + E, torch.int32, device, stream)
+    real = _empty(n + E + 1 + need // 4, torch.float32, device, stream)
+    if stream is not None:
+        _used_on(stream, scores, mask, ids)
+    at, at_real = whole.data_ptr(), real.data_ptr()
+    st = lib.kgw_moe_route(scores.data_ptr(), ld, code, _ptr(mask), _ptr(ids), 0 if ids is None else ids.element_size(),
+                           tokens, E, topk, score_code, int(bool(renormalize)), scale, at, at_real, at + 4 * n,
+                           at_real + 4 * (n + E), at_real + 4 * n, at_real + 4 * (n + E + 1) if need else None, need,
+                           _launch_stream(stream, device))
+    _check(st, "kgw_moe_route")
+    chosen, counts = whole.split((n, E))
+    weights, slope, loss, _ = real.split((n, E, 1, need // 4))
+    return chosen.view(tokens, topk), weights.view(tokens, topk), counts, loss.view(()), slope
+
+
+def kgw_moe_route_grad(scores: torch.Tensor, ids: torch.Tensor, dweights: Optional[torch.Tensor], *,
+                       dloss: Optional[torch.Tensor] = None, slope: Optional[torch.Tensor] = None,
+                       mask: Optional[torch.Tensor] = None, score: str = "softmax", renormalize: bool = True,
+                       scale: float = 1.0, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of sum(dweights * weights) + dloss * loss of kgw_moe_route by its scores, (tokens, experts) in their type.
+
+    dweights float32 (tokens, topk) or None; dloss a float32 tensor of one value, with the slope that kgw_moe_route
+    gave (or one made of counts summed over ranks: experts * counts / (topk * tokens^2)); both or neither.
+    mask, score, renormalize and scale as given to kgw_moe_route.
+    """
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be (tokens, topk), got {tuple(ids.shape)}")
+    topk = ids.shape[1]
+    device, code, ld, score_code = _route_args(scores, topk, mask, score)
+    tokens, E = scores.shape
+    _route_ids(ids, tokens, device)
+    if (dloss is None) != (slope is None):
+        raise ValueError("pass dloss and slope, or neither")
+    for t, shape, what in ((dweights, (tokens, topk), "dweights"), (slope, (E,), "slope")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or
+                              t.device != device):
+            raise ValueError(f"{what} must be a contiguous float32 {shape} tensor on {device}")
+    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1 or dloss.device != device):
+        raise ValueError(f"dloss must be a float32 tensor of one value on {device}")
+    out = _result(out, (tokens, E), scores.dtype, device, "out", stream)
+    if stream is not None:
+        _used_on(stream, scores, ids, dweights, dloss, slope, mask, out)
+    st = load_library().kgw_moe_route_grad(scores.data_ptr(), ld, code, _ptr(mask), ids.data_ptr(), ids.element_size(),
+                                           _ptr(dweights), _ptr(dloss), _ptr(slope), tokens, E, topk, score_code,
+                                           int(bool(renormalize)), scale, out.data_ptr(), _launch_stream(stream, device))
+    _check(st, "kgw_moe_route_grad")
+    return out
+
+
+# ----------------------------------------------------------------------------
+# the activation and its 8-bit checkpoint
+# ----------------------------------------------------------------------------
+_ACTS = {"swiglu": KGW_ACT_SWIGLU, "relu2": KGW_ACT_RELU2}
+
+
+def _act_args(act: str, offsets: Optional[torch.Tensor], device):
+    if act not in _ACTS:
+        raise ValueError(f"act is 'swiglu' or 'relu2', got {act!r}")
+    if offsets is not None:
+        _check_offsets(offsets, device)
+
+
+def _act_rows(t: Optional[torch.Tensor], rows: int, cols: int, halves: int, fp8: bool, dtype, device, what: str, stream):
+    """A result of the activation and its scales: rows of `dtype`, or e4m3 bytes."""
+    t = _result(t, (rows, cols), torch.uint8 if fp8 else dtype, device, what, stream)
+    blocks = halves * -(-(cols // halves) // FP8_TOKEN_ALIGN)
+    return t, _empty((blocks, rows), torch.uint8, device, stream) if fp8 else None
+
+
+def kgw_moe_act_fp8(h: torch.Tensor, *, act: str = "swiglu", offsets: Optional[torch.Tensor] = None, fp8: bool = False,
+                    save: bool = True, out: Optional[torch.Tensor] = None, stream=None):
+    """The activation between the expert products, keeping its input in 8 bits: (y, y_scales, saved, saved_scales).
+
+    act "swiglu": h (rows, 2 inner) = [g | u], y = silu(g) * u; "relu2": h (rows, inner), y = relu(h)^2.  h is fp32, bf16 or
+    fp16 with any row stride, inner a multiple of 8.  y (rows, inner) has h's type and y_scales is None; with `fp8`
+    it is e4m3 bytes (uint8) with UE8M0 y_scales (ceil(inner/128), rows), the A of kgw_mgrouped_fp8 and kgw_wgrad_fp8_rows.
+    saved and saved_scales are h in that form (swiglu: the blocks of g, then those of u), for kgw_moe_act_fp8_grad;
+    None with save=False.  With `offsets` the rows from the last one on are neither read nor written.
+    """
+    code = _out_code(h.dtype)
+    ld = _rows_2d(h, "h")
+    device = _on_gpu(h, "h")
+    _act_args(act, offsets, device)
+    halves = 2 if act == "swiglu" else 1
+    rows, wide = h.shape
+    if wide % (8 * halves):
+        raise ValueError(f"h must have {'twice ' if halves == 2 else ''}a multiple of 8 columns, got {wide}")
+    inner = wide // halves
+    y, y_scales = _act_rows(out, rows, inner, 1, fp8, h.dtype, device, "out", stream)
+    saved, saved_scales = _act_rows(None, rows, wide, halves, True, None, device, "saved", stream) if save else (None, None)
+    if stream is not None:
+        _used_on(stream, h, offsets, y)
+    st = load_library().kgw_moe_act_fp8(h.data_ptr(), ld, code, _ACTS[act], _ptr(offsets),
+                                        0 if offsets is None else offsets.numel(), rows, inner, y.data_ptr(),
+                                        _ptr(y_scales), _ptr(saved), _ptr(saved_scales), _launch_stream(stream, device))
+    _check(st, "kgw_moe_act_fp8")
+    return y, y_scales, saved, saved_scales
+
+
+def kgw_moe_act_fp8_grad(dy: torch.Tensor, saved: torch.Tensor, saved_scales: torch.Tensor, *, act: str = "swiglu",
+                         offsets: Optional[torch.Tensor] = None, fp8: bool = False, again: bool = False,
+                         again_fp8: Optional[bool] = None, dh: Optional[torch.Tensor] = None,
+                         y: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of kgw_moe_act_fp8 at the h it kept: (dh, dh_scales, y, y_scales).
+
+    dy (rows, inner) is fp32, bf16 or fp16 with any row stride.  dh has dy's type and h's shape; with `fp8` it is in
+    8 bits, scales laid out as saved_scales.  `again` also gives y = act(h) of the kept h (else None), in 8
+    bits if `again_fp8` (default: as `fp8`).
+    """
+    code = _out_code(dy.dtype)
+    ld = _rows_2d(dy, "dy")
+    device = _on_gpu(dy, "dy")
+    _act_args(act, offsets, device)
+    halves = 2 if act == "swiglu" else 1
+    rows, inner = dy.shape
+    if inner % 8:
+        raise ValueError(f"dy must have a multiple of 8 columns, got {inner}")
+    blocks = halves * -(-inner // FP8_TOKEN_ALIGN)
+    for t, shape, what in ((saved, (rows, halves * inner), "saved"), (saved_scales, (blocks, rows), "saved_scales")):
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or tuple(t.shape) != shape or not t.is_contiguous() or \
+                t.device != device:
+            raise ValueError(f"{what} must be a contiguous uint8 {shape} tensor on {device}")
+    if y is not None and not again:
+        raise ValueError("y is written with again=True only")
+    again_fp8 = fp8 if again_fp8 is None else again_fp8
+    dh, dh_scales = _act_rows(dh, rows, halves * inner, halves, fp8, dy.dtype, device, "dh", stream)
+    y, y_scales = _act_rows(y, rows, inner, 1, again_fp8, dy.dtype, device, "y", stream) if again else (None, None)
+    if stream is not None:
+        _used_on(stream, dy, saved, saved_scales, offsets, dh, y)
+    st = load_library().kgw_moe_act_fp8_grad(dy.data_ptr(), ld, code, _ACTS[act], saved.data_ptr(), saved_scales.data_ptr(),
+                                             _ptr(offsets), 0 if offsets is None else offsets.numel(), rows, inner,
+                                             dh.data_ptr(), _ptr(dh_scales), _ptr(y), _ptr(y_scales),
+                                             _launch_stream(stream, device))
+    _check(st, "kgw_moe_act_fp8_grad")
+    return dh, dh_scales, y, y_scales
 
 
 # ----------------------------------------------------------------------------

@@ -96,7 +96,7 @@ kgw_status_t check_common(const void* A, const void* B, const int32_t* offsets, 
     return KGW_SUCCESS;
 }
 
-enum class Kernel { kBf16, kFp8, kFp8Native, kFp4 };
+enum class Kernel { kBf16, kFp8, kFp8Native, kFp4, kFp8Rows };
 
 // Split-K: cut every expert's token range into `split` chunks when the output
 // tiles alone would leave most CUs idle (few experts, small hidden x n) and the
@@ -152,12 +152,13 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
                  int32_t scale_format, const int32_t* offsets, int32_t num_experts, int64_t hidden, int64_t n,
                  int64_t tokens_sum, void* out, void* const* out_ptrs, int32_t out_dtype, int32_t accumulate,
                  void* workspace, size_t workspace_bytes, void* stream, int32_t layout = 0) {
-    const bool fp8 = kernel != Kernel::kBf16;        // block-scaled operands (fp8 or fp4)
+    const bool rows = kernel == Kernel::kFp8Rows;    // 8-bit token rows through the bf16 kernel
+    const bool fp8 = kernel != Kernel::kBf16 && !rows;   // operands scaled along the tokens (fp8 or fp4)
     const bool fp4 = kernel == Kernel::kFp4;
     const int64_t bm = fp8 ? kgw::kFp8BM : kgw::kBf16BM;
     const int64_t bn = fp8 ? kgw::kFp8BN : kgw::kBf16BN;
-    const int64_t talign = fp4 ? KGW_FP4_TOKEN_ALIGN : (fp8 ? KGW_FP8_TOKEN_ALIGN : KGW_BF16_TOKEN_ALIGN);
-    const int64_t nalign = (fp8 && !fp4) ? 16 : 8;
+    const int64_t talign = fp4 ? KGW_FP4_TOKEN_ALIGN : (fp8 || rows ? KGW_FP8_TOKEN_ALIGN : KGW_BF16_TOKEN_ALIGN);
+    const int64_t nalign = (fp8 && !fp4) || (rows && sfb) ? 16 : 8;
     static_assert(KGW_OUT_FP32 == kgw::kOutF32 && KGW_OUT_BF16 == kgw::kOutBf16 && KGW_OUT_FP16 == kgw::kOutF16,
                   "output kind codes");
     static_assert(KGW_SCALES_U8 == kgw::kScalesU8 && KGW_SCALES_PACKED == kgw::kScalesPacked &&
@@ -173,6 +174,12 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
     if (fp4 && scale_format != KGW_SCALES_PACKED_32) return KGW_ERROR_INVALID_VALUE;
     if (fp8 && scale_format == KGW_SCALES_PACKED_32 && (((uintptr_t)sfa | (uintptr_t)sfb) & 3u))
         return KGW_ERROR_MISALIGNED;
+    if (rows) {
+        if (tokens_sum > 0 && hidden > 0 && n > 0 && !sfa) return KGW_ERROR_INVALID_VALUE;
+        if (hidden % 16 != 0 || (((uintptr_t)sfa | (uintptr_t)sfb) & 3u)) return KGW_ERROR_MISALIGNED;
+        // one step's 32 token rows are addressed with 32-bit offsets
+        if (64 * hidden >= ((int64_t)1 << 31)) return KGW_ERROR_UNSUPPORTED;
+    }
     if (layout & ~(KGW_A_M_MAJOR | KGW_B_K_MAJOR | KGW_RAGGED)) return KGW_ERROR_INVALID_VALUE;
     if ((layout & KGW_RAGGED) && (layout & (KGW_A_M_MAJOR | KGW_B_K_MAJOR)) != KGW_B_K_MAJOR)
         return KGW_ERROR_INVALID_VALUE;      // ragged blocks are K-contiguous for both operands
@@ -233,7 +240,7 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
     // for a finer interleave of the output stores: E=256 / 256-token experts 4.02 -> 3.85 ms
     // and 4.01 -> 3.84 ms (one process, two passes), with eight-tile columns still better
     // than four (3.71 vs 3.91 ms).
-    if (short_experts && kernel == Kernel::kBf16) p.num_xcds = 1;
+    if (short_experts && !fp8) p.num_xcds = 1;
     int out_kind = out_dtype;              // KGW_OUT_* values are the kernels' output kinds
 
     // Split-K when planned and the caller's workspace holds the partials;
@@ -251,7 +258,7 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
     p.sched = nullptr;
     const int grid = p.num_items < d.num_cus ? p.num_items : d.num_cus;
     hipError_t err = hipSuccess;
-    if (kernel == Kernel::kBf16 && !split && dynamic_plan(num_experts, hidden, n, tokens_sum, d.num_cus) &&
+    if (!fp8 && !split && dynamic_plan(num_experts, hidden, n, tokens_sum, d.num_cus) &&
         workspace && workspace_bytes >= kgw::kSchedWords * sizeof(int32_t) && aligned16(workspace) &&
         grid % d.num_xcds == 0) {
         p.sched = (int32_t*)workspace;
@@ -272,6 +279,7 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
                                                         (hipStream_t)stream)
                          : kgw::launch_wgrad_fp8(p, out_kind, grid, (hipStream_t)stream);
             break;
+        case Kernel::kFp8Rows: err = kgw::launch_wgrad_fp8_rows(p, out_kind, grid, (hipStream_t)stream); break;
         case Kernel::kFp4: err = kgw::launch_wgrad_fp4(p, out_kind, grid, (hipStream_t)stream); break;
         default: err = kgw::launch_wgrad_fp8_native(p, out_kind, grid, (hipStream_t)stream); break;
     }
@@ -352,6 +360,14 @@ kgw_status_t kgw_wgrad_fp4(const void* A, const void* sfa, const void* B, const 
                            void* const* out_ptrs, int32_t out_dtype, int32_t accumulate, void* workspace,
                            size_t workspace_bytes, void* stream) {
     return run(Kernel::kFp4, A, sfa, B, sfb, KGW_SCALES_PACKED_32, offsets, num_experts, hidden, n, tokens_sum, out,
+               out_ptrs, out_dtype, accumulate, workspace, workspace_bytes, stream);
+}
+
+kgw_status_t kgw_wgrad_fp8_rows(const void* A, const uint8_t* sa, const void* B, const uint8_t* sb,
+                                const int32_t* offsets, int32_t num_experts, int64_t hidden, int64_t n,
+                                int64_t tokens_sum, void* out, void* const* out_ptrs, int32_t out_dtype,
+                                int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+    return run(Kernel::kFp8Rows, A, sa, B, sb, KGW_SCALES_U8, offsets, num_experts, hidden, n, tokens_sum, out,
                out_ptrs, out_dtype, accumulate, workspace, workspace_bytes, stream);
 }
 

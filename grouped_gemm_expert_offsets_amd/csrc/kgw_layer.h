@@ -1,5 +1,6 @@
 // Host/device launch contract of the operators around the grouped products: the token sort,
-// permute and unpermute (kgw_moe.hip) and the Newton-Schulz orthogonalisation (kgw_newton.hip).
+// permute and unpermute (kgw_moe.hip), the router (kgw_route.hip), the activation with its 8-bit checkpoint (kgw_act.hip)
+// and the Newton-Schulz orthogonalisation (kgw_newton.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -55,6 +56,73 @@ hipError_t launch_moe_sort(const MoeSortParams& p, bool wide_ids, hipStream_t st
 // Workgroups that launch_moe_rows() starts.
 int64_t moe_rows_grid(int op, int dtype, int64_t tokens, int64_t rows, int64_t hidden);
 hipError_t launch_moe_rows(const MoeRowsParams& p, int op, int dtype, hipStream_t stream);
+
+// ----------------------------------------------------------------------------
+// the router (kgw_route.hip)
+// ----------------------------------------------------------------------------
+constexpr int kRouteMaxTopk = 64;
+constexpr int kRouteThreads = 256;      // of a workgroup of several
+constexpr int kRouteGroups = 1024;      // workgroups of a call, at most
+
+struct RouteParams {
+    const void* scores;     // (tokens, experts)
+    const uint8_t* mask;    // (tokens,) or NULL
+    const void* given;      // (tokens, topk) ids that the caller has, or NULL; the gradient: the ids
+    int32_t* ids;           // (tokens, topk)
+    float* weights;         // (tokens, topk)
+    int32_t* counts;        // (experts,)
+    float* loss;            // (1,)
+    float* slope;           // (experts,); the gradient: the caller's
+    const float* dweights;  // gradient only, from here on: (tokens, topk) or NULL
+    const float* dloss;     // (1,) or NULL
+    void* dscores;          // (tokens, experts), contiguous
+    // workspace, with more than one workgroup: every workgroup's sums and counts (2 experts words), its tokens, the
+    // finishing workgroups' parts of the loss and their counter
+    float* part;
+    float* tokens_part;
+    float* dots;
+    int32_t* arrived;
+    int64_t ld;             // of scores, in elements
+    int64_t tokens;
+    int32_t experts;
+    int32_t topk;
+    int32_t id_bytes;
+    int32_t renormalize;
+    int32_t groups;
+    float scale;
+};
+
+struct RoutePlan {
+    int rows;               // tokens that a workgroup of several takes at a time
+    int groups;             // workgroups (1: no workspace)
+    int finish;             // workgroups that add the others' parts
+    size_t words;           // of workspace
+};
+RoutePlan route_plan(int64_t tokens, int experts);
+hipError_t launch_route(const RouteParams& p, int dtype, bool sigmoid, hipStream_t stream);
+hipError_t launch_route_grad(const RouteParams& p, int dtype, bool sigmoid, hipStream_t stream);
+
+// ----------------------------------------------------------------------------
+// the activation and its 8-bit checkpoint (kgw_act.hip)
+// ----------------------------------------------------------------------------
+struct ActParams {
+    const void* h;          // (rows, inner), gated (rows, 2 inner); forward only
+    const void* dy;         // (rows, inner); gradient only
+    uint8_t* saved;         // e4m3 of h, contiguous (forward: NULL keeps none)
+    uint8_t* saved_scales;  // (blocks of a row, rows)
+    void* y;                // (rows, inner), contiguous (gradient: NULL for none)
+    uint8_t* y_scales;      // y is e4m3 with these scales (NULL: y has the rows' type)
+    void* dh;               // as h, contiguous; gradient only
+    uint8_t* dh_scales;     // likewise
+    const int32_t* offsets; // (num_experts,) or NULL: rows from the last one on are left alone
+    int64_t ld_h, ld_dy;    // row strides in elements
+    int64_t rows, inner;
+    int32_t num_experts;
+    int32_t group_rows;     // rows of a workgroup
+};
+int act_group_rows(int64_t rows, int64_t inner);
+int64_t act_grid(int64_t rows, int64_t inner);
+hipError_t launch_act(const ActParams& p, int dtype, bool gated, bool grad, hipStream_t stream);
 
 // ----------------------------------------------------------------------------
 // Newton-Schulz orthogonalisation (kgw_newton.hip)

@@ -309,6 +309,29 @@ kgw_status_t kgw_wgrad_fp4(const void* A, const void* sfa, const void* B, const 
                            size_t workspace_bytes, void* stream);
 
 /*
+ * kgw_wgrad_fp8_rows -- the weight gradient of 8-bit token rows as the forward products take them: A is what
+ * kgw_mgrouped_fp8 read as its A (or what kgw_moe_act_fp8 kept, or kgw_quantize_fp8 with token_axis 1 made of
+ * (tokens, hidden) rows), so that no second copy with scales along the tokens is made or kept.
+ *
+ *     out[e] (=|+=) a[begin:end, :]^T @ b[begin:end, :]
+ *     a(t, m) = e4m3(A[t, m]) * 2^(sa[m/128, t] - 127)      b likewise, or the bf16 B itself
+ *
+ *   A    e4m3 bytes (tokens_sum, hidden), row-major, 16-byte aligned; hidden a multiple of 16 (KGW_ERROR_MISALIGNED)
+ *        and below 2^25 (KGW_ERROR_UNSUPPORTED).
+ *   sa   uint8 (ceil(hidden/128), tokens_sum), 4-byte aligned: the last block of a row may be shorter.
+ *   B    sb NULL: bf16 (tokens_sum, n), n a multiple of 8.  Else e4m3 bytes (tokens_sum, n), n a multiple of 16, with
+ *        sb uint8 (ceil(n/128), tokens_sum).
+ *   Every value is converted exactly to bf16 with its scale folded in (one that falls below bf16's smallest normal value
+ *   becomes a subnormal or zero), products are summed in fp32 on the bf16 MFMA.  A scale byte of 0xFF makes the outputs that it reaches NaN.
+ *   Counts must be multiples of 128.  offsets, out / out_ptrs, out_dtype, accumulate, sizes and errors as for
+ *   kgw_wgrad_bf16_ex; workspace as for it, kgw_workspace_bytes(..., fp8 = 0) bytes.
+ */
+kgw_status_t kgw_wgrad_fp8_rows(const void* A, const uint8_t* sa, const void* B, const uint8_t* sb,
+                                const int32_t* offsets, int32_t num_experts, int64_t hidden, int64_t n,
+                                int64_t tokens_sum, void* out, void* const* out_ptrs, int32_t out_dtype,
+                                int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * kgw_quantize_fp8 -- produce the fp8 operands of kgw_wgrad_fp8 from bf16 on the
  * device: OCP e4m3fn bytes plus one UE8M0 scale byte per 128 tokens, the
  * blocks running along the token axis (llm-infra-atlas "05 Grouped GEMM",
@@ -620,6 +643,91 @@ kgw_status_t kgw_moe_unpermute_grad(const void* dout, int64_t ld_dout, const voi
                                     const int32_t* row_of, const int32_t* src_of, const float* weights,
                                     int64_t tokens, int32_t topk, int64_t rows, int64_t hidden, void* dy,
                                     float* dweights, void* stream);
+
+/* How the router turns a token's scores into shares. */
+typedef enum {
+    KGW_SCORE_SOFTMAX = 0,   /* u = exp(score - largest),  p = u / sum u                              */
+    KGW_SCORE_SIGMOID = 1    /* u = 1 / (1 + exp(-score)), p = u / (sum u + 1e-20)                    */
+} kgw_score_t;
+
+/* Device scratch of kgw_moe_route, 4-byte aligned, no initial contents (0: none). */
+size_t kgw_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts);
+
+/*
+ * kgw_moe_route -- each token's experts and weights, the counts and the balance loss.
+ *
+ *   scores   (tokens, num_experts) of `dtype`, rows `ld` >= num_experts elements apart.  A score of -inf is an expert that
+ *            its token may not take: p = 0.
+ *   mask     uint8 (tokens,) or NULL: a token with 0 takes no expert (padding); its scores are not read.
+ *   ids      int32 (tokens, topk): the topk largest scores in descending order, equal ones by index (-0 equals
+ *            0).  Where fewer may be taken, -1.
+ *   given_ids  NULL, or the ids (tokens, topk) of a caller that selects by itself, id_bytes 4 (int32) or 8
+ *            (int64): ids then gets these, with -1 for those outside [0, num_experts), of a masked token or with a
+ *            score of -inf or NaN.
+ *   weights  fp32 (tokens, topk): scale * p (KGW_SCORE_SIGMOID: scale * u) of the chosen, or with renormalize 1 scale * u / sum of u
+ *            over the token's chosen (KGW_SCORE_SIGMOID: + 1e-20); 0 for id -1.
+ *   counts   int32 (num_experts,): assignments of every expert.
+ *   slope    fp32 (num_experts,): num_experts * counts / (topk * N^2), N the tokens that take part (those with an expert
+ *            that they may take); zeros for N = 0.
+ *   loss     fp32 (1,): sum over t, e of slope_e p_te -- 1 where the experts are used alike, num_experts / topk at
+ *            most.  Its gradient passes through p; slope is a constant (d loss / d p_te).
+ * A NaN score is never chosen and makes the loss NaN.  Sums are fp32 in a fixed order: deterministic.
+ * num_experts <= 2048, topk <= min(num_experts, 64), tokens <= 2^23.  tokens == 0 is valid.
+ */
+kgw_status_t kgw_moe_route(const void* scores, int64_t ld, int32_t dtype, const uint8_t* mask, const void* given_ids,
+                           int32_t id_bytes, int64_t tokens, int32_t num_experts, int32_t topk, int32_t score,
+                           int32_t renormalize, float scale, int32_t* ids, float* weights, int32_t* counts, float* loss,
+                           float* slope, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kgw_moe_route_grad -- dscores (tokens, num_experts) of `dtype`, contiguous: the gradient of
+ *     sum of dweights * weights + dloss * loss
+ * with respect to the scores, for the ids of kgw_moe_route (any (tokens, topk) ids: an expert named twice counts twice).
+ *   dweights fp32 (tokens, topk) or NULL (zeros); not read where the id is -1.
+ *   dloss    fp32 (1,) on the device, with slope (num_experts,); both or neither.  slope may be made of counts summed
+ *            over several ranks.
+ * Zero for a masked token and for a score of -inf.  fp32 arithmetic, rounded once.
+ */
+kgw_status_t kgw_moe_route_grad(const void* scores, int64_t ld, int32_t dtype, const uint8_t* mask, const void* ids,
+                                int32_t id_bytes, const float* dweights, const float* dloss, const float* slope,
+                                int64_t tokens, int32_t num_experts, int32_t topk, int32_t score, int32_t renormalize,
+                                float scale, void* dscores, void* stream);
+
+/* The activation between the two expert products. */
+typedef enum {
+    KGW_ACT_SWIGLU = 0,   /* h (rows, 2 inner) = [g | u]: y = g / (1 + exp(-g)) * u */
+    KGW_ACT_RELU2 = 1     /* h (rows, inner): y = max(h, 0)^2                       */
+} kgw_act_t;
+
+/*
+ * kgw_moe_act_fp8 -- y = act(h), and h kept in 8 bits for the backward pass.
+ *
+ *   h        (rows, 2 inner) or (rows, inner) of `dtype`, rows ld_h elements apart; inner a multiple of 8.
+ *   offsets  int32 (num_experts,) inclusive cumulative rows, or NULL: rows from the last offset on belong to no expert
+ *            and are neither read nor written.
+ *   y        (rows, inner), contiguous: `dtype`; with y_scales e4m3 bytes, 8-byte aligned.
+ *   y_scales uint8 (ceil(inner/128), rows) or NULL.
+ *   saved    NULL, or e4m3 bytes of h, contiguous, 8-byte aligned, with saved_scales: uint8 (ceil(inner/128), rows), for
+ *            KGW_ACT_SWIGLU (2 ceil(inner/128), rows), the blocks of g before those of u.
+ * Codes and scales as kgw_quantize_fp8 makes them with token_axis 1: the operand A of kgw_mgrouped_fp8 (inner a
+ * multiple of 128) and of kgw_wgrad_fp8_rows (inner a multiple of 16).  The values that are
+ * quantised are fp32 (1 / (1 + exp(-g)) is zero where it is below 2^-126).  A block holding a NaN or an infinity has scale 0xFF and NaN codes.
+ */
+kgw_status_t kgw_moe_act_fp8(const void* h, int64_t ld_h, int32_t dtype, int32_t act, const int32_t* offsets,
+                             int32_t num_experts, int64_t rows, int64_t inner, void* y, uint8_t* y_scales, void* saved,
+                             uint8_t* saved_scales, void* stream);
+
+/*
+ * kgw_moe_act_fp8_grad -- dh = act'(h) dy for the h that kgw_moe_act_fp8 kept, and (y not NULL) y = act(h) of
+ * that h, for the weight gradient of the second product.
+ *   dy       (rows, inner) of `dtype`, rows ld_dy elements apart.
+ *   dh       as h, contiguous: `dtype`; with dh_scales e4m3 bytes and scales laid out as saved and saved_scales.
+ *   y, y_scales  as for kgw_moe_act_fp8.
+ */
+kgw_status_t kgw_moe_act_fp8_grad(const void* dy, int64_t ld_dy, int32_t dtype, int32_t act, const void* saved,
+                                  const uint8_t* saved_scales, const int32_t* offsets, int32_t num_experts,
+                                  int64_t rows, int64_t inner, void* dh, uint8_t* dh_scales, void* y,
+                                  uint8_t* y_scales, void* stream);
 
 /*
  * kgw_newton_schulz -- orthogonalises a batch of matrices, the update that a weight gradient

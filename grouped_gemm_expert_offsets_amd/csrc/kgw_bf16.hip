@@ -261,7 +261,7 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
         const char* Bbase;
         if constexpr (A_8) {
             a_stride = H;
-            Abase = (const char*)p.A + (int64_t)begin * H + m0;
+            Abase = (const char*)p.A + (int64_t)begin * H + m0 - 16;
         } else if constexpr (A_TR) {
             a_stride = H;
             Abase = (const char*)p.A + ((int64_t)begin * H + m0) * 2;
@@ -276,13 +276,19 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
                                                : (n0 * T + begin)) * 2;
         } else {
             b_stride = N;
-            Bbase = (const char*)p.B + ((int64_t)begin * N + n0) * (B_8 ? 1 : 2);
+            Bbase = (const char*)p.B + ((int64_t)begin * N + n0) * (B_8 ? 1 : 2) - (B_8 ? 16 : 0);
         }
-        // 8-bit rows: load t (0..1) fills token rows 8*wave + 4*t + (lane>>4) with 16 codes a lane; the scales
-        // of the wave's 8 tokens are two dwords for each of the tile's two blocks of 128 (lane 2*block + dword).
+        // 8-bit rows: load t (0..1) fills token rows 8*wave + 4*t + (lane>>4) with 16 codes a lane.  The last piece is
+        // the row's last 16 codes, also where only 8 belong to it (rows are multiples of 8 codes, 16 at least, and the
+        // base lies 16 codes before the tile, since those 16 may begin there); they are then its upper half.  The scales of
+        // the wave's 8 tokens are two dwords for each of the tile's two blocks of 128 (lane 2*block + dword).
         auto raw_voff = [&](int t, int64_t stride, int valid) __attribute__((always_inline)) {
-            return (uint32_t)(8 * wave + 4 * t + (lane >> 4)) * (uint32_t)stride + (uint32_t)min(16 * (lane & 15), valid - 16);
+            return (uint32_t)(8 * wave + 4 * t + (lane >> 4)) * (uint32_t)stride + (uint32_t)(16 + min(16 * (lane & 15), valid - 16));
         };
+        auto raw_at = [&](int valid) __attribute__((always_inline)) {       // where a lane's 8 codes of a row are
+            return (uint32_t)(8 * (lane + ((valid & 8) && 8 * (lane & 31) == valid - 8 ? 1 : 0)));
+        };
+        const uint32_t a_raw_at = A_8 ? raw_at(rows_valid) : 0u, b_raw_at = B_8 ? raw_at(cols_valid) : 0u;
         auto sc_voff = [&](int valid) __attribute__((always_inline)) {
             return (uint32_t)min((lane >> 1) & 1, (valid - 1) >> 7) * (uint32_t)T + (uint32_t)(8 * wave + 4 * (lane & 1));
         };
@@ -463,7 +469,7 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
         };
         auto raw_read = [&](bool b, int x, int u, RawStep& w) __attribute__((always_inline)) {
             const uint32_t slot = (uint32_t)(x & 3) + (b ? 4u : 0u);
-            if (u < 4) w.q[u] = lds_load_8B(tiles + R::raw_ring + 2048 * wave, slot * RAW_STAGE + (uint32_t)(512 * u + 8 * lane));
+            if (u < 4) w.q[u] = lds_load_8B(tiles + R::raw_ring + 2048 * wave, slot * RAW_STAGE + 512u * u + (b ? b_raw_at : a_raw_at));
             else w.sc = lds_load_8B(tiles + R::sc_ring + 256 * wave, slot * SC_STAGE + (uint32_t)(8 * (cv_q >> 4)));
         };
         auto raw_convert = [&](bool b, int x, int u, const RawStep& w) __attribute__((always_inline)) {

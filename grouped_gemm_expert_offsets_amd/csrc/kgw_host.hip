@@ -158,7 +158,7 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
     const int64_t bm = fp8 ? kgw::kFp8BM : kgw::kBf16BM;
     const int64_t bn = fp8 ? kgw::kFp8BN : kgw::kBf16BN;
     const int64_t talign = fp4 ? KGW_FP4_TOKEN_ALIGN : (fp8 || rows ? KGW_FP8_TOKEN_ALIGN : KGW_BF16_TOKEN_ALIGN);
-    const int64_t nalign = (fp8 && !fp4) || (rows && sfb) ? 16 : 8;
+    const int64_t nalign = (fp8 && !fp4) ? 16 : 8;
     static_assert(KGW_OUT_FP32 == kgw::kOutF32 && KGW_OUT_BF16 == kgw::kOutBf16 && KGW_OUT_FP16 == kgw::kOutF16,
                   "output kind codes");
     static_assert(KGW_SCALES_U8 == kgw::kScalesU8 && KGW_SCALES_PACKED == kgw::kScalesPacked &&
@@ -176,7 +176,8 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
         return KGW_ERROR_MISALIGNED;
     if (rows) {
         if (tokens_sum > 0 && hidden > 0 && n > 0 && !sfa) return KGW_ERROR_INVALID_VALUE;
-        if (hidden % 16 != 0 || (((uintptr_t)sfa | (uintptr_t)sfb) & 3u)) return KGW_ERROR_MISALIGNED;
+        // 8-bit rows move in pieces of 16 codes, the last one from the row's end
+        if (hidden % 8 != 0 || hidden == 8 || (sfb && n == 8) || (((uintptr_t)sfa | (uintptr_t)sfb) & 3u)) return KGW_ERROR_MISALIGNED;
         // one step's 32 token rows are addressed with 32-bit offsets
         if (64 * hidden >= ((int64_t)1 << 31)) return KGW_ERROR_UNSUPPORTED;
     }

@@ -316,10 +316,10 @@ kgw_status_t kgw_wgrad_fp4(const void* A, const void* sfa, const void* B, const 
  *     out[e] (=|+=) a[begin:end, :]^T @ b[begin:end, :]
  *     a(t, m) = e4m3(A[t, m]) * 2^(sa[m/128, t] - 127)      b likewise, or the bf16 B itself
  *
- *   A    e4m3 bytes (tokens_sum, hidden), row-major, 16-byte aligned; hidden a multiple of 16 (KGW_ERROR_MISALIGNED)
- *        and below 2^25 (KGW_ERROR_UNSUPPORTED).
+ *   A    e4m3 bytes (tokens_sum, hidden), row-major, 16-byte aligned; hidden a multiple of 8, 16 at least
+ *        (KGW_ERROR_MISALIGNED), and below 2^25 (KGW_ERROR_UNSUPPORTED).
  *   sa   uint8 (ceil(hidden/128), tokens_sum), 4-byte aligned: the last block of a row may be shorter.
- *   B    sb NULL: bf16 (tokens_sum, n), n a multiple of 8.  Else e4m3 bytes (tokens_sum, n), n a multiple of 16, with
+ *   B    sb NULL: bf16 (tokens_sum, n), n a multiple of 8.  Else e4m3 bytes (tokens_sum, n), n a multiple of 8, 16 at least, with
  *        sb uint8 (ceil(n/128), tokens_sum).
  *   Every value is converted exactly to bf16 with its scale folded in (one that falls below bf16's smallest normal value
  *   becomes a subnormal or zero), products are summed in fp32 on the bf16 MFMA.  A scale byte of 0xFF makes the outputs that it reaches NaN.
@@ -710,7 +710,7 @@ typedef enum {
  *   saved    NULL, or e4m3 bytes of h, contiguous, 8-byte aligned, with saved_scales: uint8 (ceil(inner/128), rows), for
  *            KGW_ACT_SWIGLU (2 ceil(inner/128), rows), the blocks of g before those of u.
  * Codes and scales as kgw_quantize_fp8 makes them with token_axis 1: the operand A of kgw_mgrouped_fp8 (inner a
- * multiple of 128) and of kgw_wgrad_fp8_rows (inner a multiple of 16).  The values that are
+ * multiple of 128) and of kgw_wgrad_fp8_rows.  The values that are
  * quantised are fp32 (1 / (1 + exp(-g)) is zero where it is below 2^-126).  A block holding a NaN or an infinity has scale 0xFF and NaN codes.
  */
 kgw_status_t kgw_moe_act_fp8(const void* h, int64_t ld_h, int32_t dtype, int32_t act, const int32_t* offsets,

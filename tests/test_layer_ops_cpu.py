@@ -116,8 +116,8 @@ def test_weight_gradient_arguments(lib):
     for kw in (dict(A=None), dict(sa=None), dict(B=None), dict(off=None), dict(out=None), dict(ptrs=P), dict(E=0), dict(hidden=-1),
                dict(n=-1), dict(T=-1), dict(dt=3), dict(acc=2)):
         assert wgrad(lib, **kw) == INVALID, kw
-    for kw in (dict(A=P + 8), dict(B=P + 8), dict(out=P + 8), dict(sa=P + 2), dict(sb=P + 1), dict(off=P + 2), dict(hidden=120),
-               dict(n=60), dict(n=72, sb=P), dict(out=None, ptrs=P + 4)):
+    for kw in (dict(A=P + 8), dict(B=P + 8), dict(out=P + 8), dict(sa=P + 2), dict(sb=P + 1), dict(off=P + 2), dict(hidden=124),
+               dict(n=60), dict(n=68, sb=P), dict(hidden=8), dict(n=8, sb=P), dict(out=None, ptrs=P + 4)):
         assert wgrad(lib, **kw) == MISALIGNED, kw
     assert wgrad(lib, T=200) == OFFSETS
     for kw in (dict(E=65537), dict(hidden=2 ** 25), dict(n=2 ** 28), dict(T=2 ** 31)):
@@ -128,7 +128,7 @@ def test_weight_gradient_arguments(lib):
 @no_gpu
 def test_weight_gradient_reaches_the_device(lib):
     device = kgw.KGW_ERROR_DEVICE
-    assert wgrad(lib) == device and wgrad(lib, sb=P) == device and wgrad(lib, n=72, T=128) == device
+    assert wgrad(lib) == device and wgrad(lib, sb=P) == device and wgrad(lib, n=72, hidden=24, sb=P) == device and wgrad(lib, n=72, T=128) == device
     assert wgrad(lib, T=0, A=None, sa=None, B=None) == device            # zeros to write
 
 

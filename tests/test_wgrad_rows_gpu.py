@@ -15,7 +15,8 @@ pytestmark = [pytest.mark.gpu,
 DEV = "cuda"
 SIZES = [([256, 0, 512, 768], 256, 512), ([256, 0, 512, 768], 272, 400), ([512, 256], 16, 16), ([256], 128, 144), ([256] * 5, 1040, 784),
          ([2048] * 3 + [1024], 320, 384), ([4096, 0, 8192, 256], 320, 384), ([0, 0, 256], 144, 528),
-         ([1024 + 256 * (e % 5) for e in range(32)], 2048, 2048)]
+         ([1024 + 256 * (e % 5) for e in range(32)], 2048, 2048), ([256, 512], 24, 264), ([512, 256], 264, 776), ([256], 776, 24),
+         ([256, 256], 1048, 520)]
 
 
 def rows8(tokens, cols, seed):
@@ -154,8 +155,8 @@ def test_refusals():
     bad = [lambda: f(b, sa, b, off), lambda: f(A, sa, B, off), lambda: f(A, sa, b, off, sb=sb), lambda: f(A, None, b, off),
            lambda: f(A, sa.int(), b, off), lambda: f(A, sa[:, :255], b, off), lambda: f(A, sa.t(), b, off), lambda: f(A, sa.cpu(), b, off),
            lambda: f(A[:128], sa, b, off), lambda: f(A.t(), sa, b, off), lambda: f(A, sa, b, off.long()), lambda: f(A, sa, b, off.cpu()),
-           lambda: f(A[:200].contiguous(), sa[:, :200].contiguous(), b[:200].contiguous(), off), lambda: f(*odd(120), b, off),
-           lambda: f(A, sa, odd(120)[0], off, sb=odd(120)[1]), lambda: f(A, sa, b[:, :100].contiguous(), off),
+           lambda: f(A[:200].contiguous(), sa[:, :200].contiguous(), b[:200].contiguous(), off), lambda: f(*odd(124), b, off),
+           lambda: f(*odd(8), b, off), lambda: f(A, sa, odd(124)[0], off, sb=odd(124)[1]), lambda: f(A, sa, b[:, :100].contiguous(), off),
            lambda: f(A, sa, b, off, out_dtype=torch.float64), lambda: f(A, sa, b, off, accumulate=True),
            lambda: f(A, sa, b, off, out=torch.zeros((1, 128, 127), device=DEV)),
            lambda: f(A, sa, b, torch.tensor([100], dtype=torch.int32, device=DEV), validate=True)]

@@ -146,7 +146,7 @@ def load_library():
     lib.kgw_wgrad_fp8_rows.restype = ctypes.c_int
     lib.kgw_wgrad_fp8_rows.argtypes = [p, p, p, p, p, i32, i64, i64, i64, p, p, i32, i32, p, sz, p]
     lib.kgw_moe_route_workspace_bytes.restype = sz
-    lib.kgw_moe_route_workspace_bytes.argtypes = [i64, i32]
+    lib.kgw_moe_route_workspace_bytes.argtypes = [i64, i32, i32]
     lib.kgw_moe_route.restype = ctypes.c_int
     lib.kgw_moe_route.argtypes = [p, i64, i32, p, p, i32, i64, i32, i32, i32, i32, f32, p, p, p, p, p, p, sz, p]
     lib.kgw_moe_route_grad.restype = ctypes.c_int
@@ -218,14 +218,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else int(t.data_ptr())
 
 
+_OUT_CODES = {torch.float32: KGW_OUT_FP32, torch.bfloat16: KGW_OUT_BF16, torch.float16: KGW_OUT_FP16}
+
+
 def _out_code(dtype: torch.dtype) -> int:
-    if dtype == torch.float32:
-        return KGW_OUT_FP32
-    if dtype == torch.bfloat16:
-        return KGW_OUT_BF16
-    if dtype == torch.float16:
-        return KGW_OUT_FP16
-    raise ValueError(f"output dtype must be float32, bfloat16 or float16, got {dtype}")
+    code = _OUT_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"output dtype must be float32, bfloat16 or float16, got {dtype}")
+    return code
 
 
 def _prepare_out(out, E, hidden, n, out_dtype, accumulate, device, stream):
@@ -869,11 +869,12 @@ def kgw_moe_rows(tokens: int, topk: int, num_experts: int, alignment: int = FP8_
 
 def _on_gpu(t: torch.Tensor, what: str) -> torch.device:
     """The tensor's device: the current GPU, whose memory the kernels address."""
+    device = t.device
     if not t.is_cuda:
-        raise ValueError(f"{what} must be a GPU tensor, got one on {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+        raise ValueError(f"{what} must be a GPU tensor, got one on {device}")
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} is on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device
 
 
 def _launch_stream(stream, device: torch.device) -> int:
@@ -886,11 +887,14 @@ def _rows_2d(t: torch.Tensor, what: str) -> int:
     if t.dim() != 2:
         raise ValueError(f"{what} must be 2-D, got shape {tuple(t.shape)}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{what} needs contiguous rows (stride 1 along the last axis)")
-    if rows > 1 and t.stride(0) < cols:
+    if rows <= 1:
+        return cols
+    if ld < cols:
         raise ValueError(f"{what} has overlapping rows")
-    return max(t.stride(0), cols) if rows > 1 else cols
+    return ld
 
 
 def _routing(t: torch.Tensor, what: str, dim: int, device):
@@ -908,7 +912,7 @@ def _weights(t: torch.Tensor, row_of: torch.Tensor, what: str = "weights"):
 def _result(out: Optional[torch.Tensor], shape, dtype, device, what: str, stream) -> torch.Tensor:
     if out is None:
         return _empty(shape, dtype, device, stream)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+    if out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
     return out
 
@@ -1041,25 +1045,31 @@ _SCORES = {"softmax": KGW_SCORE_SOFTMAX, "sigmoid": KGW_SCORE_SIGMOID}
 
 
 def _route_args(scores: torch.Tensor, topk: int, mask, score: str):
-    """Checks what the router and its gradient share: (device, type code, row stride, score code)."""
+    """Checks what the router and its gradient share: (device, type code, row stride, score code, tokens, experts)."""
     code = _out_code(scores.dtype)
     ld = _rows_2d(scores, "scores")
     device = _on_gpu(scores, "scores")
     tokens, E = scores.shape
     if not 1 <= E <= _MOE_MAX_EXPERTS or not 1 <= topk <= min(E, _ROUTE_MAX_TOPK):
         raise ValueError(f"need 1 .. {_MOE_MAX_EXPERTS} experts and 1 .. min(experts, {_ROUTE_MAX_TOPK}) a token, got {E}, {topk}")
-    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (tokens,) or
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (tokens,) or
                              mask.device != device or not mask.is_contiguous()):
         raise ValueError(f"mask must be a contiguous bool ({tokens},) tensor on {device}")
-    if score not in _SCORES:
+    score_code = _SCORES.get(score)
+    if score_code is None:
         raise ValueError(f"score is 'softmax' or 'sigmoid', got {score!r}")
-    return device, code, ld, _SCORES[score]
+    return device, code, ld, score_code, tokens, E
 
 
 def _route_ids(ids: torch.Tensor, tokens: int, device):
     if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 2 or ids.shape[0] != tokens or \
             not ids.is_contiguous() or ids.device != device:
         raise ValueError(f"ids must be a contiguous int32 or int64 ({tokens}, topk) tensor on {device}")
+
+
+def _floats(t: torch.Tensor, shape, device, what: str):
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what} must be a contiguous float32 {shape} tensor on {device}")
 
 
 def kgw_moe_route(scores: torch.Tensor, topk: int, *, ids: Optional[torch.Tensor] = None,
@@ -1080,28 +1090,28 @@ def kgw_moe_route(scores: torch.Tensor, topk: int, *, ids: Optional[torch.Tensor
     ids and counts are views of one buffer, weights, loss and slope of another.
     """
     topk = int(topk)
-    device, code, ld, score_code = _route_args(scores, topk, mask, score)
-    tokens, E = scores.shape
+    device, code, ld, score_code, tokens, E = _route_args(scores, topk, mask, score)
     if ids is not None:
         _route_ids(ids, tokens, device)
         if ids.shape[1] != topk:
             raise ValueError(f"ids has {ids.shape[1]} experts a token, topk is {topk}")
     lib = load_library()
     n = tokens * topk
-    need = lib.kgw_moe_route_workspace_bytes(tokens, E)
+    need = lib.kgw_moe_route_workspace_bytes(tokens, E, ids is not None)
     whole = _empty(n + E, torch.int32, device, stream)
-    real = _empty(n + E + 1 + need // 4, torch.float32, device, stream)
+    real = _empty(need // 4 + n + E + 1, torch.float32, device, stream)
     if stream is not None:
         _used_on(stream, scores, mask, ids)
     at, at_real = whole.data_ptr(), real.data_ptr()
     st = lib.kgw_moe_route(scores.data_ptr(), ld, code, _ptr(mask), _ptr(ids), 0 if ids is None else ids.element_size(),
-                           tokens, E, topk, score_code, int(bool(renormalize)), scale, at, at_real, at + 4 * n,
-                           at_real + 4 * (n + E), at_real + 4 * n, at_real + 4 * (n + E + 1) if need else None, need,
+                           tokens, E, topk, score_code, int(bool(renormalize)), scale, at, at_real + need, at + 4 * n,
+                           at_real + need + 4 * (n + E), at_real + need + 4 * n, at_real, need,
                            _launch_stream(stream, device))
     _check(st, "kgw_moe_route")
-    chosen, counts = whole.split((n, E))
-    weights, slope, loss, _ = real.split((n, E, 1, need // 4))
-    return chosen.view(tokens, topk), weights.view(tokens, topk), counts, loss.view(()), slope
+    # (as_strided: a split and a view of each part take twice the time, and a call's issue outlasts a short batch)
+    first = need // 4
+    return (whole.as_strided((tokens, topk), (topk, 1)), real.as_strided((tokens, topk), (topk, 1), first),
+            whole.as_strided((E,), (1,), n), real.as_strided((), (), first + n + E), real.as_strided((E,), (1,), first + n))
 
 
 def kgw_moe_route_grad(scores: torch.Tensor, ids: torch.Tensor, dweights: Optional[torch.Tensor], *,
@@ -1117,17 +1127,16 @@ def kgw_moe_route_grad(scores: torch.Tensor, ids: torch.Tensor, dweights: Option
     if ids.dim() != 2:
         raise ValueError(f"ids must be (tokens, topk), got {tuple(ids.shape)}")
     topk = ids.shape[1]
-    device, code, ld, score_code = _route_args(scores, topk, mask, score)
-    tokens, E = scores.shape
+    device, code, ld, score_code, tokens, E = _route_args(scores, topk, mask, score)
     _route_ids(ids, tokens, device)
     if (dloss is None) != (slope is None):
         raise ValueError("pass dloss and slope, or neither")
-    for t, shape, what in ((dweights, (tokens, topk), "dweights"), (slope, (E,), "slope")):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or
-                              t.device != device):
-            raise ValueError(f"{what} must be a contiguous float32 {shape} tensor on {device}")
-    if dloss is not None and (dloss.dtype != torch.float32 or dloss.numel() != 1 or dloss.device != device):
-        raise ValueError(f"dloss must be a float32 tensor of one value on {device}")
+    if dweights is not None:
+        _floats(dweights, (tokens, topk), device, "dweights")
+    if dloss is not None:
+        _floats(slope, (E,), device, "slope")
+        if dloss.dtype != torch.float32 or dloss.numel() != 1 or dloss.device != device:
+            raise ValueError(f"dloss must be a float32 tensor of one value on {device}")
     out = _result(out, (tokens, E), scores.dtype, device, "out", stream)
     if stream is not None:
         _used_on(stream, scores, ids, dweights, dloss, slope, mask, out)

@@ -197,9 +197,9 @@ kgw_status_t kgw_moe_unpermute_grad(const void* dout, int64_t ld_dout, const voi
     return run_rows(p, kgw::kMoeUnpermuteGrad, dtype, stream);
 }
 
-size_t kgw_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts) {
+size_t kgw_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts, int32_t given) {
     if (tokens < 0 || tokens > kMaxRowTokens || num_experts < 1 || num_experts > kgw::kMoeMaxExperts) return 0;
-    return kgw::route_plan(tokens, num_experts).words * sizeof(int32_t);
+    return kgw::route_plan(tokens, num_experts, given != 0).words * sizeof(int32_t);
 }
 
 kgw_status_t kgw_moe_route(const void* scores, int64_t ld, int32_t dtype, const uint8_t* mask, const void* given_ids,
@@ -212,10 +212,10 @@ kgw_status_t kgw_moe_route(const void* scores, int64_t ld, int32_t dtype, const 
     if (!counts || !loss || !slope || (tokens > 0 && (!scores || !ids || !weights || ld < num_experts)))
         return KGW_ERROR_INVALID_VALUE;
     if (!rows_aligned(scores, dtype) || !aligned_to(ids, 4) || !aligned_to(weights, 4) || !aligned_to(counts, 4) ||
-        !aligned_to(loss, 4) || !aligned_to(slope, 4) || !aligned_to(workspace, 4) ||
+        !aligned_to(loss, 4) || !aligned_to(slope, 4) || !aligned_to(workspace, 8) ||
         (given_ids && !aligned_to(given_ids, (uintptr_t)id_bytes)))
         return KGW_ERROR_MISALIGNED;
-    const kgw::RoutePlan plan = kgw::route_plan(tokens, num_experts);
+    const kgw::RoutePlan plan = kgw::route_plan(tokens, num_experts, given_ids != nullptr);
     if (plan.words && (!workspace || workspace_bytes < plan.words * sizeof(int32_t))) return KGW_ERROR_INVALID_VALUE;
     st = usable_device();
     if (st != KGW_SUCCESS) return st;
@@ -235,15 +235,15 @@ kgw_status_t kgw_moe_route(const void* scores, int64_t ld, int32_t dtype, const 
     p.id_bytes = id_bytes;
     p.renormalize = renormalize;
     p.scale = scale;
+    p.sigmoid = score == KGW_SCORE_SIGMOID;
     p.groups = plan.groups;
     if (plan.words) {
-        p.part = (float*)workspace;
-        p.tokens_part = p.part + (size_t)plan.groups * 2 * num_experts;
-        p.dots = p.tokens_part + plan.groups;
+        p.part = (kgw::RoutePart*)workspace;
+        p.tokens_part = (int32_t*)(p.part + (size_t)plan.groups * num_experts);
+        p.dots = (float*)(p.tokens_part + plan.groups);
         p.arrived = (int32_t*)(p.dots + plan.finish);
     }
-    return kgw::launch_route(p, dtype, score == KGW_SCORE_SIGMOID, (hipStream_t)stream) == hipSuccess ? KGW_SUCCESS
-                                                                                                  : KGW_ERROR_DEVICE;
+    return kgw::launch_route(p, dtype, (hipStream_t)stream) == hipSuccess ? KGW_SUCCESS : KGW_ERROR_DEVICE;
 }
 
 kgw_status_t kgw_moe_route_grad(const void* scores, int64_t ld, int32_t dtype, const uint8_t* mask, const void* ids,

@@ -61,8 +61,9 @@ hipError_t launch_moe_rows(const MoeRowsParams& p, int op, int dtype, hipStream_
 // the router (kgw_route.hip)
 // ----------------------------------------------------------------------------
 constexpr int kRouteMaxTopk = 64;
-constexpr int kRouteThreads = 256;      // of a workgroup of several
-constexpr int kRouteGroups = 1024;      // workgroups of a call, at most
+constexpr int kRouteGroups = 256;       // workgroups of 1024 threads, at most (of 256: four times as many)
+
+typedef float RoutePart __attribute__((ext_vector_type(2)));     // a workgroup's sum of an expert's shares, and its count
 
 struct RouteParams {
     const void* scores;     // (tokens, experts)
@@ -76,10 +77,10 @@ struct RouteParams {
     const float* dweights;  // gradient only, from here on: (tokens, topk) or NULL
     const float* dloss;     // (1,) or NULL
     void* dscores;          // (tokens, experts), contiguous
-    // workspace, with more than one workgroup: every workgroup's sums and counts (2 experts words), its tokens, the
+    // workspace, with more than one workgroup: every workgroup's parts (groups, experts), its tokens, the
     // finishing workgroups' parts of the loss and their counter
-    float* part;
-    float* tokens_part;
+    RoutePart* part;
+    int32_t* tokens_part;
     float* dots;
     int32_t* arrived;
     int64_t ld;             // of scores, in elements
@@ -88,18 +89,19 @@ struct RouteParams {
     int32_t topk;
     int32_t id_bytes;
     int32_t renormalize;
+    int32_t sigmoid;        // (the gradient's kernels are told apart by it)
     int32_t groups;
     float scale;
 };
 
 struct RoutePlan {
-    int rows;               // tokens that a workgroup of several takes at a time
+    int threads;            // of a workgroup
     int groups;             // workgroups (1: no workspace)
     int finish;             // workgroups that add the others' parts
     size_t words;           // of workspace
 };
-RoutePlan route_plan(int64_t tokens, int experts);
-hipError_t launch_route(const RouteParams& p, int dtype, bool sigmoid, hipStream_t stream);
+RoutePlan route_plan(int64_t tokens, int experts, bool given);
+hipError_t launch_route(const RouteParams& p, int dtype, hipStream_t stream);
 hipError_t launch_route_grad(const RouteParams& p, int dtype, bool sigmoid, hipStream_t stream);
 
 // ----------------------------------------------------------------------------

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kgw_device.h"
+#include "kgw_quant_device.h"
 
 namespace kgw {
 
@@ -53,24 +54,24 @@ __device__ __forceinline__ void store4(char* p, const float (&f)[4]) {
     }
 }
 
-// Swaps within quads (lanes xor 1, xor 2), then the half-row mirror (i <-> 7 - i of each 8) and the row mirror (i <-> 15 - i):
-// after each step every lane holds the combination over its group so far, in an order that is the same for all of its
-// lanes up to commuting, so every lane ends with the same bits.  Groups of 64 go on through the LDS crossbar.
+// Combines a value over the L lanes that share a row: swaps within quads, then the half-row mirror and the row mirror (as in
+// kgw_quant_device.h).  After each step every lane holds the combination over its group so far, in an order that is the
+// same for all of its lanes up to commuting, so every lane ends with the same bits.  Groups of 64 go on through the
+// LDS crossbar.
+// (bound_ctrl lets the compiler make the move part of the instruction that takes its result; no lane is out of bounds)
+template <int CTRL>
+__device__ __forceinline__ int lane_dpp(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true); }
 template <int CTRL>
 __device__ __forceinline__ float lane_dpp(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
-}
-template <int CTRL>
-__device__ __forceinline__ int lane_dpp(int v) {
-    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(float, lane_dpp<CTRL>(__builtin_bit_cast(int, v)));
 }
 template <int L, class T, class F>
 __device__ __forceinline__ T over_lanes(T v, F f) {
     static_assert(L == 4 || L == 8 || L == 16 || L == 64, "lanes of a row");
-    v = f(v, lane_dpp<0xB1>(v));
-    v = f(v, lane_dpp<0x4E>(v));
-    if constexpr (L >= 8) v = f(v, lane_dpp<0x141>(v));
-    if constexpr (L >= 16) v = f(v, lane_dpp<0x140>(v));
+    v = f(v, lane_dpp<kDppXor1>(v));
+    v = f(v, lane_dpp<kDppXor2>(v));
+    if constexpr (L >= 8) v = f(v, lane_dpp<kDppHalfMirror>(v));
+    if constexpr (L >= 16) v = f(v, lane_dpp<kDppMirror>(v));
     if constexpr (L == 64) {
         v = f(v, __shfl_xor(v, 16));
         v = f(v, __shfl_xor(v, 32));
@@ -84,6 +85,14 @@ __device__ __forceinline__ float lanes_max(float v) {
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
     return over_lanes<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ int lanes_sum(int v) {
+    return over_lanes<L>(v, [](int a, int b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ int lanes_max(int v) {
+    return over_lanes<L>(v, [](int a, int b) { return max(a, b); });
 }
 template <int L>
 __device__ __forceinline__ int lanes_min(int v) {

@@ -650,8 +650,8 @@ typedef enum {
     KGW_SCORE_SIGMOID = 1    /* u = 1 / (1 + exp(-score)), p = u / (sum u + 1e-20)                    */
 } kgw_score_t;
 
-/* Device scratch of kgw_moe_route, 4-byte aligned, no initial contents (0: none). */
-size_t kgw_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts);
+/* Device scratch of kgw_moe_route, 8-byte aligned, no initial contents (0: none); given 1: with given_ids. */
+size_t kgw_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts, int32_t given);
 
 /*
  * kgw_moe_route -- each token's experts and weights, the counts and the balance loss.

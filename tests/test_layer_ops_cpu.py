@@ -44,10 +44,10 @@ def test_router_pointers(lib):
         assert route(lib, **{name: None}) == INVALID, name
         assert route(lib, **{name: P + 2}) == MISALIGNED, name
     assert route(lib, given=P, id_bytes=2) == INVALID and route(lib, given=P + 4, id_bytes=8) == MISALIGNED
-    need = lib.kgw_moe_route_workspace_bytes(4096, 16)
+    need = lib.kgw_moe_route_workspace_bytes(4096, 16, 0)
     assert need > 0
     assert route(lib, tokens=4096) == INVALID and route(lib, tokens=4096, ws=P, ws_bytes=need - 1) == INVALID
-    assert route(lib, tokens=4096, ws=P + 2, ws_bytes=need) == MISALIGNED
+    assert route(lib, tokens=4096, ws=P + 4, ws_bytes=need) == MISALIGNED
     assert route_grad(lib, out=None) == INVALID and route_grad(lib, out=P + 1) == MISALIGNED
     assert route_grad(lib, dloss=None) == INVALID and route_grad(lib, slope=None) == INVALID
     assert route_grad(lib, id_bytes=3) == INVALID and route_grad(lib, id_bytes=8, ids=P + 4) == MISALIGNED
@@ -58,15 +58,15 @@ def test_router_pointers(lib):
 
 def test_router_workspace(lib):
     f = lib.kgw_moe_route_workspace_bytes
-    assert f(64, 256) == 0 and f(0, 8) == 0                     # one workgroup, one launch
-    assert f(-1, 8) == 0 and f(8, 0) == 0 and f(8, 2049) == 0 and f(2 ** 23 + 1, 8) == 0
-    assert f(2 ** 23, 256) == f(10 ** 6, 256) > 0               # never more workgroups
+    assert f(64, 256, 0) == 0 and f(0, 8, 0) == f(0, 8, 1) == 0        # one workgroup, one launch
+    assert f(-1, 8, 0) == 0 and f(8, 0, 0) == 0 and f(8, 2049, 1) == 0 and f(2 ** 23 + 1, 8, 0) == 0
+    assert f(2 ** 23, 256, 0) == f(10 ** 6, 256, 0) > 0               # never more workgroups
 
 
 @no_gpu
 def test_router_reaches_the_device(lib):
     device = kgw.KGW_ERROR_DEVICE
-    need = lib.kgw_moe_route_workspace_bytes(2 ** 23, 2048)
+    need = lib.kgw_moe_route_workspace_bytes(2 ** 23, 2048, 0)
     assert route(lib) == device and route(lib, tokens=2 ** 23, E=2048, ld=2048, k=64, ws=P, ws_bytes=need) == device
     assert route(lib, tokens=0, scores=None, ids=None, weights=None) == device
     assert route_grad(lib) == device and route_grad(lib, dw=None, dloss=None, slope=None) == device

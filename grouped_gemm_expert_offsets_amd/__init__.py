@@ -79,7 +79,7 @@ EXPORTED_SYMBOLS = ("kgw_wgrad_bf16", "kgw_wgrad_bf16_noalloc", "kgw_wgrad_bf16_
                     "kgw_mfma_ceiling", "kgw_status_string", "kgw_device_info", "kgw_moe_rows",
                     "kgw_moe_sort_workspace_bytes", "kgw_moe_sort", "kgw_moe_permute", "kgw_moe_unpermute",
                     "kgw_moe_unpermute_grad", "kgw_newton_schulz", "kgw_newton_schulz_workspace_bytes", "kgw_wgrad_fp8_rows",
-                    "kgw_moe_route_workspace_bytes", "kgw_moe_route", "kgw_moe_route_grad", "kgw_moe_act_fp8",
+                    "kgw_wgrad_fp8_rows_workspace_bytes", "kgw_moe_route_workspace_bytes", "kgw_moe_route", "kgw_moe_route_grad", "kgw_moe_act_fp8",
                     "kgw_moe_act_fp8_grad")
 
 
@@ -145,6 +145,8 @@ def load_library():
     f32 = ctypes.c_float
     lib.kgw_wgrad_fp8_rows.restype = ctypes.c_int
     lib.kgw_wgrad_fp8_rows.argtypes = [p, p, p, p, p, i32, i64, i64, i64, p, p, i32, i32, p, sz, p]
+    lib.kgw_wgrad_fp8_rows_workspace_bytes.restype = sz
+    lib.kgw_wgrad_fp8_rows_workspace_bytes.argtypes = [i32, i64, i64, i64]
     lib.kgw_moe_route_workspace_bytes.restype = sz
     lib.kgw_moe_route_workspace_bytes.argtypes = [i64, i32, i32]
     lib.kgw_moe_route.restype = ctypes.c_int
@@ -574,9 +576,12 @@ def kgw_wgrad_fp8_rows(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, offse
     out, outs, ptrs, code = _outputs(out, outs, E, hidden, n, out_dtype, accumulate, device, stream)
     if validate:
         kgw_validate_offsets(offsets, T, FP8_TOKEN_ALIGN, stream=stream)
-    ws, ws_bytes = _workspace(E, hidden, n, T, False, device, stream, split_k)
-    _used_on(stream, A, sa, B, sb, offsets, out, *(outs or ()))
-    st = load_library().kgw_wgrad_fp8_rows(_ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(offsets), E, hidden, n, T, _ptr(out),
+    lib = load_library()
+    ws_bytes = lib.kgw_wgrad_fp8_rows_workspace_bytes(E, hidden, n, T) if split_k else 0
+    ws = _empty(ws_bytes, torch.uint8, device, stream) if ws_bytes else None
+    if stream is not None:
+        _used_on(stream, A, sa, B, sb, offsets, out, *(outs or ()))
+    st = lib.kgw_wgrad_fp8_rows(_ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(offsets), E, hidden, n, T, _ptr(out),
                                            _ptr(ptrs), code, int(bool(accumulate)), _ptr(ws), ws_bytes,
                                            _stream_ptr(stream))
     _check(st, "kgw_wgrad_fp8_rows")

@@ -38,15 +38,7 @@
 //   A TR + B TC:  the default with the operands' roles swapped;
 //   A TC + B TC:  A 3 two-step slots, B 2 two-step slots; odd steps issue a
 //                 whole B stage (two steps ahead) and half an A stage, even
-//                 steps the other half of an A stage;
-//   A R8 + B TR, A R8 + B R8:  token rows of e4m3 codes with a scale for every 128
-//                 columns of a token (a scale that changes along the contracted axis,
-//                 so neither MFMA scales nor a conversion of whole fragments can take
-//                 it).  Step s loads the codes and scales of step s+5 into a ring of four
-//                 steps (10 of 18 KiB go to LDS as they would in bf16), and each wave
-//                 turns its own 8 token rows of step s+2 into bf16 in a ring of two TR
-//                 stages, between the first MFMAs of step s; only its own loads have to
-//                 have landed for that, and the barrier of step s+1 publishes it.
+//                 steps the other half of an A stage.
 // One barrier per step publishes step s+1 and frees what step s read; the 16
 // block reads of step s+1 follow MFMAs 16..31 of step s, one per MFMA (this
 // spacing measured 4% faster than two reads per MFMA for the first eight).  Steps
@@ -61,6 +53,7 @@
 
 #include "kgw_device.h"
 #include "kgw_internal.h"
+#include "kgw_schedule.h"
 #include "kgw_tile_io.h"
 
 namespace kgw {
@@ -71,31 +64,25 @@ constexpr int NT = 256;
 constexpr int TC_STAGE = 256 * 2 * BK * 2;  // 32 KiB: 256 rows x 128 B (two K steps)
 constexpr int TR_STAGE = BK * 256 * 2;      // 16 KiB: 32 token rows x 512 B (one K step)
 
-enum Pair { kTRTR = 0, kTRTC = 1, kTCTC = 2, kTCTR = 3, kR8TR = 4, kR8R8 = 5 };
-constexpr int RAW_STAGE = BK * 256;         // 8 KiB: 32 token rows x 256 codes (one K step)
-constexpr int SC_STAGE = 4 * 256;           // scales of a K step: 64 dwords a wave, the first four used
+enum Pair { kTRTR = 0, kTRTC = 1, kTCTC = 2, kTCTR = 3 };
 
 template <int PAIR>
 struct Rings {
-    static constexpr bool a_8 = PAIR == kR8TR || PAIR == kR8R8;
-    static constexpr bool b_8 = PAIR == kR8R8;
-    static constexpr bool a_tr = PAIR == kTRTR || PAIR == kTRTC || a_8;
+    static constexpr bool a_tr = PAIR == kTRTR || PAIR == kTRTC;
     static constexpr bool b_tc = PAIR == kTRTC || PAIR == kTCTC;
-    static constexpr int na = a_8 ? 2 : (PAIR == kTRTR || PAIR == kTRTC ? 4 : 3);
-    static constexpr int nb = b_8 ? 2 : (PAIR == kTRTC ? 3 : (PAIR == kTCTC ? 2 : 4));
+    static constexpr int na = PAIR == kTRTR ? 4 : (PAIR == kTRTC ? 4 : 3);
+    static constexpr int nb = PAIR == kTRTR ? 4 : (PAIR == kTRTC ? 3 : (PAIR == kTCTC ? 2 : 4));
     static constexpr int a_stage = a_tr ? TR_STAGE : TC_STAGE;
     static constexpr int b_stage = b_tc ? TC_STAGE : TR_STAGE;
     static constexpr int b_ring = na * a_stage;
-    static constexpr int raw_ring = b_ring + nb * b_stage;               // 8-bit operands: four steps of codes each
-    static constexpr int sc_ring = raw_ring + ((a_8 ? 4 : 0) + (b_8 ? 4 : 0)) * RAW_STAGE;
-    static constexpr int total = sc_ring + ((a_8 ? 4 : 0) + (b_8 ? 4 : 0)) * SC_STAGE;
+    static constexpr int total = b_ring + nb * b_stage;
     static_assert(total <= 160 * 1024, "LDS budget");
 };
 
 template <int OUT, int PAIR>
 __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
     using R = Rings<PAIR>;
-    constexpr bool A_TR = R::a_tr, B_TC = R::b_tc, A_8 = R::a_8, B_8 = R::b_8;
+    constexpr bool A_TR = R::a_tr, B_TC = R::b_tc;
     constexpr int NA = R::na, NB = R::nb;
     __shared__ __attribute__((aligned(1024))) char smem[R::total];
     lds_char* tiles = (lds_char*)smem;
@@ -138,113 +125,31 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
     }
 
     const int TT = p.tiles_m * p.tiles_n;
-    const int G = gridDim.x;
-    const int slot = xcd_slot(blockIdx.x, G, p.num_xcds);
-
-    // Static schedule: round r covers items [r*G, (r+1)*G); with p.snake the slots of odd
-    // rounds run in reverse, so a workgroup alternates between the front and the back of
-    // consecutive rounds (each XCD still holds a contiguous run of 32 items).
-    //
-    // Dynamic schedule (p.sched): the same runs of G/nq items per round form nq queues, one
-    // per XCD (queue q: the q-th run of every round), claimed one item at a time through
-    // the queue's counter; a workgroup drains the queue of its XCD (block id mod nq, the
-    // hardware's round-robin placement), then those of the next ones, so every claimed
-    // index is unique and every workgroup stops after at most nq empty claims.  Experts
-    // run longest first: lane k of every wave holds the expert of rank k (ties by index),
-    // so the last items to be claimed are the shortest.  Thread 0 claims the next item
-    // while the current one writes its output, and passes it on through LDS word 0 (the
-    // rings are idle between items) between two barriers.
-    const bool dyn = p.sched != nullptr;
-    int perm = lane;
-    if (dyn) {
-        const int E = p.num_experts;                        // <= kSchedMaxExperts
-        int cnt = -1;
-        if (lane < E) {
-            const int64_t b0 = lane ? (int64_t)p.offsets[lane - 1] : 0, e0 = p.offsets[lane];
-            const int64_t b1 = b0 < 0 ? 0 : (b0 > T ? T : b0);
-            const int64_t e1 = e0 < 0 ? 0 : (e0 > T ? T : e0);
-            cnt = (int)(e1 > b1 ? e1 - b1 : 0);
-        }
-        int rank = lane;
-        if (lane < E) {
-            rank = 0;
-            for (int j = 0; j < E; ++j) {
-                const int cj = __builtin_amdgcn_readlane(cnt, j);
-                rank += (cj > cnt || (cj == cnt && j < lane)) ? 1 : 0;
-            }
-        }
-        perm = __builtin_amdgcn_ds_permute(rank << 2, lane);
-    }
-    const int nq = p.num_xcds, qrun = G / p.num_xcds;
-    int q = (int)(blockIdx.x % (unsigned)nq), left = nq;    // thread 0's queue state
-    int r = 0;                                              // static: next round
-    // thread 0: the item of raw claim `idx` in queue q; an exhausted queue sends it on to
-    // the next one (claiming there), -1 once every queue is exhausted
-    auto resolve = [&](int idx) -> int {
-        for (;;) {
-            const int it = (idx / qrun) * G + q * qrun + idx % qrun;
-            if (it < p.num_items) return it;
-            if (--left == 0) return -1;
-            q = q + 1 == nq ? 0 : q + 1;
-            idx = atomicAdd(p.sched + q, 1);
-        }
-    };
-    auto broadcast = [&](int v) -> int {
-        if (tid == 0) *(__attribute__((address_space(3))) int*)tiles = v;
-        barrier_no_fence();
-        v = *(__attribute__((address_space(3))) int*)tiles;
-        barrier_no_fence();
-        return __builtin_amdgcn_readfirstlane(v);
-    };
-    auto next_static = [&]() -> int {
-        while (r * G < p.num_items) {
-            const int it = r * G + ((r & 1) && p.snake ? G - 1 - slot : slot);
-            ++r;
-            if (it < p.num_items) return it;
-        }
-        return -1;
-    };
-    int pend = 0;                                           // thread 0: raw claim of the next item
-    auto claim_next = [&]() {
-        if (dyn && tid == 0) pend = atomicAdd(p.sched + q, 1);
-    };
-    auto next_item = [&]() -> int {
-        if (!dyn) return next_static();
-        return broadcast(tid == 0 ? resolve(pend) : 0);
-    };
-    if (dyn && tid == 0) pend = atomicAdd(p.sched + q, 1);
-    for (int item = next_item(); item >= 0; item = next_item()) {
+    Schedule sched(p, tiles, tid);
+    for (int item = sched.next(); item >= 0; item = sched.next()) {
         const int ec = item / TT;
         const int local = item - ec * TT;
-        const int e = dyn ? __builtin_amdgcn_readlane(perm, ec) : ec / p.split;   // dynamic: split is 1
-        const int c = ec - (dyn ? ec : e * p.split);
+        const int e = sched.expert(ec);
+        const int c = ec - (sched.dyn ? ec : e * p.split);
         const int eo = c * p.num_experts + e;
         if (p.out_ptrs && !p.out_ptrs[eo]) {
-            claim_next();
+            sched.claim_next();
             continue;
         }
         int tm, tn;
         tile_coords(local, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
         const int64_t m0 = (int64_t)tm * BM;
         const int64_t n0 = (int64_t)tn * BN;
-        const int64_t raw_begin = e ? (int64_t)p.offsets[e - 1] : 0;
-        const int64_t raw_end = p.offsets[e];
-        const int32_t ebegin = (int32_t)(raw_begin < 0 ? 0 : (raw_begin > T ? T : raw_begin));
-        const int32_t eend = max(ebegin, (int32_t)(raw_end < 0 ? 0 : (raw_end > T ? T : raw_end)));
-        int32_t begin = ebegin, end = eend;
-        if (p.split > 1) {
-            const int32_t len = ((end - begin + p.split - 1) / p.split + kSplitUnit - 1) & ~(kSplitUnit - 1);
-            const int32_t cb = (int32_t)min<int64_t>(end, (int64_t)begin + (int64_t)c * len);
-            end = (int32_t)min<int64_t>(end, (int64_t)cb + len);
-            begin = cb;
-        }
+        const TokenRange range = token_range(p, e, c);
+        const int32_t ebegin = range.ebegin, eend = range.eend, end = range.end;
+        int32_t begin = range.begin;
         // Whole 64-token units; ragged blocks are counted from their own start, so
         // the loads stay inside the expert's block even for malformed offsets.
         if (ragged) begin = ebegin + ((begin - ebegin) & ~(2 * BK - 1));
         else begin &= ~(2 * BK - 1);
         const int ksteps = ((end - begin) / (2 * BK)) * 2;
         if (ksteps == 0) {
-            claim_next();
+            sched.claim_next();
             if (!p.accumulate) zero_slab_part<OUT, NT>(p, eo, local, TT, tid);
             continue;
         }
@@ -259,10 +164,7 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
         int64_t a_stride, b_stride;
         const char* Abase;
         const char* Bbase;
-        if constexpr (A_8) {
-            a_stride = H;
-            Abase = (const char*)p.A + (int64_t)begin * H + m0 - 16;
-        } else if constexpr (A_TR) {
+        if constexpr (A_TR) {
             a_stride = H;
             Abase = (const char*)p.A + ((int64_t)begin * H + m0) * 2;
         } else {
@@ -276,33 +178,14 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
                                                : (n0 * T + begin)) * 2;
         } else {
             b_stride = N;
-            Bbase = (const char*)p.B + ((int64_t)begin * N + n0) * (B_8 ? 1 : 2) - (B_8 ? 16 : 0);
+            Bbase = (const char*)p.B + ((int64_t)begin * N + n0) * 2;
         }
-        // 8-bit rows: load t (0..1) fills token rows 8*wave + 4*t + (lane>>4) with 16 codes a lane.  The last piece is
-        // the row's last 16 codes, also where only 8 belong to it (rows are multiples of 8 codes, 16 at least, and the
-        // base lies 16 codes before the tile, since those 16 may begin there); they are then its upper half.  The scales of
-        // the wave's 8 tokens are two dwords for each of the tile's two blocks of 128 (lane 2*block + dword).
-        auto raw_voff = [&](int t, int64_t stride, int valid) __attribute__((always_inline)) {
-            return (uint32_t)(8 * wave + 4 * t + (lane >> 4)) * (uint32_t)stride + (uint32_t)(16 + min(16 * (lane & 15), valid - 16));
-        };
-        auto raw_at = [&](int valid) __attribute__((always_inline)) {       // where a lane's 8 codes of a row are
-            return (uint32_t)(8 * (lane + ((valid & 8) && 8 * (lane & 31) == valid - 8 ? 1 : 0)));
-        };
-        const uint32_t a_raw_at = A_8 ? raw_at(rows_valid) : 0u, b_raw_at = B_8 ? raw_at(cols_valid) : 0u;
-        auto sc_voff = [&](int valid) __attribute__((always_inline)) {
-            return (uint32_t)min((lane >> 1) & 1, (valid - 1) >> 7) * (uint32_t)T + (uint32_t)(8 * wave + 4 * (lane & 1));
-        };
-        const uint32_t a_sc_voff = A_8 ? sc_voff(rows_valid) : 0u, b_sc_voff = B_8 ? sc_voff(cols_valid) : 0u;
-        const uint8_t* const a_sc = A_8 ? p.sfa + (m0 >> 7) * T + begin : nullptr;
-        const uint8_t* const b_sc = B_8 ? p.sfb + (n0 >> 7) * T + begin : nullptr;
         // Per-lane byte offsets inside a stage (rows past the valid extent are
         // clamped onto the last valid one: they only feed outputs never stored).
         uint32_t a_voff[8], b_voff[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            if constexpr (A_8) {
-                if (t < 2) a_voff[t] = raw_voff(t, a_stride, rows_valid);
-            } else if constexpr (A_TR) {
+            if constexpr (A_TR) {
                 if (t < 4) {
                     const int krow = 8 * wave + 2 * t + (lane >> 5);
                     a_voff[t] = (uint32_t)krow * (uint32_t)(a_stride * 2) +
@@ -312,9 +195,7 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
                 const int row = min(64 * wave + 8 * t + (lane >> 3), rows_valid - 1);
                 a_voff[t] = (uint32_t)row * (uint32_t)(a_stride * 2) + (uint32_t)c_q[t] * 16u;
             }
-            if constexpr (B_8) {
-                if (t < 2) b_voff[t] = raw_voff(t, b_stride, cols_valid);
-            } else if constexpr (B_TC) {
+            if constexpr (B_TC) {
                 const int row = min(64 * wave + 8 * t + (lane >> 3), cols_valid - 1);
                 b_voff[t] = (uint32_t)row * (uint32_t)(b_stride * 2) + (uint32_t)c_q[t] * 16u;
             } else {
@@ -342,31 +223,11 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
             const bool live = B_TC ? 2 * x < ksteps : x < ksteps;
             dma_16B(rsrc_words(Bbase + (int64_t)x * step_bytes, live ? 0xFFFFFFFFu : 0u), b_voff[t], dst);
         };
-        // Load d (0..2) of step x of an 8-bit operand: its codes and its scales, into the wave's own rows of the rings.
-        auto dma_raw = [&](bool b, int x, int d) __attribute__((always_inline)) {
-            const uint32_t num = x < ksteps ? 0xFFFFFFFFu : 0u;
-            const uint32_t slot = (uint32_t)(x & 3) + (b ? 4u : 0u);
-            if (d < 2)
-                dma_16B(rsrc_words((b ? Bbase + (int64_t)x * BK * b_stride : Abase + (int64_t)x * BK * a_stride), num),
-                        b ? b_voff[d] : a_voff[d],
-                        tiles_addr + (uint32_t)(R::raw_ring + 2048 * wave + 1024 * d) + slot * RAW_STAGE);
-            else
-                dma_4B(rsrc_words((b ? b_sc : a_sc) + (int64_t)x * BK, num), b ? b_sc_voff : a_sc_voff,
-                       tiles_addr + (uint32_t)(R::sc_ring + 256 * wave) + slot * SC_STAGE);
-        };
         // Loads of step s (also the prologue's virtual steps s < 0), in issue order.
-        constexpr int LOADS_ODD = PAIR == kTCTC ? 12 : (PAIR == kR8TR ? 7 : (PAIR == kR8R8 ? 6 : 8));
-        constexpr int LOADS_EVEN = PAIR == kTCTC ? 4 : LOADS_ODD;
+        constexpr int LOADS_ODD = PAIR == kTCTC ? 12 : 8;
+        constexpr int LOADS_EVEN = PAIR == kTCTC ? 4 : 8;
         auto dma_step = [&](int s, int d) __attribute__((always_inline)) {
-            if constexpr (PAIR == kR8TR) {
-                if (d < 4) {
-                    if (s + 4 >= 0) dma_b(s + 4, d);
-                } else if (d < 7) {
-                    dma_raw(false, s + 5, d - 4);
-                }
-            } else if constexpr (PAIR == kR8R8) {
-                if (d < 6) dma_raw(d >= 3, s + 5, d % 3);
-            } else if constexpr (PAIR == kTRTR) {
+            if constexpr (PAIR == kTRTR) {
                 if (s + 4 >= 0) {
                     if (d < 4) dma_b(s + 4, d);
                     else dma_a(s + 4, d - 4);
@@ -459,61 +320,15 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
             acc[j][i] = mfma_bf16_32x32x16(bv, av, acc[j][i]);
         };
 
-        // 8-bit operands: the wave takes its own 8 token rows of a step out of the ring of codes, two rows
-        // (u = 0..3) at a time, 8 codes a lane, and writes them as bf16 where a TR stage has them.  Exact: e4m3 times a
-        // power of two is a bf16 value.
-        const int cv_hi = lane >> 5, cv_q = lane & 31;
-        struct RawStep {
-            i32x2 q[4];
-            i32x2 sc;
-        };
-        auto raw_read = [&](bool b, int x, int u, RawStep& w) __attribute__((always_inline)) {
-            const uint32_t slot = (uint32_t)(x & 3) + (b ? 4u : 0u);
-            if (u < 4) w.q[u] = lds_load_8B(tiles + R::raw_ring + 2048 * wave, slot * RAW_STAGE + 512u * u + (b ? b_raw_at : a_raw_at));
-            else w.sc = lds_load_8B(tiles + R::sc_ring + 256 * wave, slot * SC_STAGE + (uint32_t)(8 * (cv_q >> 4)));
-        };
-        auto raw_convert = [&](bool b, int x, int u, const RawStep& w) __attribute__((always_inline)) {
-            const uint32_t byte = __builtin_amdgcn_ubfe((uint32_t)w.sc[u >> 1], (uint32_t)(16 * (u & 1) + 8 * cv_hi), 8);
-            const int krow = 8 * wave + 2 * u + cv_hi;
-            lds_store_16B(tiles + (b ? R::b_ring : 0),
-                          (uint32_t)((x & 1) * TR_STAGE + krow * 512 + ((cv_q ^ ((krow & 3) << 2)) << 4)),
-                          cvt_e4m3x8_bf16(w.q[u], e8m0_scale_operand(byte)));
-        };
-        RawStep raw_a, raw_b;
-        auto convert_step = [&](int x) __attribute__((always_inline)) {
-#pragma unroll
-            for (int u = 4; u >= 0; --u) {
-                raw_read(false, x, u, raw_a);
-                if constexpr (B_8) raw_read(true, x, u, raw_b);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                raw_convert(false, x, u, raw_a);
-                if constexpr (B_8) raw_convert(true, x, u, raw_b);
-            }
-        };
-        // What step s does for step s + 2 after its MFMA k: the reads after the first five, then a conversion after
-        // every third (both operands: two).
-        auto convert_part = [&](int s, int k) __attribute__((always_inline)) {
-            if (k < 5) {
-                raw_read(false, s + 2, 4 - k, raw_a);
-                if constexpr (B_8) raw_read(true, s + 2, 4 - k, raw_b);
-            } else if (k < 17 && (k - 5) % 3 == 0) {
-                raw_convert(false, s + 2, (k - 5) / 3, raw_a);
-                if constexpr (B_8) raw_convert(true, s + 2, (k - 5) / 3, raw_b);
-            }
-        };
-
         wait_vmcnt<0>();
         // Prologue: virtual steps -5..-1, then wait for step 0's operands:
         //   TR+TR: steps 0..3 issued, step 0 first: 24 later loads may remain;
         //   TR+TC: as the default kernel mirrored (A steps 0..3, B stages 0-1 and the
         //          first half of 2): 24 after the second half of B stage 0;
         //   TC+TC: A stage 0 (-5, -4), B stage 0 and half of A stage 1 (-3), the rest
-        //          of A stage 1 (-2), B stage 1 and half of A stage 2 (-1): 20 after B 0;
-        //   8-bit: codes of steps 0..3 (-5..-2), B steps 0..2; the two steps after those of steps 0 and 1 (and B
-        //          step 0) may remain while steps 0 and 1 are converted, then step 4 is loaded over step 0.
-        auto prologue_step = [&](int v) __attribute__((always_inline)) {
+        //          of A stage 1 (-2), B stage 1 and half of A stage 2 (-1): 20 after B 0.
+#pragma unroll
+        for (int v = -5; v < 0; ++v) {
             if (v & 1) {
 #pragma unroll
                 for (int d = 0; d < LOADS_ODD; ++d) dma_step(v, d);
@@ -521,22 +336,9 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
 #pragma unroll
                 for (int d = 0; d < LOADS_EVEN; ++d) dma_step(v, d);
             }
-        };
-#pragma unroll
-        for (int v = -5; v < (A_8 ? -1 : 0); ++v) prologue_step(v);
-        if constexpr (A_8) {
-            wait_vmcnt<2 * LOADS_ODD>();
-            asm volatile("" ::: "memory");
-            convert_step(0);
-            convert_step(1);
-            asm volatile("" ::: "memory");
-            wait_lgkmcnt0();
-            prologue_step(-1);                  // its codes take the place of step 0's
-        } else if constexpr (PAIR == kTCTC) {
-            wait_vmcnt<20>();
-        } else {
-            wait_vmcnt<24>();
         }
+        if constexpr (PAIR == kTCTC) wait_vmcnt<20>();
+        else wait_vmcnt<24>();
         barrier_no_fence();
         Frags f0, f1;
 #pragma unroll
@@ -548,10 +350,8 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
         // and the 16 block reads of step s+1 after the 16th MFMA.
         auto body = [&](int s, auto odd_tag, Frags& cur, Frags& nxt) __attribute__((always_inline)) {
             constexpr bool odd = decltype(odd_tag)::value;
-            if constexpr (A_8) asm volatile("" ::: "memory");    // step s+1's conversions come before the wait
             wait_lgkmcnt0();
-            if constexpr (A_8) wait_vmcnt<2 * LOADS_ODD>();
-            else if constexpr (PAIR == kTRTR) wait_vmcnt<16>();
+            if constexpr (PAIR == kTRTR) wait_vmcnt<16>();
             else if constexpr (PAIR == kTRTC || PAIR == kTCTR) {
                 if constexpr (odd) wait_vmcnt<16>();
                 else wait_vmcnt<20>();
@@ -575,7 +375,6 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
                 } else {
                     if ((k & 3) == 0) dma_step(s, k >> 2);
                 }
-                if constexpr (A_8) convert_part(s, k);
                 if (k >= 16) read_one(s + 1, k - 16, nxt);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -587,7 +386,7 @@ __global__ __launch_bounds__(NT, 1) void wgrad_bf16_kernel(GroupedParams p) {
         wait_vmcnt<0>();
         wait_lgkmcnt0();
         barrier_no_fence();
-        claim_next();
+        sched.claim_next();
         store_wave_tile_staged<OUT>(p, eo, m0 + wm * 128, n0 + wn * 128, lane, acc, tiles + wave * 32768);
         barrier_no_fence();
     }
@@ -616,12 +415,6 @@ hipError_t launch_wgrad_bf16_layout(const GroupedParams& p, bool a_m_major, bool
     else if (a_m_major) launch_pair<kTRTC>(p, out_kind, grid, stream);
     else if (b_k_major) launch_pair<kTCTC>(p, out_kind, grid, stream);
     else launch_pair<kTCTR>(p, out_kind, grid, stream);
-    return hipGetLastError();
-}
-
-hipError_t launch_wgrad_fp8_rows(const GroupedParams& p, int out_kind, int grid, hipStream_t stream) {
-    if (p.sfb) launch_pair<kR8R8>(p, out_kind, grid, stream);
-    else launch_pair<kR8TR>(p, out_kind, grid, stream);
     return hipGetLastError();
 }
 

@@ -117,7 +117,8 @@ hipError_t launch_wgrad_bf16(const GroupedParams& p, int out_kind, int grid, hip
 hipError_t launch_wgrad_bf16_layout(const GroupedParams& p, bool a_m_major, bool b_k_major, int out_kind, int grid,
                                     hipStream_t stream);
 // A (tokens_sum, hidden) e4m3 with scales (ceil(hidden/128), tokens_sum) in sfa; B (tokens_sum, n) bf16 (sfb NULL) or the same.
-hipError_t launch_wgrad_fp8_rows(const GroupedParams& p, int out_kind, int grid, hipStream_t stream);
+// tile: edge of the output tiles that p counts, 256, 128 or 64.
+hipError_t launch_wgrad_fp8_rows(const GroupedParams& p, int out_kind, int tile, int grid, hipStream_t stream);
 // Split-K second pass: out[e] (=|+=) the sum over c = 0..split-1, in order, of the fp32
 // partial slabs ws[c*E + e]; in accumulate mode an expert without tokens is left as is.
 hipError_t launch_splitk_reduce(const float* ws, const int32_t* offsets, int32_t num_experts, int64_t hidden,

@@ -316,16 +316,17 @@ kgw_status_t kgw_wgrad_fp4(const void* A, const void* sfa, const void* B, const 
  *     out[e] (=|+=) a[begin:end, :]^T @ b[begin:end, :]
  *     a(t, m) = e4m3(A[t, m]) * 2^(sa[m/128, t] - 127)      b likewise, or the bf16 B itself
  *
- *   A    e4m3 bytes (tokens_sum, hidden), row-major, 16-byte aligned; hidden a multiple of 8, 16 at least
- *        (KGW_ERROR_MISALIGNED), and below 2^25 (KGW_ERROR_UNSUPPORTED).
+ *   A    e4m3 bytes (tokens_sum, hidden), row-major, 16-byte aligned; hidden a multiple of 8
+ *        (KGW_ERROR_MISALIGNED) and below 2^25 (KGW_ERROR_UNSUPPORTED).
  *   sa   uint8 (ceil(hidden/128), tokens_sum), 4-byte aligned: the last block of a row may be shorter.
- *   B    sb NULL: bf16 (tokens_sum, n), n a multiple of 8.  Else e4m3 bytes (tokens_sum, n), n a multiple of 8, 16 at least, with
+ *   B    sb NULL: bf16 (tokens_sum, n), n a multiple of 8.  Else e4m3 bytes (tokens_sum, n), n a multiple of 8, with
  *        sb uint8 (ceil(n/128), tokens_sum).
  *   Every value is converted exactly to bf16 with its scale folded in (one that falls below bf16's smallest normal value
  *   becomes a subnormal or zero), products are summed in fp32 on the bf16 MFMA.  A scale byte of 0xFF makes the outputs that it reaches NaN.
  *   Counts must be multiples of 128.  offsets, out / out_ptrs, out_dtype, accumulate, sizes and errors as for
- *   kgw_wgrad_bf16_ex; workspace as for it, kgw_workspace_bytes(..., fp8 = 0) bytes.
+ *   kgw_wgrad_bf16_ex; workspace as for it, kgw_wgrad_fp8_rows_workspace_bytes() bytes.
  */
+size_t kgw_wgrad_fp8_rows_workspace_bytes(int32_t num_experts, int64_t hidden, int64_t n, int64_t tokens_sum);
 kgw_status_t kgw_wgrad_fp8_rows(const void* A, const uint8_t* sa, const void* B, const uint8_t* sb,
                                 const int32_t* offsets, int32_t num_experts, int64_t hidden, int64_t n,
                                 int64_t tokens_sum, void* out, void* const* out_ptrs, int32_t out_dtype,

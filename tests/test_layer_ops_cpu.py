@@ -117,7 +117,7 @@ def test_weight_gradient_arguments(lib):
                dict(n=-1), dict(T=-1), dict(dt=3), dict(acc=2)):
         assert wgrad(lib, **kw) == INVALID, kw
     for kw in (dict(A=P + 8), dict(B=P + 8), dict(out=P + 8), dict(sa=P + 2), dict(sb=P + 1), dict(off=P + 2), dict(hidden=124),
-               dict(n=60), dict(n=68, sb=P), dict(hidden=8), dict(n=8, sb=P), dict(out=None, ptrs=P + 4)):
+               dict(n=60), dict(n=68, sb=P), dict(out=None, ptrs=P + 4)):
         assert wgrad(lib, **kw) == MISALIGNED, kw
     assert wgrad(lib, T=200) == OFFSETS
     for kw in (dict(E=65537), dict(hidden=2 ** 25), dict(n=2 ** 28), dict(T=2 ** 31)):

@@ -15,7 +15,7 @@ pytestmark = [pytest.mark.gpu,
 DEV = "cuda"
 SIZES = [([256, 0, 512, 768], 256, 512), ([256, 0, 512, 768], 272, 400), ([512, 256], 16, 16), ([256], 128, 144), ([256] * 5, 1040, 784),
          ([2048] * 3 + [1024], 320, 384), ([4096, 0, 8192, 256], 320, 384), ([0, 0, 256], 144, 528),
-         ([1024 + 256 * (e % 5) for e in range(32)], 2048, 2048), ([256, 512], 24, 264), ([512, 256], 264, 776), ([256], 776, 24),
+         ([1024 + 256 * (e % 5) for e in range(32)], 2048, 2048), ([256, 512], 24, 264), ([512, 256], 264, 776), ([256], 776, 24), ([256, 256], 8, 136), ([256], 136, 8),
          ([256, 256], 1048, 520)]
 
 
@@ -48,11 +48,23 @@ def test_equals_the_bf16_product_of_the_same_rows(counts, hidden, n, out_dtype, 
     off = offsets_of(counts)
     out = torch.full((E, hidden, n), float("nan"), dtype=out_dtype, device=DEV)
     got = kgw.kgw_wgrad_fp8_rows(A, sa, B if both else b, off, sb=sb if both else None, out=out)
-    want = kgw.kgw_wgrad_bf16_ex(a, b, off, a_major="m", out_dtype=out_dtype)
-    assert got is out and torch.equal(got, want)
     one = kgw.kgw_wgrad_fp8_rows(A.view(torch.float8_e4m3fn), sa, B.view(torch.float8_e4m3fn) if both else b, off,
                                  sb=sb if both else None, out_dtype=out_dtype, split_k=False)
-    assert torch.equal(one, kgw.kgw_wgrad_bf16_ex(a, b, off, a_major="m", out_dtype=out_dtype, split_k=False))
+    want = kgw.kgw_wgrad_bf16_ex(a, b, off, a_major="m", out_dtype=out_dtype, split_k=False)
+    assert got is out and torch.equal(one, want)
+    if kgw.load_library().kgw_wgrad_fp8_rows_workspace_bytes(E, hidden, n, T) <= 256:
+        assert torch.equal(got, want)
+    else:                                                   # shares of the tokens summed apart: another order of the same sums
+        exact = to_f64(kgw.kgw_wgrad_bf16_ex(a, b, off, a_major="m", split_k=False))
+        if out_dtype == torch.float32:
+            assert_fp32_close(to_f64(got), exact)
+        elif out_dtype == torch.bfloat16:
+            assert_bf16_close(to_f64(got), exact)
+        else:
+            past = np.abs(exact) > 6e4                      # (beyond fp16: infinities of the same sign)
+            g = to_f64(got)
+            assert np.array_equal(np.sign(g[past]), np.sign(exact[past]))
+            assert_fp16_close(np.where(past, 0, g), np.where(past, 0, exact))
 
 
 @pytest.mark.parametrize("both", [False, True])
@@ -156,7 +168,7 @@ def test_refusals():
            lambda: f(A, sa.int(), b, off), lambda: f(A, sa[:, :255], b, off), lambda: f(A, sa.t(), b, off), lambda: f(A, sa.cpu(), b, off),
            lambda: f(A[:128], sa, b, off), lambda: f(A.t(), sa, b, off), lambda: f(A, sa, b, off.long()), lambda: f(A, sa, b, off.cpu()),
            lambda: f(A[:200].contiguous(), sa[:, :200].contiguous(), b[:200].contiguous(), off), lambda: f(*odd(124), b, off),
-           lambda: f(*odd(8), b, off), lambda: f(A, sa, odd(124)[0], off, sb=odd(124)[1]), lambda: f(A, sa, b[:, :100].contiguous(), off),
+           lambda: f(A, sa, odd(124)[0], off, sb=odd(124)[1]), lambda: f(A, sa, b[:, :100].contiguous(), off),
            lambda: f(A, sa, b, off, out_dtype=torch.float64), lambda: f(A, sa, b, off, accumulate=True),
            lambda: f(A, sa, b, off, out=torch.zeros((1, 128, 127), device=DEV)),
            lambda: f(A, sa, b, torch.tensor([100], dtype=torch.int32, device=DEV), validate=True)]

@@ -2,6 +2,7 @@
 // Declarations and the contract of every entry point are in include/kgw.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <mutex>
 #include <stdint.h>
 #include <string.h>
@@ -148,6 +149,51 @@ SplitPlan split_plan(int32_t num_experts, int64_t hidden, int64_t n, int64_t tok
     return plan;
 }
 
+// Output tiles of the 8-bit rows' kernel, and how many shares an expert's tokens are cut into.
+//
+// A step of 32 tokens takes a compute unit 0.82 us for a tile of 256 x 256, 0.57 us for two of 128 x 128 (0.33 us for one)
+// and 0.53 us for four of 64 x 64, so large tiles do most a unit and small ones leave fewer units idle.  Between 256 and 128
+// the rounds of each decide: 8 x 4096 x 2048 (1024 or 4096 tiles) 441 us with 256, 583 with 128; 16 x 1408 x 768 (288 or
+// 1056) 39 and 33; 2048 x 2048 (64 or 256) 50 and 24.  Below half as many tiles of 128 as units, long experts are cut into
+// shares while they keep 1024 tokens each (3 x 600 x 200, 8192 tokens each: 79 us, 25 with eight shares; 1 x 1040 x 776,
+// 8192: 79, 33 with four), and tiles of 64 are left for what is still too little (256 x 256, 32768 tokens,
+// sixteen shares: 26 us, with 128 35; 8 x 256 x 256, 256 tokens: 10 either way).
+struct RowsPlan {
+    int tile = 256;
+    int groups = 1;                                  // workgroups of a compute unit
+    SplitPlan split;
+};
+
+RowsPlan rows_plan(int32_t num_experts, int64_t hidden, int64_t n, int64_t tokens_sum, int num_cus) {
+    RowsPlan plan;
+    if (num_experts < 1 || hidden <= 0 || n <= 0 || tokens_sum <= 0 || num_cus <= 0) return plan;
+    auto items = [&](int64_t t) { return ((hidden + t - 1) / t) * ((n + t - 1) / t) * num_experts; };
+    const int64_t cus = num_cus, large = items(256), middle = items(128), rest = middle % (2 * cus);
+    const int64_t large_cost = (large + cus - 1) / cus * 82;
+    const int64_t middle_cost = middle / (2 * cus) * 57 + (rest == 0 ? 0 : rest <= cus ? 33 : 57);
+    if (large_cost <= middle_cost) return plan;
+    int64_t shares = 1;
+    auto shares_of = [&](int64_t tiles) {
+        int64_t s = std::min(std::min(kMaxSplit, cus / tiles), tokens_sum / (num_experts * kMinChunkTokens));
+        if (s < 2 || (size_t)s * (size_t)num_experts * (size_t)hidden * (size_t)n * sizeof(float) > kMaxSplitWorkspace) s = 1;
+        return s;
+    };
+    plan.tile = 128;
+    if (2 * middle <= cus) {
+        shares = shares_of(middle);
+        if (2 * middle * shares < cus) {
+            plan.tile = 64;
+            shares = 2 * items(64) <= cus ? shares_of(items(64)) : 1;
+        }
+    }
+    plan.groups = plan.tile == 128 ? 2 : 4;
+    if (shares > 1) {
+        plan.split.split = (int32_t)shares;
+        plan.split.bytes = (size_t)shares * (size_t)num_experts * (size_t)hidden * (size_t)n * sizeof(float);
+    }
+    return plan;
+}
+
 kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, const void* sfb,
                  int32_t scale_format, const int32_t* offsets, int32_t num_experts, int64_t hidden, int64_t n,
                  int64_t tokens_sum, void* out, void* const* out_ptrs, int32_t out_dtype, int32_t accumulate,
@@ -155,8 +201,8 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
     const bool rows = kernel == Kernel::kFp8Rows;    // 8-bit token rows through the bf16 kernel
     const bool fp8 = kernel != Kernel::kBf16 && !rows;   // operands scaled along the tokens (fp8 or fp4)
     const bool fp4 = kernel == Kernel::kFp4;
-    const int64_t bm = fp8 ? kgw::kFp8BM : kgw::kBf16BM;
-    const int64_t bn = fp8 ? kgw::kFp8BN : kgw::kBf16BN;
+    int64_t bm = fp8 ? kgw::kFp8BM : kgw::kBf16BM;
+    int64_t bn = fp8 ? kgw::kFp8BN : kgw::kBf16BN;
     const int64_t talign = fp4 ? KGW_FP4_TOKEN_ALIGN : (fp8 || rows ? KGW_FP8_TOKEN_ALIGN : KGW_BF16_TOKEN_ALIGN);
     const int64_t nalign = (fp8 && !fp4) ? 16 : 8;
     static_assert(KGW_OUT_FP32 == kgw::kOutF32 && KGW_OUT_BF16 == kgw::kOutBf16 && KGW_OUT_FP16 == kgw::kOutF16,
@@ -176,8 +222,7 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
         return KGW_ERROR_MISALIGNED;
     if (rows) {
         if (tokens_sum > 0 && hidden > 0 && n > 0 && !sfa) return KGW_ERROR_INVALID_VALUE;
-        // 8-bit rows move in pieces of 16 codes, the last one from the row's end
-        if (hidden % 8 != 0 || hidden == 8 || (sfb && n == 8) || (((uintptr_t)sfa | (uintptr_t)sfb) & 3u)) return KGW_ERROR_MISALIGNED;
+        if (hidden % 8 != 0 || (((uintptr_t)sfa | (uintptr_t)sfb) & 3u)) return KGW_ERROR_MISALIGNED;
         // one step's 32 token rows are addressed with 32-bit offsets
         if (64 * hidden >= ((int64_t)1 << 31)) return KGW_ERROR_UNSUPPORTED;
     }
@@ -202,6 +247,8 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
     st = current_props(&d);
     if (st != KGW_SUCCESS) return st;
     if (!d.is_gfx950) return KGW_ERROR_DEVICE;
+    const RowsPlan rplan = rows ? rows_plan(num_experts, hidden, n, tokens_sum, d.num_cus) : RowsPlan();
+    if (rows) bm = bn = rplan.tile;
 
     kgw::GroupedParams p;
     p.A = A;
@@ -246,7 +293,7 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
 
     // Split-K when planned and the caller's workspace holds the partials;
     // otherwise one pass (same result up to the order of the fp32 additions).
-    const SplitPlan plan = split_plan(num_experts, hidden, n, tokens_sum, fp8, d.num_cus);
+    const SplitPlan plan = rows ? rplan.split : split_plan(num_experts, hidden, n, tokens_sum, fp8, d.num_cus);
     const bool split = plan.split > 1 && workspace && workspace_bytes >= plan.bytes && aligned16(workspace);
     if (split) {
         p.split = plan.split;
@@ -257,9 +304,10 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
         out_kind = kgw::kOutF32;
     }
     p.sched = nullptr;
-    const int grid = p.num_items < d.num_cus ? p.num_items : d.num_cus;
+    const int most = d.num_cus * rplan.groups;
+    const int grid = p.num_items < most ? p.num_items : most;
     hipError_t err = hipSuccess;
-    if (!fp8 && !split && dynamic_plan(num_experts, hidden, n, tokens_sum, d.num_cus) &&
+    if (!fp8 && (!rows || rplan.tile == 256) && !split && dynamic_plan(num_experts, hidden, n, tokens_sum, d.num_cus) &&
         workspace && workspace_bytes >= kgw::kSchedWords * sizeof(int32_t) && aligned16(workspace) &&
         grid % d.num_xcds == 0) {
         p.sched = (int32_t*)workspace;
@@ -280,7 +328,7 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
                                                         (hipStream_t)stream)
                          : kgw::launch_wgrad_fp8(p, out_kind, grid, (hipStream_t)stream);
             break;
-        case Kernel::kFp8Rows: err = kgw::launch_wgrad_fp8_rows(p, out_kind, grid, (hipStream_t)stream); break;
+        case Kernel::kFp8Rows: err = kgw::launch_wgrad_fp8_rows(p, out_kind, rplan.tile, grid, (hipStream_t)stream); break;
         case Kernel::kFp4: err = kgw::launch_wgrad_fp4(p, out_kind, grid, (hipStream_t)stream); break;
         default: err = kgw::launch_wgrad_fp8_native(p, out_kind, grid, (hipStream_t)stream); break;
     }
@@ -508,6 +556,14 @@ kgw_status_t kgw_mgrouped_fp8(const void* A, const uint8_t* sa, const void* W, c
     const int grid = p.num_items < d.num_cus ? p.num_items : d.num_cus;
     const hipError_t err = kgw::launch_mgrouped_fp8(p, layout == KGW_LAYOUT_NT, out_dtype, grid, (hipStream_t)stream);
     return err == hipSuccess ? KGW_SUCCESS : KGW_ERROR_DEVICE;
+}
+
+size_t kgw_wgrad_fp8_rows_workspace_bytes(int32_t num_experts, int64_t hidden, int64_t n, int64_t tokens_sum) {
+    DeviceProps d;
+    const int num_cus = current_props(&d) == KGW_SUCCESS ? d.num_cus : kDefaultCus;
+    const RowsPlan plan = rows_plan(num_experts, hidden, n, tokens_sum, num_cus);
+    if (plan.split.split > 1) return plan.split.bytes;
+    return plan.tile == 256 && dynamic_plan(num_experts, hidden, n, tokens_sum, num_cus) ? kgw::kSchedWords * sizeof(int32_t) : 0;
 }
 
 size_t kgw_workspace_bytes(int32_t num_experts, int64_t hidden, int64_t n, int64_t tokens_sum, int32_t fp8) {

@@ -253,11 +253,11 @@ __global__ __launch_bounds__(NT, kGroups<F>) void wgrad_rows8_kernel(GroupedPara
             else sb.store(tiles + (SLOTS + slot) * STAGE, StageB::LOADS - 1 - (i - StageA::LOADS), wave, lane, rb[set]);
         };
         Frag<F> fa[2], fb[2];                               // of the step's first and last 16 tokens
-        // read i of 4 F: blocks of A and B in turn, both halves of each
+        // read i of 4 F, two of a block, in the order in which the MFMAs need the blocks: A 0, B 0, the rest of A, of B
         auto read_item = [&](int slot, int ks, int i) __attribute__((always_inline)) {
-            const int j = i >> 2, h = i & 1;
-            if (i & 2) reader_b.read(tiles + (SLOTS + slot) * STAGE, ks, j, h, fb[ks]);
-            else reader_a.read(tiles + slot * STAGE, ks, j, h, fa[ks]);
+            const int block = i >> 1, h = i & 1;
+            if (block == 1 || block > F) reader_b.read(tiles + (SLOTS + slot) * STAGE, ks, block == 1 ? 0 : block - F, h, fb[ks]);
+            else reader_a.read(tiles + slot * STAGE, ks, block == 0 ? 0 : block - 1, h, fa[ks]);
         };
 #pragma unroll
         for (int x = 0; x < SETS; ++x)
@@ -283,8 +283,9 @@ __global__ __launch_bounds__(NT, kGroups<F>) void wgrad_rows8_kernel(GroupedPara
             constexpr int READS = 4 * F, WORK = LAST ? LOADS : STORES;
 #pragma unroll
             for (int k = 0; k < BLOCKS; ++k) {
-                // the reads come in the first half of the MFMAs, the other work after them
-                constexpr int FIRST = BLOCKS > 1 ? BLOCKS / 2 : 1;
+                // Reads: one an MFMA in the large tile, whose waves have their SIMDs alone; ahead of the last MFMAs in the
+                // smaller ones, where an MFMA that waits costs more (2048 x 2048 x 2048: 24.0 us, spread evenly 26.0).
+                constexpr int FIRST = F == 2 ? BLOCKS / 2 : BLOCKS;
                 if (k < FIRST) {
 #pragma unroll
                     for (int i = k * READS / FIRST; i < (k + 1) * READS / FIRST; ++i)
@@ -301,8 +302,10 @@ __global__ __launch_bounds__(NT, kGroups<F>) void wgrad_rows8_kernel(GroupedPara
             }
         };
         auto body = [&](auto rc, int s) __attribute__((always_inline)) {
-            asm volatile("" ::: "memory");                  // step s+1's values are written before the wait
-            wait_lgkmcnt0();
+            // Step s+1's values are written and step s-1's slot is read: LDS works in order, and only step s's first
+            // fragments were asked for after that.
+            asm volatile("" ::: "memory");
+            wait_lgkmcnt<(4 * F < 15 ? 4 * F : 15)>();
             barrier_no_fence();
             half(rc, s, std::false_type{});
             half(rc, s, std::true_type{});

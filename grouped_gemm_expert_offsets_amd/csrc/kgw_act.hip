@@ -9,11 +9,14 @@
 // 8 bits, as operands of the products that follow.
 //
 // 16 lanes hold a block, 8 values each; its largest magnitude goes round them on the DPP paths and every value is computed
-// in fp32 and rounded once.  A workgroup takes 512 columns (1 KiB of bf16 a row and load) of a run of rows; the scales,
-// one byte for a block, collect in LDS and leave as runs of bytes along the rows, as their layout (blocks, R) has
-// them.  Rows past the last offset belong to no expert: they are neither read nor written.
+// in fp32 and rounded once.  A workgroup takes 512, 256 or 128 columns, as they fit the row's length (blocks_of), of a run
+// of rows; the scales, one byte for a block, collect in LDS and leave as runs of bytes along the rows, as their layout
+// (blocks, R) has them.  Rows past the last offset belong to no expert: they are neither read nor written.
 //
-// HBM bounds both directions.
+// HBM bounds both directions from some megabytes on, a launch (4 us) and its issue below.  Measured, bf16 swiglu, MI355X:
+// 65536 x 2048 forward 166 us with a 16-bit result (6.5 TB/s), gradient 210 us, with the activation again 264 us;
+// 8192 x 4096 forward 44 us (6.1 TB/s), gradient 45 us; 33024 x 768 forward 38.6 us, gradient 37.1 us.  A copy
+// of such sizes moves 4.9 TB/s: reads outnumber writes here, which the memory takes faster.
 #include <type_traits>
 
 #include "kgw_layer.h"
@@ -24,8 +27,6 @@ namespace kgw {
 namespace {
 
 constexpr int NT = 256, WAVES = NT / 64;
-constexpr int BLOCKS = 4;                       // of a workgroup's columns
-constexpr int COLS = 128 * BLOCKS;
 constexpr int MOST_ROWS = 64;                   // of a workgroup
 
 // Eight values of a row as they are in memory.
@@ -55,19 +56,25 @@ __device__ __forceinline__ void values8(const Raw8<DT>& r, float (&f)[8]) {
         }
     }
 }
-template <int DT>
+// Results, past the caches' retention or not (see kStreamBytes).
+template <bool STREAM, class T>
+__device__ __forceinline__ void store_result(T v, KGW_GLOBAL T* p) {
+    if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+template <int DT, bool STREAM>
 __device__ __forceinline__ void store8(char* p, const float (&f)[8]) {
     using Words = std::conditional_t<DT == kOutF32, Words4At4, Words4At2>;
     if constexpr (DT == kOutF32) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const f32x4 v = {f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
-            *(KGW_GLOBAL Words*)(p + 16 * i) = __builtin_bit_cast(i32x4, v);
+            store_result<STREAM, Words>(__builtin_bit_cast(i32x4, v), (KGW_GLOBAL Words*)(p + 16 * i));
         }
     } else {
         const i32x4 v = {(int)pack_half2<DT>(f[0], f[1]), (int)pack_half2<DT>(f[2], f[3]),
                          (int)pack_half2<DT>(f[4], f[5]), (int)pack_half2<DT>(f[6], f[7])};
-        *(KGW_GLOBAL Words*)p = v;
+        store_result<STREAM, Words>(v, (KGW_GLOBAL Words*)p);
     }
 }
 
@@ -113,7 +120,7 @@ __device__ __forceinline__ int64_t live_rows(const ActParams& p) {
     return last < 0 ? 0 : min(last, p.rows);
 }
 
-// The workgroup's scale bytes of one tensor: (BLOCKS, rows) in LDS to (blocks, p.rows), whole runs along the rows.
+// The workgroup's scale bytes of one tensor: (blocks, rows) in LDS to (blocks, p.rows), whole runs along the rows.
 __device__ __forceinline__ void store_scales(const uint8_t (*sc)[MOST_ROWS], uint8_t* out, int64_t rows, int64_t b0,
                                              int blocks, int64_t r0, int count, int tid) {
     const int quads = (count + 3) / 4;
@@ -129,8 +136,11 @@ __device__ __forceinline__ void store_scales(const uint8_t (*sc)[MOST_ROWS], uin
     }
 }
 
-// Where this lane works: the workgroup's rows and blocks, and its 8 columns of every row.
+// Where this lane works: the workgroup's rows and blocks, and its 8 columns of some rows.  A wave takes PASS rows at a
+// time, 16 BLOCKS lanes each.
+template <int BLOCKS>
 struct Place {
+    static constexpr int COLS = 128 * BLOCKS, PASS = 4 / BLOCKS;
     int64_t r0;             // first row of the workgroup
     int count;              // its rows
     int64_t b0;             // its first block of a half
@@ -138,48 +148,52 @@ struct Place {
     int64_t nb;             // blocks of a half
     int64_t col;            // the lane's first column
     bool in;                // it has columns
-    int first, rows;        // the wave's rows
-};
-__device__ __forceinline__ bool place(const ActParams& p, int tid, Place& at) {
-    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t chunks = (p.inner + COLS - 1) / COLS;
-    const int64_t block = blockIdx.x / chunks, chunk = blockIdx.x - block * chunks;
-    at.r0 = block * p.group_rows;
-    const int64_t left = live_rows(p) - at.r0;
-    if (left <= 0) return false;
-    at.count = (int)min<int64_t>(left, p.group_rows);
-    at.nb = (p.inner + 127) / 128;
-    at.b0 = chunk * BLOCKS;
-    at.blocks = (int)min<int64_t>(BLOCKS, at.nb - at.b0);
-    at.col = chunk * COLS + 8 * lane;
-    at.in = at.col < p.inner;                   // inner is a multiple of 8
-    const int each = p.group_rows / WAVES;
-    at.first = wave * each;
-    at.rows = max(0, min(each, at.count - at.first));
-    return true;
-}
+    int first, passes;      // the lane's first row, and how often the wave goes on by PASS rows
 
-template <int DT, bool GATED>
+    __device__ __forceinline__ bool init(const ActParams& p, int tid) {
+        const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int64_t chunks = (p.inner + COLS - 1) / COLS;
+        const int64_t run = blockIdx.x / chunks, chunk = blockIdx.x - run * chunks;
+        r0 = run * p.group_rows;
+        const int64_t left = live_rows(p) - r0;
+        if (left <= 0) return false;
+        count = (int)min<int64_t>(left, p.group_rows);
+        nb = (p.inner + 127) / 128;
+        b0 = chunk * BLOCKS;
+        blocks = (int)min<int64_t>(BLOCKS, nb - b0);
+        col = chunk * COLS + 8 * (lane & (16 * BLOCKS - 1));
+        in = col < p.inner;                     // inner is a multiple of 8
+        const int each = p.group_rows / WAVES;
+        first = wave * each + lane / (16 * BLOCKS);
+        passes = (max(0, min(each, count - wave * each)) + PASS - 1) / PASS;
+        return true;
+    }
+    __device__ __forceinline__ bool has(int r) const { return in && r < count; }
+};
+
+template <int DT, bool GATED, int BLOCKS>
 __global__ __launch_bounds__(NT) void act_kernel(ActParams p) {
     constexpr int S = RowElem<DT>::size, HALVES = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(4))) uint8_t sc[HALVES + 1][BLOCKS][MOST_ROWS];
-    const int tid = threadIdx.x, lane = tid & 63, block = lane >> 4;
-    Place at;
-    if (!place(p, tid, at)) return;
+    const int tid = threadIdx.x, lane = tid & 63, block = (lane >> 4) & (BLOCKS - 1);
+    constexpr int PASS = Place<BLOCKS>::PASS;
+    Place<BLOCKS> at;
+    if (!at.init(p, tid)) return;
     const int64_t wide = HALVES * p.inner;
     auto load = [&](int r, Raw8<DT> (&raw)[HALVES]) __attribute__((always_inline)) {
         const char* row = (const char*)p.h + ((at.r0 + r) * p.ld_h + at.col) * S;
 #pragma unroll
         for (int k = 0; k < HALVES; ++k) {
-            if (at.in) raw[k] = load8_once<DT>(row + k * p.inner * S);
+            if (at.has(r)) raw[k] = load8_once<DT>(row + k * p.inner * S);
             else raw[k] = Raw8<DT>{};
         }
     };
     Raw8<DT> now[HALVES], next[HALVES];
-    if (at.rows > 0) load(at.first, now);
-    for (int i = 0; i < at.rows; ++i) {
-        const int r = at.first + i;
-        if (i + 1 < at.rows) load(r + 1, next);
+    if (at.passes > 0) load(at.first, now);
+    for (int i = 0; i < at.passes; ++i) {
+        const int r = at.first + i * PASS;
+        const bool in = at.has(r);
+        if (i + 1 < at.passes) load(r + PASS, next);
         float f[HALVES][8], y[8];
 #pragma unroll
         for (int k = 0; k < HALVES; ++k) values8<DT>(now[k], f[k]);
@@ -198,17 +212,17 @@ __global__ __launch_bounds__(NT) void act_kernel(ActParams p) {
             for (int k = 0; k < HALVES; ++k) {
                 i32x2 codes;
                 const uint32_t e = quantise8(f[k], codes);
-                if (at.in) store_codes(p.saved + row * wide + k * p.inner + at.col, codes);
+                if (in) store_codes(p.saved + row * wide + k * p.inner + at.col, codes);
                 if ((lane & 15) == 0) sc[k][block][r] = (uint8_t)e;
             }
         }
         if (p.y_scales) {
             i32x2 codes;
             const uint32_t e = quantise8(y, codes);
-            if (at.in) *(KGW_GLOBAL i32x2*)((uint8_t*)p.y + row * p.inner + at.col) = codes;
+            if (in) store_result<false>(codes, (KGW_GLOBAL i32x2*)((uint8_t*)p.y + row * p.inner + at.col));
             if ((lane & 15) == 0) sc[HALVES][block][r] = (uint8_t)e;
-        } else if (at.in) {
-            store8<DT>((char*)p.y + (row * p.inner + at.col) * S, y);
+        } else if (in) {
+            store8<DT, false>((char*)p.y + (row * p.inner + at.col) * S, y);
         }
 #pragma unroll
         for (int k = 0; k < HALVES; ++k) now[k] = next[k];
@@ -223,13 +237,14 @@ __global__ __launch_bounds__(NT) void act_kernel(ActParams p) {
     if (p.y_scales) store_scales(sc[HALVES], p.y_scales, p.rows, at.b0, at.blocks, at.r0, at.count, tid);
 }
 
-template <int DT, bool GATED>
+template <int DT, bool GATED, int BLOCKS, bool STREAM>
 __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
     constexpr int S = RowElem<DT>::size, HALVES = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(4))) uint8_t sc[HALVES + 1][BLOCKS][MOST_ROWS];
-    const int tid = threadIdx.x, lane = tid & 63, block = lane >> 4;
-    Place at;
-    if (!place(p, tid, at)) return;
+    const int tid = threadIdx.x, lane = tid & 63, block = (lane >> 4) & (BLOCKS - 1);
+    constexpr int PASS = Place<BLOCKS>::PASS;
+    Place<BLOCKS> at;
+    if (!at.init(p, tid)) return;
     const int64_t wide = HALVES * p.inner;
     struct Row {
         i32x2 codes[HALVES];
@@ -238,7 +253,7 @@ __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
     };
     auto load = [&](int r, Row& raw) __attribute__((always_inline)) {
         const int64_t row = at.r0 + r;
-        if (at.in) {
+        if (at.has(r)) {
             raw.dy = load8_once<DT>((const char*)p.dy + (row * p.ld_dy + at.col) * S);
 #pragma unroll
             for (int k = 0; k < HALVES; ++k) {
@@ -250,10 +265,11 @@ __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
         }
     };
     Row now, next;
-    if (at.rows > 0) load(at.first, now);
-    for (int i = 0; i < at.rows; ++i) {
-        const int r = at.first + i;
-        if (i + 1 < at.rows) load(r + 1, next);
+    if (at.passes > 0) load(at.first, now);
+    for (int i = 0; i < at.passes; ++i) {
+        const int r = at.first + i * PASS;
+        const bool in = at.has(r);
+        if (i + 1 < at.passes) load(r + PASS, next);
         float f[HALVES][8], dy[8], y[8], d[HALVES][8];
 #pragma unroll
         for (int k = 0; k < HALVES; ++k) decode8(now.codes[k], now.scale[k], f[k]);
@@ -278,19 +294,19 @@ __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
             if (p.dh_scales) {
                 i32x2 codes;
                 const uint32_t e = quantise8(d[k], codes);
-                if (at.in) *(KGW_GLOBAL i32x2*)((uint8_t*)p.dh + to) = codes;
+                if (in) store_result<STREAM>(codes, (KGW_GLOBAL i32x2*)((uint8_t*)p.dh + to));
                 if ((lane & 15) == 0) sc[k][block][r] = (uint8_t)e;
-            } else if (at.in) {
-                store8<DT>((char*)p.dh + to * S, d[k]);
+            } else if (in) {
+                store8<DT, STREAM>((char*)p.dh + to * S, d[k]);
             }
         }
         if (p.y_scales) {
             i32x2 codes;
             const uint32_t e = quantise8(y, codes);
-            if (at.in) *(KGW_GLOBAL i32x2*)((uint8_t*)p.y + row * p.inner + at.col) = codes;
+            if (in) store_result<STREAM>(codes, (KGW_GLOBAL i32x2*)((uint8_t*)p.y + row * p.inner + at.col));
             if ((lane & 15) == 0) sc[HALVES][block][r] = (uint8_t)e;
-        } else if (p.y && at.in) {
-            store8<DT>((char*)p.y + (row * p.inner + at.col) * S, y);
+        } else if (p.y && in) {
+            store8<DT, STREAM>((char*)p.y + (row * p.inner + at.col) * S, y);
         }
         now = next;
     }
@@ -304,29 +320,62 @@ __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
     if (p.y_scales) store_scales(sc[HALVES], p.y_scales, p.rows, at.b0, at.blocks, at.r0, at.count, tid);
 }
 
+// A workgroup's blocks: as many as leave at most an eighth of the lanes idle (768 columns, six blocks: three workgroups
+// of two; with four a half-empty one a row cost a quarter of the bandwidth).
+int blocks_of(int64_t inner) {
+    const int64_t nb = (inner + 127) / 128;
+    for (int blocks = 4; blocks > 1; blocks /= 2)
+        if (8 * nb >= 7 * ((nb + blocks - 1) / blocks * blocks)) return blocks;
+    return 1;
+}
+
+// Gradients of this and more go past the caches' retention: half as much again as the Infinity Cache's 256 MB, so that the
+// product that reads them does not find them there anyway (65536 x 2048 bf16, 0.54 GB: 219 -> 210 us; 0.27 GB, relu2:
+// 110 -> 121).  A store of 16-bit rows or codes writes whole lines; one of fp32 rows every other 16 bytes, and loses (204 ->
+// 213 us).  y is stored for the product that follows at once (166 -> 205 us).
+constexpr int64_t kStreamBytes = (int64_t)384 << 20;
+int64_t written(const ActParams& p, int halves) {
+    return p.rows * p.inner * ((p.dh_scales ? 1 : 2) * halves + (!p.y ? 0 : p.y_scales ? 1 : 2));
+}
+
+template <int DT, bool GATED, int BLOCKS>
+void launch_blocks(const ActParams& p, bool grad, unsigned grid, hipStream_t stream) {
+    if (grad) {
+        if (DT != kOutF32 && written(p, GATED ? 2 : 1) >= kStreamBytes)
+            hipLaunchKernelGGL((act_grad_kernel<DT, GATED, BLOCKS, true>), dim3(grid), dim3(NT), 0, stream, p);
+        else
+            hipLaunchKernelGGL((act_grad_kernel<DT, GATED, BLOCKS, false>), dim3(grid), dim3(NT), 0, stream, p);
+    } else {
+        hipLaunchKernelGGL((act_kernel<DT, GATED, BLOCKS>), dim3(grid), dim3(NT), 0, stream, p);
+    }
+}
+template <int DT, bool GATED>
+void launch_gated(const ActParams& p, bool grad, unsigned grid, hipStream_t stream) {
+    const int blocks = blocks_of(p.inner);
+    if (blocks == 4) launch_blocks<DT, GATED, 4>(p, grad, grid, stream);
+    else if (blocks == 2) launch_blocks<DT, GATED, 2>(p, grad, grid, stream);
+    else launch_blocks<DT, GATED, 1>(p, grad, grid, stream);
+}
 template <int DT>
 void launch_dtype(const ActParams& p, bool gated, bool grad, unsigned grid, hipStream_t stream) {
-    if (grad) {
-        if (gated) hipLaunchKernelGGL((act_grad_kernel<DT, true>), dim3(grid), dim3(NT), 0, stream, p);
-        else hipLaunchKernelGGL((act_grad_kernel<DT, false>), dim3(grid), dim3(NT), 0, stream, p);
-    } else {
-        if (gated) hipLaunchKernelGGL((act_kernel<DT, true>), dim3(grid), dim3(NT), 0, stream, p);
-        else hipLaunchKernelGGL((act_kernel<DT, false>), dim3(grid), dim3(NT), 0, stream, p);
-    }
+    if (gated) launch_gated<DT, true>(p, grad, grid, stream);
+    else launch_gated<DT, false>(p, grad, grid, stream);
 }
 
 }  // namespace
 
+// Rows of a workgroup: 64 where that makes enough of them (runs of 64 scale bytes), fewer down to a pass of its waves.
 int act_group_rows(int64_t rows, int64_t inner) {
-    const int64_t chunks = (inner + COLS - 1) / COLS;
-    for (int each = MOST_ROWS; each > WAVES; each /= 4)
+    const int blocks = blocks_of(inner), least = WAVES * (4 / blocks);
+    const int64_t chunks = (inner + 128 * blocks - 1) / (128 * blocks);
+    for (int each = MOST_ROWS; each > least; each /= 2)
         if ((rows + each - 1) / each * chunks >= 1024) return each;
-    return WAVES;
+    return least;
 }
 
 int64_t act_grid(int64_t rows, int64_t inner) {
-    const int64_t each = act_group_rows(rows, inner);
-    return (rows + each - 1) / each * ((inner + COLS - 1) / COLS);
+    const int64_t each = act_group_rows(rows, inner), cols = 128 * blocks_of(inner);
+    return (rows + each - 1) / each * ((inner + cols - 1) / cols);
 }
 
 hipError_t launch_act(const ActParams& p, int dtype, bool gated, bool grad, hipStream_t stream) {

@@ -14,7 +14,7 @@
 // (blocks, R) has them.  Rows past the last offset belong to no expert: they are neither read nor written.
 //
 // HBM bounds both directions from some megabytes on, a launch (4 us) and its issue below.  Measured, bf16 swiglu, MI355X:
-// 65536 x 2048 forward 166 us with a 16-bit result (6.5 TB/s), gradient 210 us, with the activation again 264 us;
+// 65536 x 2048 forward 166 us with a 16-bit result (6.5 TB/s), gradient 210 us, with the activation again 231 us (5.8);
 // 8192 x 4096 forward 44 us (6.1 TB/s), gradient 45 us; 33024 x 768 forward 38.6 us, gradient 37.1 us.  A copy
 // of such sizes moves 4.9 TB/s: reads outnumber writes here, which the memory takes faster.
 #include <type_traits>
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(NT) void act_kernel(ActParams p) {
     if (p.y_scales) store_scales(sc[HALVES], p.y_scales, p.rows, at.b0, at.blocks, at.r0, at.count, tid);
 }
 
-template <int DT, bool GATED, int BLOCKS, bool STREAM>
+template <int DT, bool GATED, int BLOCKS, bool STREAM, bool STREAM_Y>
 __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
     constexpr int S = RowElem<DT>::size, HALVES = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(4))) uint8_t sc[HALVES + 1][BLOCKS][MOST_ROWS];
@@ -303,10 +303,10 @@ __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
         if (p.y_scales) {
             i32x2 codes;
             const uint32_t e = quantise8(y, codes);
-            if (in) store_result<STREAM>(codes, (KGW_GLOBAL i32x2*)((uint8_t*)p.y + row * p.inner + at.col));
+            if (in) store_result<STREAM_Y>(codes, (KGW_GLOBAL i32x2*)((uint8_t*)p.y + row * p.inner + at.col));
             if ((lane & 15) == 0) sc[HALVES][block][r] = (uint8_t)e;
         } else if (p.y && in) {
-            store8<DT, STREAM>((char*)p.y + (row * p.inner + at.col) * S, y);
+            store8<DT, STREAM_Y>((char*)p.y + (row * p.inner + at.col) * S, y);
         }
         now = next;
     }
@@ -330,24 +330,23 @@ int blocks_of(int64_t inner) {
 }
 
 // Gradients of this and more go past the caches' retention: half as much again as the Infinity Cache's 256 MB, so that the
-// product that reads them does not find them there anyway (65536 x 2048 bf16, 0.54 GB: 219 -> 210 us; 0.27 GB, relu2:
-// 110 -> 121).  A store of 16-bit rows or codes writes whole lines; one of fp32 rows every other 16 bytes, and loses (204 ->
-// 213 us).  y is stored for the product that follows at once (166 -> 205 us).
+// product that reads them does not find them there anyway.  dh goes where it and y together reach this, y where it
+// does by itself: y then keeps the caches, and its product is the next to run.  bf16 swiglu, the gradient with the
+// activation again: 65536 x 2048 (dh 0.54 GB, y 0.27) 274 us with neither, 264 with both, 231 with dh alone;
+// 131072 x 2048 541 with neither, 524 with both.  Below it: 65536 x 2048 relu2 (0.27 GB) 110 -> 121 us.  fp32 rows are
+// written every other 16 bytes a store and lose (204 -> 213 us), and so does the forward pass (y 0.54 GB: 367 -> 407 us).
 constexpr int64_t kStreamBytes = (int64_t)384 << 20;
-int64_t written(const ActParams& p, int halves) {
-    return p.rows * p.inner * ((p.dh_scales ? 1 : 2) * halves + (!p.y ? 0 : p.y_scales ? 1 : 2));
-}
+int64_t bytes_of_y(const ActParams& p) { return !p.y ? 0 : p.rows * p.inner * (p.y_scales ? 1 : 2); }
+int64_t bytes_of_dh(const ActParams& p, int halves) { return p.rows * p.inner * halves * (p.dh_scales ? 1 : 2); }
 
 template <int DT, bool GATED, int BLOCKS>
 void launch_blocks(const ActParams& p, bool grad, unsigned grid, hipStream_t stream) {
-    if (grad) {
-        if (DT != kOutF32 && written(p, GATED ? 2 : 1) >= kStreamBytes)
-            hipLaunchKernelGGL((act_grad_kernel<DT, GATED, BLOCKS, true>), dim3(grid), dim3(NT), 0, stream, p);
-        else
-            hipLaunchKernelGGL((act_grad_kernel<DT, GATED, BLOCKS, false>), dim3(grid), dim3(NT), 0, stream, p);
-    } else {
-        hipLaunchKernelGGL((act_kernel<DT, GATED, BLOCKS>), dim3(grid), dim3(NT), 0, stream, p);
-    }
+    const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), 0, stream, p); };
+    const int64_t y = bytes_of_y(p), all = bytes_of_dh(p, GATED ? 2 : 1) + y;
+    if (!grad) go(act_kernel<DT, GATED, BLOCKS>);
+    else if (DT == kOutF32 || all < kStreamBytes) go(act_grad_kernel<DT, GATED, BLOCKS, false, false>);
+    else if (y < kStreamBytes) go(act_grad_kernel<DT, GATED, BLOCKS, true, false>);
+    else go(act_grad_kernel<DT, GATED, BLOCKS, true, true>);
 }
 template <int DT, bool GATED>
 void launch_gated(const ActParams& p, bool grad, unsigned grid, hipStream_t stream) {

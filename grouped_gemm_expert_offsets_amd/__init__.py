@@ -1167,8 +1167,12 @@ def _act_args(act: str, offsets: Optional[torch.Tensor], device):
 
 def _act_rows(t: Optional[torch.Tensor], rows: int, cols: int, halves: int, fp8: bool, dtype, device, what: str, stream):
     """A result of the activation and its scales: rows of `dtype`, or e4m3 bytes."""
-    t = _result(t, (rows, cols), torch.uint8 if fp8 else dtype, device, what, stream)
-    blocks = halves * -(-(cols // halves) // FP8_TOKEN_ALIGN)
+    dtype = torch.uint8 if fp8 else dtype
+    blocks = halves * -(-(cols // halves) // FP8_TOKEN_ALIGN) if fp8 else 0
+    if stream is None and t is None:                       # (with its strides given an allocation takes 1.3 us, without 1.6)
+        t = torch.empty_strided((rows, cols), (cols or 1, 1), dtype=dtype, device=device)
+        return t, torch.empty_strided((blocks, rows), (rows or 1, 1), dtype=torch.uint8, device=device) if fp8 else None
+    t = _result(t, (rows, cols), dtype, device, what, stream)
     return t, _empty((blocks, rows), torch.uint8, device, stream) if fp8 else None
 
 

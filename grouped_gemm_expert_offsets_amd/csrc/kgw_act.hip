@@ -15,8 +15,9 @@
 //
 // HBM bounds both directions from some megabytes on, a launch (4 us) and its issue below.  Measured, bf16 swiglu, MI355X:
 // 65536 x 2048 forward 166 us with a 16-bit result (6.5 TB/s), gradient 210 us, with the activation again 231 us (5.8);
-// 8192 x 4096 forward 44 us (6.1 TB/s), gradient 45 us; 33024 x 768 forward 38.6 us, gradient 37.1 us.  A copy
-// of such sizes moves 4.9 TB/s: reads outnumber writes here, which the memory takes faster.
+// 8192 x 4096 forward 44 us (6.1 TB/s), gradient 45 us; 33024 x 768 forward 38.6 us, gradient 37.1 us; fp32:
+// 16384 x 4096 forward 148 us (6.3 TB/s), gradient 184 us, with the activation again 212 us (5.7).  A copy of such sizes moves
+// 4.7 to 5.4 TB/s and a fill 6.9; the counters show that no byte is written twice.
 #include <type_traits>
 
 #include "kgw_layer.h"
@@ -29,19 +30,39 @@ namespace {
 constexpr int NT = 256, WAVES = NT / 64;
 constexpr int MOST_ROWS = 64;                   // of a workgroup
 
-// Eight values of a row as they are in memory.
+// A lane's eight values of a block: eight in a row of 16-bit types, so that a load or store of 16 bytes a lane takes whole
+// lines; for fp32 four of the block's first half and four of its second, for the same reason (with eight in a row, 16
+// bytes in every 32 a load, the gradient of 33024 x 768 with the activation again took 99 us, with fours 80; the codes go by
+// fours then too, which costs 8-bit results 2 to 6%).
+template <int DT>
+constexpr int kSecond = DT == kOutF32 ? 64 : 4;        // column of the second four, from the first's
+template <int DT>
+constexpr int kFours = DT == kOutF32 ? 2 : 1;          // runs of a lane
+
+// As they are in memory; `in` tells which of the lane's runs the row has.
 template <int DT>
 struct Raw8 {
-    i32x4 v[DT == kOutF32 ? 2 : 1];
+    i32x4 v[kFours<DT>];
 };
 template <int DT>
-__device__ __forceinline__ Raw8<DT> load8_once(const char* p) {
-    Raw8<DT> r;
+__device__ __forceinline__ Raw8<DT> load8_once(const char* p, const bool (&in)[2]) {
+    Raw8<DT> r{};
     using Words = std::conditional_t<DT == kOutF32, Words4At4, Words4At2>;
 #pragma unroll
-    for (int i = 0; i < (DT == kOutF32 ? 2 : 1); ++i)
-        r.v[i] = __builtin_nontemporal_load((const KGW_GLOBAL Words*)(p + 16 * i));
+    for (int i = 0; i < kFours<DT>; ++i)
+        if (in[i]) r.v[i] = __builtin_nontemporal_load((const KGW_GLOBAL Words*)(p + 4 * kSecond<DT> * i));
     return r;
+}
+template <int DT>
+__device__ __forceinline__ i32x2 load_codes(const uint8_t* p, const bool (&in)[2]) {
+    i32x2 c = {0, 0};
+    if constexpr (kFours<DT> == 2) {
+        if (in[0]) c[0] = __builtin_nontemporal_load((const KGW_GLOBAL int*)p);
+        if (in[1]) c[1] = __builtin_nontemporal_load((const KGW_GLOBAL int*)(p + kSecond<DT>));
+    } else {
+        if (in[0]) c = __builtin_nontemporal_load((const KGW_GLOBAL i32x2*)p);
+    }
+    return c;
 }
 template <int DT>
 __device__ __forceinline__ void values8(const Raw8<DT>& r, float (&f)[8]) {
@@ -63,18 +84,27 @@ __device__ __forceinline__ void store_result(T v, KGW_GLOBAL T* p) {
     else *p = v;
 }
 template <int DT, bool STREAM>
-__device__ __forceinline__ void store8(char* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(char* p, const float (&f)[8], const bool (&in)[2]) {
     using Words = std::conditional_t<DT == kOutF32, Words4At4, Words4At2>;
     if constexpr (DT == kOutF32) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const f32x4 v = {f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
-            store_result<STREAM, Words>(__builtin_bit_cast(i32x4, v), (KGW_GLOBAL Words*)(p + 16 * i));
+            if (in[i]) store_result<STREAM, Words>(__builtin_bit_cast(i32x4, v), (KGW_GLOBAL Words*)(p + 4 * kSecond<DT> * i));
         }
     } else {
         const i32x4 v = {(int)pack_half2<DT>(f[0], f[1]), (int)pack_half2<DT>(f[2], f[3]),
                          (int)pack_half2<DT>(f[4], f[5]), (int)pack_half2<DT>(f[6], f[7])};
-        store_result<STREAM, Words>(v, (KGW_GLOBAL Words*)p);
+        if (in[0]) store_result<STREAM, Words>(v, (KGW_GLOBAL Words*)p);
+    }
+}
+template <int DT, bool STREAM>
+__device__ __forceinline__ void store_codes(uint8_t* p, i32x2 codes, const bool (&in)[2]) {
+    if constexpr (kFours<DT> == 2) {
+        if (in[0]) store_result<STREAM>((int)codes[0], (KGW_GLOBAL int*)p);
+        if (in[1]) store_result<STREAM>((int)codes[1], (KGW_GLOBAL int*)(p + kSecond<DT>));
+    } else {
+        if (in[0]) store_result<STREAM>(codes, (KGW_GLOBAL i32x2*)p);
     }
 }
 
@@ -94,9 +124,6 @@ __device__ __forceinline__ uint32_t quantise8(const float (&f)[8], i32x2& codes)
     codes[0] = cvt4(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
     codes[1] = cvt4(f[4] * s, f[5] * s, f[6] * s, f[7] * s);
     return e;
-}
-__device__ __forceinline__ void store_codes(uint8_t* p, i32x2 codes) {
-    __builtin_nontemporal_store(codes, (KGW_GLOBAL i32x2*)p);
 }
 __device__ __forceinline__ void decode8(i32x2 codes, uint32_t scale, float (&f)[8]) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -136,9 +163,9 @@ __device__ __forceinline__ void store_scales(const uint8_t (*sc)[MOST_ROWS], uin
     }
 }
 
-// Where this lane works: the workgroup's rows and blocks, and its 8 columns of some rows.  A wave takes PASS rows at a
-// time, 16 BLOCKS lanes each.
-template <int BLOCKS>
+// Where this lane works: the workgroup's rows and blocks, and its 8 columns of some rows, `SECOND` between the fours.  A
+// wave takes PASS rows at a time, 16 BLOCKS lanes each.
+template <int BLOCKS, int SECOND>
 struct Place {
     static constexpr int COLS = 128 * BLOCKS, PASS = 4 / BLOCKS;
     int64_t r0;             // first row of the workgroup
@@ -147,7 +174,7 @@ struct Place {
     int blocks;             // its blocks
     int64_t nb;             // blocks of a half
     int64_t col;            // the lane's first column
-    bool in;                // it has columns
+    bool in[2];             // whether the row has its fours
     int first, passes;      // the lane's first row, and how often the wave goes on by PASS rows
 
     __device__ __forceinline__ bool init(const ActParams& p, int tid) {
@@ -161,14 +188,19 @@ struct Place {
         nb = (p.inner + 127) / 128;
         b0 = chunk * BLOCKS;
         blocks = (int)min<int64_t>(BLOCKS, nb - b0);
-        col = chunk * COLS + 8 * (lane & (16 * BLOCKS - 1));
-        in = col < p.inner;                     // inner is a multiple of 8
+        const int at = lane & (16 * BLOCKS - 1);
+        col = chunk * COLS + (SECOND == 4 ? 8 * at : 128 * (at >> 4) + 4 * (at & 15));
+        in[0] = col < p.inner;                  // inner is a multiple of 8
+        in[1] = col + SECOND < p.inner;
         const int each = p.group_rows / WAVES;
         first = wave * each + lane / (16 * BLOCKS);
         passes = (max(0, min(each, count - wave * each)) + PASS - 1) / PASS;
         return true;
     }
-    __device__ __forceinline__ bool has(int r) const { return in && r < count; }
+    __device__ __forceinline__ void has(int r, bool (&here)[2]) const {
+        here[0] = in[0] && r < count;
+        here[1] = in[1] && r < count;
+    }
 };
 
 template <int DT, bool GATED, int BLOCKS>
@@ -176,23 +208,29 @@ __global__ __launch_bounds__(NT) void act_kernel(ActParams p) {
     constexpr int S = RowElem<DT>::size, HALVES = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(4))) uint8_t sc[HALVES + 1][BLOCKS][MOST_ROWS];
     const int tid = threadIdx.x, lane = tid & 63, block = (lane >> 4) & (BLOCKS - 1);
-    constexpr int PASS = Place<BLOCKS>::PASS;
-    Place<BLOCKS> at;
+    using At = Place<BLOCKS, kSecond<DT>>;
+    constexpr int PASS = At::PASS;
+    At at;
     if (!at.init(p, tid)) return;
     const int64_t wide = HALVES * p.inner;
     auto load = [&](int r, Raw8<DT> (&raw)[HALVES]) __attribute__((always_inline)) {
         const char* row = (const char*)p.h + ((at.r0 + r) * p.ld_h + at.col) * S;
+        bool in[2];
+        at.has(r, in);
+        if (in[0]) {
 #pragma unroll
-        for (int k = 0; k < HALVES; ++k) {
-            if (at.has(r)) raw[k] = load8_once<DT>(row + k * p.inner * S);
-            else raw[k] = Raw8<DT>{};
+            for (int k = 0; k < HALVES; ++k) raw[k] = load8_once<DT>(row + k * p.inner * S, in);
+        } else {
+#pragma unroll
+            for (int k = 0; k < HALVES; ++k) raw[k] = Raw8<DT>{};
         }
     };
     Raw8<DT> now[HALVES], next[HALVES];
     if (at.passes > 0) load(at.first, now);
     for (int i = 0; i < at.passes; ++i) {
         const int r = at.first + i * PASS;
-        const bool in = at.has(r);
+        bool in[2];
+        at.has(r, in);
         if (i + 1 < at.passes) load(r + PASS, next);
         float f[HALVES][8], y[8];
 #pragma unroll
@@ -212,17 +250,17 @@ __global__ __launch_bounds__(NT) void act_kernel(ActParams p) {
             for (int k = 0; k < HALVES; ++k) {
                 i32x2 codes;
                 const uint32_t e = quantise8(f[k], codes);
-                if (in) store_codes(p.saved + row * wide + k * p.inner + at.col, codes);
+                store_codes<DT, true>(p.saved + row * wide + k * p.inner + at.col, codes, in);
                 if ((lane & 15) == 0) sc[k][block][r] = (uint8_t)e;
             }
         }
         if (p.y_scales) {
             i32x2 codes;
             const uint32_t e = quantise8(y, codes);
-            if (in) store_result<false>(codes, (KGW_GLOBAL i32x2*)((uint8_t*)p.y + row * p.inner + at.col));
+            store_codes<DT, false>((uint8_t*)p.y + row * p.inner + at.col, codes, in);
             if ((lane & 15) == 0) sc[HALVES][block][r] = (uint8_t)e;
-        } else if (in) {
-            store8<DT, false>((char*)p.y + (row * p.inner + at.col) * S, y);
+        } else {
+            store8<DT, false>((char*)p.y + (row * p.inner + at.col) * S, y, in);
         }
 #pragma unroll
         for (int k = 0; k < HALVES; ++k) now[k] = next[k];
@@ -242,8 +280,9 @@ __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
     constexpr int S = RowElem<DT>::size, HALVES = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(4))) uint8_t sc[HALVES + 1][BLOCKS][MOST_ROWS];
     const int tid = threadIdx.x, lane = tid & 63, block = (lane >> 4) & (BLOCKS - 1);
-    constexpr int PASS = Place<BLOCKS>::PASS;
-    Place<BLOCKS> at;
+    using At = Place<BLOCKS, kSecond<DT>>;
+    constexpr int PASS = At::PASS;
+    At at;
     if (!at.init(p, tid)) return;
     const int64_t wide = HALVES * p.inner;
     struct Row {
@@ -253,22 +292,25 @@ __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
     };
     auto load = [&](int r, Row& raw) __attribute__((always_inline)) {
         const int64_t row = at.r0 + r;
-        if (at.has(r)) {
-            raw.dy = load8_once<DT>((const char*)p.dy + (row * p.ld_dy + at.col) * S);
-#pragma unroll
-            for (int k = 0; k < HALVES; ++k) {
-                raw.codes[k] = __builtin_nontemporal_load((const KGW_GLOBAL i32x2*)(p.saved + row * wide + k * p.inner + at.col));
-                raw.scale[k] = *(const KGW_GLOBAL uint8_t*)(p.saved_scales + (k * at.nb + at.b0 + block) * p.rows + row);
-            }
-        } else {
+        bool in[2];
+        at.has(r, in);
+        if (!in[0]) {
             raw = Row{};
+            return;
+        }
+        raw.dy = load8_once<DT>((const char*)p.dy + (row * p.ld_dy + at.col) * S, in);
+#pragma unroll
+        for (int k = 0; k < HALVES; ++k) {
+            raw.codes[k] = load_codes<DT>(p.saved + row * wide + k * p.inner + at.col, in);
+            raw.scale[k] = *(const KGW_GLOBAL uint8_t*)(p.saved_scales + (k * at.nb + at.b0 + block) * p.rows + row);
         }
     };
     Row now, next;
     if (at.passes > 0) load(at.first, now);
     for (int i = 0; i < at.passes; ++i) {
         const int r = at.first + i * PASS;
-        const bool in = at.has(r);
+        bool in[2];
+        at.has(r, in);
         if (i + 1 < at.passes) load(r + PASS, next);
         float f[HALVES][8], dy[8], y[8], d[HALVES][8];
 #pragma unroll
@@ -294,19 +336,19 @@ __global__ __launch_bounds__(NT) void act_grad_kernel(ActParams p) {
             if (p.dh_scales) {
                 i32x2 codes;
                 const uint32_t e = quantise8(d[k], codes);
-                if (in) store_result<STREAM>(codes, (KGW_GLOBAL i32x2*)((uint8_t*)p.dh + to));
+                store_codes<DT, STREAM>((uint8_t*)p.dh + to, codes, in);
                 if ((lane & 15) == 0) sc[k][block][r] = (uint8_t)e;
-            } else if (in) {
-                store8<DT, STREAM>((char*)p.dh + to * S, d[k]);
+            } else {
+                store8<DT, STREAM>((char*)p.dh + to * S, d[k], in);
             }
         }
         if (p.y_scales) {
             i32x2 codes;
             const uint32_t e = quantise8(y, codes);
-            if (in) store_result<STREAM_Y>(codes, (KGW_GLOBAL i32x2*)((uint8_t*)p.y + row * p.inner + at.col));
+            store_codes<DT, STREAM_Y>((uint8_t*)p.y + row * p.inner + at.col, codes, in);
             if ((lane & 15) == 0) sc[HALVES][block][r] = (uint8_t)e;
-        } else if (p.y && in) {
-            store8<DT, STREAM_Y>((char*)p.y + (row * p.inner + at.col) * S, y);
+        } else if (p.y) {
+            store8<DT, STREAM_Y>((char*)p.y + (row * p.inner + at.col) * S, y, in);
         }
         now = next;
     }
@@ -333,18 +375,16 @@ int blocks_of(int64_t inner) {
 // product that reads them does not find them there anyway.  dh goes where it and y together reach this, y where it
 // does by itself: y then keeps the caches, and its product is the next to run.  bf16 swiglu, the gradient with the
 // activation again: 65536 x 2048 (dh 0.54 GB, y 0.27) 274 us with neither, 264 with both, 231 with dh alone;
-// 131072 x 2048 541 with neither, 524 with both.  Below it: 65536 x 2048 relu2 (0.27 GB) 110 -> 121 us.  fp32 rows are
-// written every other 16 bytes a store and lose (204 -> 213 us), and so does the forward pass (y 0.54 GB: 367 -> 407 us).
+// 131072 x 2048 541 with neither, 524 with both; fp32, 16384 x 4096 253 and 212.  Below it: 65536 x 2048 relu2 (0.27 GB) 110 ->
+// 121 us.  The forward pass loses (y of 0.54 GB: 367 -> 407 us).
 constexpr int64_t kStreamBytes = (int64_t)384 << 20;
-int64_t bytes_of_y(const ActParams& p) { return !p.y ? 0 : p.rows * p.inner * (p.y_scales ? 1 : 2); }
-int64_t bytes_of_dh(const ActParams& p, int halves) { return p.rows * p.inner * halves * (p.dh_scales ? 1 : 2); }
-
 template <int DT, bool GATED, int BLOCKS>
 void launch_blocks(const ActParams& p, bool grad, unsigned grid, hipStream_t stream) {
     const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), 0, stream, p); };
-    const int64_t y = bytes_of_y(p), all = bytes_of_dh(p, GATED ? 2 : 1) + y;
+    const int64_t values = p.rows * p.inner, S = RowElem<DT>::size;
+    const int64_t y = !p.y ? 0 : values * (p.y_scales ? 1 : S), all = y + values * (GATED ? 2 : 1) * (p.dh_scales ? 1 : S);
     if (!grad) go(act_kernel<DT, GATED, BLOCKS>);
-    else if (DT == kOutF32 || all < kStreamBytes) go(act_grad_kernel<DT, GATED, BLOCKS, false, false>);
+    else if (all < kStreamBytes) go(act_grad_kernel<DT, GATED, BLOCKS, false, false>);
     else if (y < kStreamBytes) go(act_grad_kernel<DT, GATED, BLOCKS, true, false>);
     else go(act_grad_kernel<DT, GATED, BLOCKS, true, true>);
 }

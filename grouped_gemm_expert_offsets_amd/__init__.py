@@ -562,7 +562,7 @@ def kgw_wgrad_fp8_rows(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, offse
         raise ValueError(f"A must be (T, hidden) and B (T, n), got {tuple(A.shape)} and {tuple(B.shape)}")
     T, hidden = A.shape
     n = B.shape[1]
-    device = A.device
+    device = _on_gpu(A, "A")
     for s, cols, what in ((sa, hidden, "sa"), (sb, n, "sb")):
         if s is None and what == "sb":
             continue
@@ -581,9 +581,8 @@ def kgw_wgrad_fp8_rows(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, offse
     ws = _empty(ws_bytes, torch.uint8, device, stream) if ws_bytes else None
     if stream is not None:
         _used_on(stream, A, sa, B, sb, offsets, out, *(outs or ()))
-    st = lib.kgw_wgrad_fp8_rows(_ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(offsets), E, hidden, n, T, _ptr(out),
-                                           _ptr(ptrs), code, int(bool(accumulate)), _ptr(ws), ws_bytes,
-                                           _stream_ptr(stream))
+    st = lib.kgw_wgrad_fp8_rows(_ptr(A), _ptr(sa), _ptr(B), _ptr(sb), _ptr(offsets), E, hidden, n, T, _ptr(out), _ptr(ptrs),
+                                code, int(bool(accumulate)), _ptr(ws), ws_bytes, _launch_stream(stream, device))
     _check(st, "kgw_wgrad_fp8_rows")
     return out if outs is None else outs
 

@@ -136,7 +136,9 @@ def test_binding_refuses_cpu_tensors():
     s, ids = torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32)
     h, q = torch.zeros((4, 256)), torch.zeros((4, 256), dtype=torch.uint8)
     for call in (lambda: kgw.kgw_moe_route(s, 2), lambda: kgw.kgw_moe_route_grad(s, ids, torch.zeros((4, 2))),
-                 lambda: kgw.kgw_moe_act_fp8(h), lambda: kgw.kgw_moe_act_fp8_grad(h[:, :128].contiguous(), q, q)):
+                 lambda: kgw.kgw_moe_act_fp8(h), lambda: kgw.kgw_moe_act_fp8_grad(h[:, :128].contiguous(), q, q),
+                 lambda: kgw.kgw_wgrad_fp8_rows(torch.zeros((128, 8), dtype=torch.uint8), torch.zeros((1, 128), dtype=torch.uint8),
+                                                torch.zeros((128, 8), dtype=torch.bfloat16), ids.flatten()[:1])):
         with pytest.raises(ValueError):
             call()
 

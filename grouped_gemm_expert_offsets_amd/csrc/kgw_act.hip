@@ -13,11 +13,11 @@
 // of rows; the scales, one byte for a block, collect in LDS and leave as runs of bytes along the rows, as their layout
 // (blocks, R) has them.  Rows past the last offset belong to no expert: they are neither read nor written.
 //
-// HBM bounds both directions from some megabytes on, a launch (4 us) and its issue below.  Measured, bf16 swiglu, MI355X:
-// 65536 x 2048 forward 166 us with a 16-bit result (6.5 TB/s), gradient 210 us, with the activation again 231 us (5.8);
-// 8192 x 4096 forward 44 us (6.1 TB/s), gradient 45 us; 33024 x 768 forward 38.6 us, gradient 37.1 us; fp32:
-// 16384 x 4096 forward 148 us (6.3 TB/s), gradient 184 us, with the activation again 212 us (5.7).  A copy of such sizes moves
-// 4.7 to 5.4 TB/s and a fill 6.9; the counters show that no byte is written twice.
+// HBM bounds both directions from some megabytes on, a launch (4 us) and its issue below.  Measured, MI355X, every call with
+// results of its own: bf16 swiglu of 65536 x 2048 forward 204 us (5.3 TB/s), gradient 211 us (5.1), with the activation again
+// 265 us (5.1); 8192 x 4096 53, 57 and 71 us; 33024 x 768 43, 45 and 56 us; fp32, 16384 x 4096 181, 192 and 247 us.  A copy of such
+// sizes moves 4.7 to 5.4 TB/s; the counters show that no byte moves twice.  Results that the last call left in the caches
+// are quicker (8192 x 4096 44, 45 and 54 us).
 #include <type_traits>
 
 #include "kgw_layer.h"
@@ -203,7 +203,7 @@ struct Place {
     }
 };
 
-template <int DT, bool GATED, int BLOCKS>
+template <int DT, bool GATED, int BLOCKS, bool STREAM_Y>
 __global__ __launch_bounds__(NT) void act_kernel(ActParams p) {
     constexpr int S = RowElem<DT>::size, HALVES = GATED ? 2 : 1;
     __shared__ __attribute__((aligned(4))) uint8_t sc[HALVES + 1][BLOCKS][MOST_ROWS];
@@ -257,10 +257,10 @@ __global__ __launch_bounds__(NT) void act_kernel(ActParams p) {
         if (p.y_scales) {
             i32x2 codes;
             const uint32_t e = quantise8(y, codes);
-            store_codes<DT, false>((uint8_t*)p.y + row * p.inner + at.col, codes, in);
+            store_codes<DT, STREAM_Y>((uint8_t*)p.y + row * p.inner + at.col, codes, in);
             if ((lane & 15) == 0) sc[HALVES][block][r] = (uint8_t)e;
         } else {
-            store8<DT, false>((char*)p.y + (row * p.inner + at.col) * S, y, in);
+            store8<DT, STREAM_Y>((char*)p.y + (row * p.inner + at.col) * S, y, in);
         }
 #pragma unroll
         for (int k = 0; k < HALVES; ++k) now[k] = next[k];
@@ -371,22 +371,26 @@ int blocks_of(int64_t inner) {
     return 1;
 }
 
-// Gradients of this and more go past the caches' retention: half as much again as the Infinity Cache's 256 MB, so that the
-// product that reads them does not find them there anyway.  dh goes where it and y together reach this, y where it
-// does by itself: y then keeps the caches, and its product is the next to run.  bf16 swiglu, the gradient with the
-// activation again: 65536 x 2048 (dh 0.54 GB, y 0.27) 274 us with neither, 264 with both, 231 with dh alone;
-// 131072 x 2048 541 with neither, 524 with both; fp32, 16384 x 4096 253 and 212.  Below it: 65536 x 2048 relu2 (0.27 GB) 110 ->
-// 121 us.  The forward pass loses (y of 0.54 GB: 367 -> 407 us).
-constexpr int64_t kStreamBytes = (int64_t)384 << 20;
+// Results of this and more go past the caches' retention: the Infinity Cache's 256 MB could not hold them for the product
+// that reads them next.  bf16 swiglu, every call with results of its own (65536 x 2048, y 0.27 GB, dh 0.54): forward 215 us, past the
+// caches 204; gradient 219 and 211, with the activation again 274 and 265; fp32 16384 x 4096 190 and 182, 201 and 192, 259 and
+// 248.  Smaller ones may still be there when they are read, or written anew (32768 x 2048, y of 0.13 GB written every
+// second time: 87 us, past the caches 104).
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
+
 template <int DT, bool GATED, int BLOCKS>
 void launch_blocks(const ActParams& p, bool grad, unsigned grid, hipStream_t stream) {
     const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), 0, stream, p); };
     const int64_t values = p.rows * p.inner, S = RowElem<DT>::size;
-    const int64_t y = !p.y ? 0 : values * (p.y_scales ? 1 : S), all = y + values * (GATED ? 2 : 1) * (p.dh_scales ? 1 : S);
-    if (!grad) go(act_kernel<DT, GATED, BLOCKS>);
-    else if (all < kStreamBytes) go(act_grad_kernel<DT, GATED, BLOCKS, false, false>);
-    else if (y < kStreamBytes) go(act_grad_kernel<DT, GATED, BLOCKS, true, false>);
-    else go(act_grad_kernel<DT, GATED, BLOCKS, true, true>);
+    const bool y = p.y && values * (p.y_scales ? 1 : S) >= kStreamBytes;
+    if (!grad) {
+        if (y) go(act_kernel<DT, GATED, BLOCKS, true>);
+        else go(act_kernel<DT, GATED, BLOCKS, false>);
+    } else {
+        if (y) go(act_grad_kernel<DT, GATED, BLOCKS, true, true>);
+        else if (values * (GATED ? 2 : 1) * (p.dh_scales ? 1 : S) >= kStreamBytes) go(act_grad_kernel<DT, GATED, BLOCKS, true, false>);
+        else go(act_grad_kernel<DT, GATED, BLOCKS, false, false>);
+    }
 }
 template <int DT, bool GATED>
 void launch_gated(const ActParams& p, bool grad, unsigned grid, hipStream_t stream) {

@@ -569,15 +569,23 @@ void with_dtype(int dtype, F f) {
 }  // namespace
 
 // Workgroups of 1024 threads where all of a CU's waves then have tokens, or where one takes all of them in a round (one
-// launch); of 256 between these, so that more CUs have some, and where the ids are given and there is little to do.
+// launch); of 256 between these, so that more CUs have some, and where the ids are given and there is little to do.  Lanes
+// of 32 scores need 207 registers, of which 1024 threads leave them 128: 512 then (65536 x 512 97 -> 60 us, 16384 x 2048 112 -> 97,
+// 64 x 512 in one workgroup 18 -> 15).
+template <int Q>
+constexpr int kWide = Q == 8 ? 512 : 1024;
 RoutePlan route_plan(int64_t tokens, int experts, bool given) {
     RoutePlan plan;
-    int lanes = 64;
-    with_shape(experts, [&](auto l, auto) { lanes = decltype(l)::value; });
+    int lanes = 64, wide = 1024;
+    with_shape(experts, [&](auto l, auto q) {
+        lanes = decltype(l)::value;
+        wide = kWide<decltype(q)::value>;
+    });
     const int64_t threads = tokens * lanes;
-    plan.threads = !given && (threads <= 1024 || threads > 1024 * kRouteGroups) ? 1024 : 256;
-    const int64_t wanted = (threads + plan.threads - 1) / plan.threads;
-    const int64_t most = plan.threads == 1024 ? kRouteGroups : experts <= 512 ? 4 * kRouteGroups : 2 * kRouteGroups;
+    const bool one = !given && threads <= 1024;
+    plan.threads = one || (!given && threads > 1024 * kRouteGroups) ? wide : 256;
+    const int64_t wanted = one ? 1 : (threads + plan.threads - 1) / plan.threads;
+    const int64_t most = plan.threads == wide ? kRouteGroups : experts <= 512 ? 4 * kRouteGroups : 2 * kRouteGroups;
     plan.groups = (int)(wanted < 1 ? 1 : wanted < most ? wanted : most);
     plan.finish = (experts + COLUMNS - 1) / COLUMNS;
     plan.words = plan.groups == 1 ? 0 : (size_t)plan.groups * (2 * experts + 1) + plan.finish + 1;
@@ -591,7 +599,7 @@ hipError_t launch_route(const RouteParams& p, int dtype, hipStream_t stream) {
             constexpr int L = decltype(l)::value, Q = decltype(q)::value, DT = decltype(dt)::value;
             const dim3 grid((unsigned)plan.groups);
             if (p.given) hipLaunchKernelGGL((route_kernel<DT, L, Q, 256, true>), grid, dim3(256), 0, stream, p);
-            else if (plan.threads == 1024) hipLaunchKernelGGL((route_kernel<DT, L, Q, 1024, false>), grid, dim3(1024), 0, stream, p);
+            else if (plan.threads == kWide<Q>) hipLaunchKernelGGL((route_kernel<DT, L, Q, kWide<Q>, false>), grid, dim3(kWide<Q>), 0, stream, p);
             else hipLaunchKernelGGL((route_kernel<DT, L, Q, 256, false>), grid, dim3(256), 0, stream, p);
         });
     });

@@ -651,7 +651,8 @@ typedef enum {
     KGW_SCORE_SIGMOID = 1    /* u = 1 / (1 + exp(-score)), p = u / (sum u + 1e-20)                    */
 } kgw_score_t;
 
-/* Device scratch of kgw_moe_route, 8-byte aligned, no initial contents (0: none); given 1: with given_ids. */
+/* Device scratch of kgw_moe_route, 8-byte aligned, no initial contents (0: none); given 1: with given_ids.  Not to be used
+ * by another call that may run at the same time. */
 size_t kgw_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts, int32_t given);
 
 /*
@@ -659,7 +660,7 @@ size_t kgw_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts, int32_
  *
  *   scores   (tokens, num_experts) of `dtype`, rows `ld` >= num_experts elements apart.  A score of -inf is an expert that
  *            its token may not take: p = 0.
- *   mask     uint8 (tokens,) or NULL: a token with 0 takes no expert (padding); its scores are not read.
+ *   mask     uint8 (tokens,) or NULL: a token with 0 takes no expert (padding), whatever its scores are.
  *   ids      int32 (tokens, topk): the topk largest scores in descending order, equal ones by index (-0 equals
  *            0).  Where fewer may be taken, -1.
  *   given_ids  NULL, or the ids (tokens, topk) of a caller that selects by itself, id_bytes 4 (int32) or 8

@@ -281,6 +281,12 @@ def test_many_tokens(tokens):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("tokens,experts,k", [(17000, 512, 8), (4301, 2048, 8), (17001, 200, 6), (4200, 900, 5)])
+def test_many_tokens_of_wide_rows(tokens, experts, k):
+    """The large workgroups of every row length."""
+    check(make_scores(tokens, experts, torch.float32, 4), k)
+
+
 def test_scores_past_four_gigabytes():
     # 2^19 rows 2112 apart: offsets pass 2^30 elements, 2^32 bytes
     tokens, experts = 1 << 19, 64

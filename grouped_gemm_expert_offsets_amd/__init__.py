@@ -1091,7 +1091,7 @@ def kgw_moe_route(scores: torch.Tensor, topk: int, *, ids: Optional[torch.Tensor
     take, a False in `mask` (tokens,) a token that takes none: id -1, weight 0, no part in the loss.  `ids`
     (int32 or int64, (tokens, topk)) are experts chosen elsewhere.
 
-    ids and counts are views of one buffer, weights, loss and slope of another.
+    The results are views of one buffer.
     """
     topk = int(topk)
     device, code, ld, score_code, tokens, E = _route_args(scores, topk, mask, score)
@@ -1102,20 +1102,22 @@ def kgw_moe_route(scores: torch.Tensor, topk: int, *, ids: Optional[torch.Tensor
     lib = load_library()
     n = tokens * topk
     need = lib.kgw_moe_route_workspace_bytes(tokens, E, ids is not None)
-    whole = _empty(n + E, torch.int32, device, stream)
-    real = _empty(need // 4 + n + E + 1, torch.float32, device, stream)
+    whole = _empty(need // 4 + 2 * (n + E) + 1, torch.int32, device, stream)
+    real = whole.view(torch.float32)                       # (half the time of another allocation)
     if stream is not None:
         _used_on(stream, scores, mask, ids)
-    at, at_real = whole.data_ptr(), real.data_ptr()
+    workspace = whole.data_ptr()
+    at, at_real = workspace + need, workspace + need + 4 * (n + E)
     st = lib.kgw_moe_route(scores.data_ptr(), ld, code, _ptr(mask), _ptr(ids), 0 if ids is None else ids.element_size(),
-                           tokens, E, topk, score_code, int(bool(renormalize)), scale, at, at_real + need, at + 4 * n,
-                           at_real + need + 4 * (n + E), at_real + need + 4 * n, at_real, need,
+                           tokens, E, topk, score_code, int(bool(renormalize)), scale, at, at_real, at + 4 * n,
+                           at_real + 4 * (n + E), at_real + 4 * n, workspace, need,
                            _launch_stream(stream, device))
     _check(st, "kgw_moe_route")
     # (as_strided: a split and a view of each part take twice the time, and a call's issue outlasts a short batch)
     first = need // 4
-    return (whole.as_strided((tokens, topk), (topk, 1)), real.as_strided((tokens, topk), (topk, 1), first),
-            whole.as_strided((E,), (1,), n), real.as_strided((), (), first + n + E), real.as_strided((E,), (1,), first + n))
+    then = first + n + E
+    return (whole.as_strided((tokens, topk), (topk, 1), first), real.as_strided((tokens, topk), (topk, 1), then),
+            whole.as_strided((E,), (1,), first + n), real.as_strided((), (), then + n + E), real.as_strided((E,), (1,), then + n))
 
 
 def kgw_moe_route_grad(scores: torch.Tensor, ids: torch.Tensor, dweights: Optional[torch.Tensor], *,

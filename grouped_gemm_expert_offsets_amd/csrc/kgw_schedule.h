@@ -18,7 +18,10 @@ namespace kgw {
 // run longest first: lane k of every wave holds the expert of rank k (ties by index),
 // so the last items to be claimed are the shortest.  Thread 0 claims the next item
 // while the current one writes its output, and passes it on through LDS word 0 (the
-// rings are idle between items) between two barriers.
+// rings are idle between items) between two barriers.  The barriers order nothing by
+// themselves: the word is waited for before the first (or others could read what was there,
+// part of the last tile, and take it for an item) and each wave's read before the second
+// (or the next item's ring could overwrite it).
 struct Schedule {
     const GroupedParams& p;
     lds_char* const tiles;
@@ -68,8 +71,12 @@ struct Schedule {
     }
     __device__ __forceinline__ int broadcast(int v) {
         if (tid == 0) *(__attribute__((address_space(3))) int*)tiles = v;
+        asm volatile("" ::: "memory");
+        wait_lgkmcnt0();
         barrier_no_fence();
         v = *(__attribute__((address_space(3))) int*)tiles;
+        asm volatile("" ::: "memory");
+        wait_lgkmcnt0();
         barrier_no_fence();
         return __builtin_amdgcn_readfirstlane(v);
     }

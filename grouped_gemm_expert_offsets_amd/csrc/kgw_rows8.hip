@@ -134,6 +134,7 @@ __device__ __forceinline__ i32x4 join(i16x4 lo, i16x4 hi) {
 
 // A wave's (32 FM) x (32 FN) part of a small tile, through `stage` (4 KiB FN of LDS of its own), 32 rows at a time, with
 // the layout of store_wave_tile_staged: acc[j][i][4g + t] is row 32i + (lane & 31), column 32j + 8g + 4 (lane >> 5) + t.
+// All of the wave's LDS accesses are complete at the end, also where nothing is stored.
 template <int OUT, int FM, int FN>
 __device__ __forceinline__ void store_small_tile(const GroupedParams& p, int e, int64_t mb, int64_t nb, int lane,
                                                  const f32x16 (&acc)[FN][FM], lds_char* stage) {
@@ -188,6 +189,8 @@ __device__ __forceinline__ void store_small_tile(const GroupedParams& p, int e, 
             __builtin_nontemporal_store(out, to);
         }
     }
+    asm volatile("" ::: "memory");
+    wait_lgkmcnt0();
 }
 
 template <int F>

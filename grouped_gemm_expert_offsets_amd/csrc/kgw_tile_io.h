@@ -164,8 +164,10 @@ __device__ __forceinline__ void store_rows_from_lds(gbl_char* obase, int64_t m_p
 // non-temporal hints: each output byte is read (accumulate) and written once
 // per call (measured 6% faster on the E=256 fp32 workload, whose 15 GB output
 // write dominates).  The caller
-// must keep other waves' LDS traffic out of `stage` until this returns (its LDS
-// reads are complete once its last store is issued).
+// must keep other waves' LDS traffic out of `stage` until this returns.  Then this wave's
+// LDS accesses are complete: those whose results are stored by the stores' own waits, all
+// others (a wave whose rows or columns lie outside the matrix stores nothing, and need not
+// even read) by the wait at the end.
 template <int OUT, class P>
 __device__ __forceinline__ void store_wave_tile_staged(const P& p, int e, int64_t mb, int64_t nb,
                                                        int lane, const f32x16 (&acc)[4][4], lds_char* stage) {
@@ -205,6 +207,8 @@ __device__ __forceinline__ void store_wave_tile_staged(const P& p, int e, int64_
                 store_rows_from_lds<OUT, false, false>(obase, m_pass, nb, p.hidden, p.n, lane, stage);
         }
     }
+    asm volatile("" ::: "memory");
+    wait_lgkmcnt0();
 }
 
 }  // namespace kgw

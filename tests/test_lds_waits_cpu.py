@@ -133,3 +133,11 @@ def test_the_claimed_item_is_passed_on_through_lds(kernels):
         assert any(op == "ds_write_b32" for op, _ in body), name
         assert not outstanding(body, lambda op: op == "ds_write_b32"), name
         assert not outstanding(body, lambda op: op == "ds_read_b32"), name
+
+
+def test_no_write_is_outstanding_where_waves_meet(kernels):
+    """Not the results staged by a wave that stores none of them (its part of a tile lies outside the matrix) either: the
+    next tile's operands go to the same place."""
+    assert sum("wgrad" in k or "mgrouped" in k for k in kernels) >= 70
+    bad = [k for k, body in kernels.items() if outstanding(body, lambda op: "write" in op or op.startswith("ds_add"))]
+    assert not bad, f"{len(bad)} kernels, first {bad[:3]}"

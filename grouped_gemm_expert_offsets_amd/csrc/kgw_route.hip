@@ -516,6 +516,8 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteParams p) {
             const int i = 4 * q + c;
             d[c] = (push[i] - all) * (u[i] * inverse);
             if constexpr (SIGMOID) d[c] *= x[i];
+            // zero, not zero times something: for a masked token and a score of -inf whatever is infinite or NaN elsewhere
+            d[c] = u[i] != 0.0f ? d[c] : 0.0f;
         }
         *(f32x4*)&grad[row][expert_at<L>(q, 0, sub)] = d;
     }

@@ -221,7 +221,8 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteParams p) {
             if (p.renormalize) per = sigmoid ? reciprocal(chosen + kTiny) : (chosen > 0.0f ? reciprocal(chosen) : 0.0f);
             return per * p.scale;
         };
-        auto share = [&](float x) __attribute__((always_inline)) { return sigmoid ? share_of<true>(x, top) : share_of<false>(x, top); };
+        // (beside `from`: the row's largest score, or that of the chosen)
+        auto share = [&](float x, float from) __attribute__((always_inline)) { return sigmoid ? share_of<true>(x, from) : share_of<false>(x, from); };
         auto leave = [&](int j, int id, float u, float per) __attribute__((always_inline)) {
             p.ids[t * K + j] = id;
             p.weights[t * K + j] = id >= 0 ? u * per : 0.0f;
@@ -265,7 +266,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteParams p) {
                     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the next token's writes come after
                     const int rank = rank_of(key, id, sub < total);
                     const bool taken = sub < total && rank < K;
-                    const float u = taken ? share(score_of(key)) : 0.0f;
+                    const float u = taken ? share(score_of(key), top) : 0.0f;
                     const float per = factor(u);
                     if (there && taken) leave(rank, id, u, per);
                     if (there && sub >= total && sub < K) leave(sub, -1, 0.0f, 0.0f);
@@ -305,12 +306,23 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteParams p) {
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        float from = top;
+        if constexpr (GIVEN) {
+            // The caller's need not have the row's largest score, beside which their shares may all vanish: those that are
+            // made to sum to one go by the largest of their own.
+            if (p.renormalize && !sigmoid) {
+                int most = kNoOrder;
+                for (int j = sub; j < K; j += L) most = max(most, sel[row][1][j]);
+                most = lanes_max<L>(most);
+                from = most == kNoOrder ? 0.0f : score_of(most);
+            }
+        }
         float held = 0.0f;
         for (int j = sub; j < K; j += L)
-            if (sel[row][0][j] >= 0) held += share(score_of(sel[row][1][j]));
+            if (sel[row][0][j] >= 0) held += share(score_of(sel[row][1][j]), from);
         const float per = factor(held);
         if (there)
-            for (int j = sub; j < K; j += L) leave(j, sel[row][0][j], share(score_of(sel[row][1][j])), per);
+            for (int j = sub; j < K; j += L) leave(j, sel[row][0][j], share(score_of(sel[row][1][j]), from), per);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     // the wave's tokens, then the waves in turn
@@ -489,12 +501,23 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteParams p) {
     int id0 = -1;
     float s0 = kNone, dw0 = 0.0f;                          // the lane's first; a lane has more where K > L
     if (sub < K) pick(sub, id0, s0, dw0);
+    float from = top;                                      // as in the forward pass
+    if (!SIGMOID && p.renormalize) {
+        float most = id0 >= 0 ? s0 : kNone;
+        for (int j = sub + L; j < K; j += L) {
+            int id;
+            float s, dw;
+            pick(j, id, s, dw);
+            most = id >= 0 ? fmaxf(most, s) : most;
+        }
+        from = finite_top(lanes_max<L>(most));
+    }
     for (int j = sub; j < K; j += L) {
         int id = id0;
         float s = s0, dw = dw0;
         if (j != sub) pick(j, id, s, dw);
         if (id >= 0) {
-            const float v = share_of<SIGMOID>(s, top);
+            const float v = share_of<SIGMOID>(s, from);
             chosen += v;
             weighed += v * dw;
         }
@@ -527,7 +550,7 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteParams p) {
         float s = s0, dw = dw0;
         if (j != sub) pick(j, id, s, dw);
         if (id >= 0) {
-            float d = share_of<SIGMOID>(s, top) * per * (dw - less);
+            float d = share_of<SIGMOID>(s, from) * per * (dw - less);
             if constexpr (SIGMOID) d *= sigmoid_of(-s);
             atomicAdd(&grad[row][id], d);                    // adds up where a token names an expert twice
         }

@@ -198,7 +198,7 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
                  int32_t scale_format, const int32_t* offsets, int32_t num_experts, int64_t hidden, int64_t n,
                  int64_t tokens_sum, void* out, void* const* out_ptrs, int32_t out_dtype, int32_t accumulate,
                  void* workspace, size_t workspace_bytes, void* stream, int32_t layout = 0) {
-    const bool rows = kernel == Kernel::kFp8Rows;    // 8-bit token rows through the bf16 kernel
+    const bool rows = kernel == Kernel::kFp8Rows;    // 8-bit token rows: a kernel and tiles of their own
     const bool fp8 = kernel != Kernel::kBf16 && !rows;   // operands scaled along the tokens (fp8 or fp4)
     const bool fp4 = kernel == Kernel::kFp4;
     int64_t bm = fp8 ? kgw::kFp8BM : kgw::kBf16BM;
@@ -245,10 +245,14 @@ kgw_status_t run(Kernel kernel, const void* A, const void* sfa, const void* B, c
 
     DeviceProps d;
     st = current_props(&d);
+    const RowsPlan rplan =
+        rows ? rows_plan(num_experts, hidden, n, tokens_sum, st == KGW_SUCCESS ? d.num_cus : kDefaultCus) : RowsPlan();
+    if (rows) {
+        bm = bn = rplan.tile;                       // check_common() has counted tiles of 256
+        if (((hidden + bm - 1) / bm) * ((n + bn - 1) / bn) * num_experts >= INT32_MAX) return KGW_ERROR_UNSUPPORTED;
+    }
     if (st != KGW_SUCCESS) return st;
     if (!d.is_gfx950) return KGW_ERROR_DEVICE;
-    const RowsPlan rplan = rows ? rows_plan(num_experts, hidden, n, tokens_sum, d.num_cus) : RowsPlan();
-    if (rows) bm = bn = rplan.tile;
 
     kgw::GroupedParams p;
     p.A = A;

@@ -1090,6 +1090,8 @@ def kgw_moe_route(scores: torch.Tensor, topk: int, *, ids: Optional[torch.Tensor
     sigmoids), divided by their sum if `renormalize`, times `scale`.  A score of -inf is an expert that its token may not
     take, a False in `mask` (tokens,) a token that takes none: id -1, weight 0, no part in the loss.  `ids`
     (int32 or int64, (tokens, topk)) are experts chosen elsewhere.
+
+    Every result has memory of its own.
     """
     topk = int(topk)
     device, code, ld, score_code, tokens, E = _route_args(scores, topk, mask, score)
@@ -1136,7 +1138,8 @@ def kgw_moe_route_grad(scores: torch.Tensor, ids: torch.Tensor, dweights: Option
 
     dweights float32 (tokens, topk) or None; dloss a float32 tensor of one value, with the slope that kgw_moe_route
     gave (or one made of counts summed over ranks: experts * counts / (topk * tokens^2)); both or neither.
-    mask, score, renormalize and scale as given to kgw_moe_route.
+    mask, score, renormalize and scale as given to kgw_moe_route.  Masked tokens and scores of -inf get zeros, also where
+    dloss or a weight's gradient is not finite.
     """
     if ids.dim() != 2:
         raise ValueError(f"ids must be (tokens, topk), got {tuple(ids.shape)}")

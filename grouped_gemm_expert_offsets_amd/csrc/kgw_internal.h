@@ -40,10 +40,10 @@ struct GroupedParams {
     int32_t ragged;         // bf16 layouts: A and B are per-expert (., n_e) blocks back to back
     int32_t group_m;        // bf16: M tiles per column of the tile order (4 or 8)
     int32_t snake;          // bf16: odd rounds of the persistent stride run the slots in reverse
-    int32_t* sched;         // bf16: kSchedWords zeroed counters -> dynamic schedule (NULL: static)
+    int32_t* sched;         // bf16, 8-bit rows: kSchedWords zeroed counters -> dynamic schedule (NULL: static)
 };
 
-// Dynamic schedule of the bf16 kernel: one claim counter per XCD queue, zeroed by
+// Dynamic schedule of the bf16 and the 8-bit rows' kernel: one claim counter per XCD queue, zeroed by
 // launch_sched_reset on the launch stream right before the kernel.  Experts run longest
 // first (at most kSchedMaxExperts of them, each its own lane of a wave).
 constexpr int kSchedWords = 64;              // 256 bytes of the caller's workspace

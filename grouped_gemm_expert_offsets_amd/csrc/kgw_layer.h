@@ -61,7 +61,7 @@ hipError_t launch_moe_rows(const MoeRowsParams& p, int op, int dtype, hipStream_
 // the router (kgw_route.hip)
 // ----------------------------------------------------------------------------
 constexpr int kRouteMaxTopk = 64;
-constexpr int kRouteGroups = 256;       // workgroups of 1024 (or 512) threads, at most (of 256: four times as many)
+constexpr int kRouteGroups = 256;       // workgroups of 1024 (or 512) threads, at most (of 256: four times as many, past 512 experts twice)
 
 typedef float RoutePart __attribute__((ext_vector_type(2)));     // a workgroup's sum of an expert's shares, and its count
 

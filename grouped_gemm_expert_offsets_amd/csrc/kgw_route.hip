@@ -18,7 +18,9 @@
 // Vector instructions bound the forward kernel where there are many tokens (top-k needs several per score), launches and
 // the call's issue elsewhere.  Measured, MI355X: 32768 x 256 fp32, top 8 of sigmoids, 17.8 us and 5.7 us for the sums
 // of the workgroups' parts (its bytes, 36 MB, take 7 us); 64 x 256 in one workgroup and launch 7.8 us; 5003 x 61 bf16 5.2 and
-// 4.1 us.  Gradient: 32768 x 32 fp32 5.9 us, 16411 x 256 fp16 7.0 us (17.6 MB from the Infinity Cache: 2.5 TB/s).
+// 4.1 us; fp32 softmax, top 8: 32768 x 32 7.6 and 3.9 us, 20000 x 512 26 and 7.4, 65536 x 512 49 and 7.8, 16384 x 2048 79 and 19;
+// given ids: 32768 x 256 11.8 and 6.7 us, 32768 x 32 6.7 and 4.1, 16384 x 2048 34 and 20.
+// Gradient: 32768 x 32 fp32 5.9 us, 16411 x 256 fp16 7.0 us (17.6 MB from the Infinity Cache: 2.5 TB/s).
 #include <type_traits>
 
 #include "kgw_layer.h"
@@ -596,7 +598,9 @@ void with_dtype(int dtype, F f) {
 // Workgroups of 1024 threads where all of a CU's waves then have tokens, or where one takes all of them in a round (one
 // launch); of 256 between these, so that more CUs have some, and where the ids are given and there is little to do.  Lanes
 // of 32 scores need 207 registers, of which 1024 threads leave them 128: 512 then (65536 x 512 97 -> 60 us, 16384 x 2048 112 -> 97,
-// 64 x 512 in one workgroup 18 -> 15).
+// 64 x 512 in one workgroup 18 -> 15).  Workgroups of 256 threads are at most 1024, past 512 experts 512: the second launch
+// reads a part of every expert for each of them (4096 x 2048 45 us, with 1024 of them 49; 4096 x 1024 27 and 28; 3000 x 700 24 and 23;
+// only many tokens with given ids do better with more: 65536 x 1024 95 and 70).
 template <int Q>
 constexpr int kWide = Q == 8 ? 512 : 1024;
 RoutePlan route_plan(int64_t tokens, int experts, bool given) {

@@ -16,11 +16,14 @@
 // (ds_read_b64_tr_b16); 16-byte chunk q of token row k lies at q ^ swizzle(k), so that the four rows of a read lie in
 // different banks.  Loads of steps past an expert's range go to an empty buffer range (zeros, no traffic).
 //
-// The matrix cores bound the large tile: 32 experts of 7168 x 4096, 264320 tokens, B in 8 bits, 11.7 ms (1.32 PFLOP/s, of the
-// 1.37 that a library bf16 product of 8192^3 reaches on this card), cores busy 64% at 1.97 GHz, no LDS bank conflicts; 8 experts
-// of 4096 x 2048, 32768 tokens, B bf16, 446 us (1.23).  Staging through registers and LDS is for the conversion, once for a
+// The matrix cores bound the large tile: 32 experts of 7168 x 4096, 264320 tokens, B in 8 bits, bf16 results, 11.7 ms (1.32
+// PFLOP/s, of the 1.37 that a library bf16 product of 8192^3 reaches on this card), cores busy 64% at 1.97 GHz, no LDS bank
+// conflicts; 8 experts of 4096 x 2048, 32768 tokens, B bf16, 441 us (1.25).  With fp32 results the large tile's loop does not
+// fit its registers (12 spilled for B in 8 bits, 32 for bf16): 8 experts 454 and 478 us, the 32 experts with 262144 tokens 12.3 and
+// 13.1 ms (bf16 results: 12.0 and 12.0).  Staging through registers and LDS is for the conversion, once for a
 // value and tile; direct loads with the conversion from LDS to LDS before took 12.7 ms.  The small tiles are bound by a
-// step's latency and the rounds of compute units: 5 experts of 1040 x 776, 5760 tokens, 24 us (315 tiles of 128).
+// step's length and the rounds of compute units: 5 experts of 1040 x 776, 5760 tokens, 24 us (315 tiles of 128; a wave issues in
+// 45% of its cycles, waits in 32% for data or the others, in 23% for its turn, and has the matrix core for 21%).
 #include <type_traits>
 
 #include "kgw_device.h"
